@@ -1,0 +1,101 @@
+/*
+ * attn.h -- C ABI of the attention kernels for MI355X (gfx950): causal attention over
+ * packed sequences, forward and backward, and attention over a paged key/value cache with
+ * the append that fills it (libattn.so, which loads librope_qk.so beside it).
+ *
+ * The attention is what stands between the rotation of rope_qk.h and the output projection:
+ * packed samples must not see each other ("Packing non contamine" on the Unsloth page cited
+ * in rope_qk.h), so a token attends to the tokens of its own sequence up to itself.
+ *
+ * Semantics. Query head h reads key/value head h / (Hq / Hkv). Of a sequence that holds m
+ * tokens, the n newest of them are queries (packed attention: n = m); query i sits at
+ * position m - n + i and sees the keys of the positions 0 .. m - n + i:
+ *     s_ij = scale * sum_d q_id k_jd,  lse_i = ln sum_j exp(s_ij),
+ *     out_i = sum_j exp(s_ij - lse_i) v_j
+ * A query that sees no key (a negative position) gets out = 0 and lse = -inf. Keys that a
+ * query does not see have no influence on its forward outputs, whatever they hold
+ * (infinities and NaN among it).
+ * Products are formed on the matrix cores from the storage type into fp32; the softmax and
+ * its sums are fp32; the weights are rounded to the storage type before they meet V, and
+ * outputs once at the end. Results do not depend on the order of execution: no atomics.
+ *
+ * Layouts. Rows are [token][head][D], the heads of a token contiguous; every tensor has a
+ * token stride in elements (0 = heads * D), so q, k and v may be views of one fused
+ * projection. D is a multiple of 8, 8 .. 256 (backward: 8 .. 128). Data pointers are
+ * 16-byte aligned and strides multiples of 8 elements, below 2^24. dtype is ROPE_BF16 or
+ * ROPE_F16 (the append takes ROPE_F32 too). lse is float [T][Hq].
+ *
+ * Ownership, threading and errors are those of rope_qk.h: the caller owns every buffer, the
+ * library allocates nothing, keeps no state, never synchronizes, and only enqueues work on
+ * `stream`; arguments are checked on the host before any HIP call (rope_status codes).
+ * Inputs and outputs must not overlap, except where stated.
+ */
+#ifndef ATTN_H
+#define ATTN_H
+
+#include <stdint.h>
+
+#include "rope_qk.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define ATTN_ROW_TILE 128   /* packed query rows (token-major, the heads of a group minor) */
+#define ATTN_KEY_TILE 128   /* keys of a work item of the dK/dV pass */
+#define ATTN_PLAN_HEADER 16 /* int32 words before a plan's items */
+
+/* ---- packed sequences -------------------------------------------------------------- */
+
+/* int32 words of a plan for num_seqs sequences in T rows, or -1 for bad arguments. */
+int64_t attn_plan_ints(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv);
+
+/* Writes the plan of a packed batch: the list of work items, the longest first. One small
+ * launch per batch, which serves every layer, forward and backward.
+ *  cu_seqlens  device int32[num_seqs + 1]; sequence s is the rows cu_seqlens[s] ..
+ *              cu_seqlens[s+1] - 1. Entries are read as clamped to [0, T] and to be
+ *              non-decreasing (a smaller entry counts as the largest before it), so any
+ *              contents are memory-safe.
+ *  seqused     device int32[num_seqs] or NULL: sequence s holds its first seqused[s] rows
+ *              only (padded layouts); the others belong to no sequence
+ *  T           rows, 0 .. 2^31 - 1, with T * Hq / Hkv below 2^31
+ *  Hq, Hkv     head counts, 1 .. 4096, Hq a multiple of Hkv
+ *  plan        device int32[plan_ints], 16-byte aligned, written; plan_ints at least
+ *              attn_plan_ints(T, num_seqs, Hq, Hkv) */
+int32_t attn_plan(const int32_t* cu_seqlens, int32_t num_seqs, const int32_t* seqused, int64_t T,
+                  int32_t Hq, int32_t Hkv, int32_t* plan, int64_t plan_ints, void* stream);
+
+/* Causal attention of packed sequences.
+ *  q, k, v     device [T][Hq][D], [T][Hkv][D], [T][Hkv][D], read
+ *  out, lse    device [T][Hq][D] and float [T][Hq], written
+ *  plan        written by attn_plan for the same T, num_seqs, Hq and Hkv. Where it was made
+ *              for others, memory stays safe and nothing is written.
+ *  scale       positive, and times log2 e within 1e-37 .. 3e38; usually D^-0.5
+ *  fill        rows of no sequence: 0 leaves out and lse as they are, 1 writes out = 0 and
+ *              lse = -inf */
+int32_t attn_fwd(const void* q, const void* k, const void* v, void* out, float* lse, int64_t T,
+                 int32_t Hq, int32_t Hkv, int32_t D, int64_t q_stride, int64_t k_stride,
+                 int64_t v_stride, int64_t out_stride, const int32_t* plan, int32_t num_seqs,
+                 double scale, int32_t dtype, int32_t fill, void* stream);
+
+/* Its gradients, from dout and what attn_fwd read and wrote:
+ *     dP_ij = dout_i . v_j,  D_i = dout_i . out_i,  dS_ij = P_ij (dP_ij - D_i),
+ *     dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
+ * with i over the queries of every head that reads key/value head j's head.
+ *  delta       device float [T][Hq], scratch (D_i)
+ *  dq, dk, dv  device, written; token strides as the others'
+ *  fill        as in attn_fwd: 1 writes zeros to the gradients of rows of no sequence
+ * D is at most 128. Unlike the forward, a non-finite value may reach the gradients of rows
+ * that do not see it, within the 128 rows around it. */
+int32_t attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                 const float* lse, float* delta, void* dq, void* dk, void* dv, int64_t T,
+                 int32_t Hq, int32_t Hkv, int32_t D, int64_t dout_stride, int64_t q_stride,
+                 int64_t k_stride, int64_t v_stride, int64_t out_stride, int64_t dq_stride,
+                 int64_t dk_stride, int64_t dv_stride, const int32_t* plan, int32_t num_seqs,
+                 double scale, int32_t dtype, int32_t fill, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* ATTN_H */

@@ -26,7 +26,7 @@ __all__ = [
     "RopeError", "qk_fwd_", "qk_bwd_", "qk_apply_", "qk_apply_ex_", "qk_apply_table_",
     "qk_apply_padded_", "valid_prefix", "qk_fwd_pos_", "qk_bwd_pos_",
     "positions", "cos_sin", "cos_sin_table", "inv_freq", "abi_version", "LIB_PATH", "INDEX_AUTO", "INDEX_32",
-    "INDEX_64", "glu_fwd", "glu_bwd", "GLU_KINDS",
+    "INDEX_64", "glu_fwd", "glu_bwd", "GLU_KINDS", "AttnPlan", "attn_plan", "attn_fwd",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librope_qk.so")
@@ -428,3 +428,8 @@ def glu_bwd(kind: str, dh, e, g, de=None, dg=None, index_mode: int = INDEX_AUTO)
                       _stream(e.device))
     _check(st, "glu_bwd")
     return de, dg
+
+
+# ---------------------------------------------------------------- attention
+
+from .attention import AttnPlan, attn_fwd, attn_plan  # noqa: E402

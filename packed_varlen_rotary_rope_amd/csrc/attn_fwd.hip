@@ -1,0 +1,188 @@
+// attn_fwd.hip -- causal attention of packed sequences, forward (attn_fwd of include/attn.h).
+//
+// One workgroup per item of the plan's row list and key/value head: 128 packed rows
+// (token-major, the group's heads minor), so that the heads of a group share every key and
+// value read and a tile spans few tokens, which wastes little above the diagonal and in
+// short sequences.
+#include "attn_tile.h"
+
+namespace attn {
+namespace {
+
+struct FwdParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  const int32_t* plan;
+  const int4* items;
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  int32_t T, Hq, Hkv, G, D, num_seqs;
+  float scale;  // times log2 e
+  int32_t fill;
+  Div31 by_hkv, by_g;
+};
+
+template <typename T, int DB>
+__global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const FwdParams p) {
+  using Tile = FwdTile<T, DB>;
+  constexpr int CPR = Tile::CPR, BN = Tile::BN;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Tile::kLdsBytes];
+
+  const uint32_t index = div31(blockIdx.x, p.by_hkv);
+  const uint32_t kvh = blockIdx.x - index * p.Hkv;
+  if (p.plan[2] != p.T || p.plan[3] != p.G || p.plan[4] != p.num_seqs) return;
+  if ((int32_t)index >= p.plan[0]) return;
+  const int4 item = p.items[index];
+  const int32_t start = item.x, n = item.y;
+  if (start < 0 || n <= 0 || start > p.T - n) return;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t chunks = p.D >> 3;
+  T* out = static_cast<T*>(p.out);
+
+  if (item.w != 0) {  // rows of no sequence
+    if (!p.fill) return;
+    const uint32_t per_token = p.G * chunks;
+    for (uint32_t i = tid; i < n * per_token; i += 256) {
+      const uint32_t t = i / per_token, c = i - t * per_token;
+      *reinterpret_cast<u32x4*>(out + (int64_t)(start + t) * p.out_stride +
+                                (int64_t)kvh * p.G * p.D + 8 * c) = (u32x4){0, 0, 0, 0};
+    }
+    for (uint32_t i = tid; i < (uint32_t)n * p.G; i += 256) {
+      const uint32_t t = i / p.G, g = i - t * p.G;
+      p.lse[(int64_t)(start + t) * p.Hq + kvh * p.G + g] = -__builtin_inff();
+    }
+    return;
+  }
+
+  const int32_t rows = n * p.G;
+  const int32_t row0 = item.z;
+  if (row0 < 0 || row0 >= rows) return;
+  const int32_t row_end = min(row0 + kRowTile, rows);
+  const int32_t wave_row0 = row0 + 32 * wave;
+  const int32_t row = wave_row0 + (lane & 31);
+  const bool on = row < row_end;
+  const int32_t clamped = on ? row : row_end - 1;
+  const int32_t token = div31(clamped, p.by_g);
+  const int32_t head = kvh * p.G + (clamped - token * p.G);
+  const int32_t seen = token + 1;
+  // keys that some row, and that every row, of the wave and of the tile sees
+  const int32_t wave_end = wave_row0 < row_end ? (int32_t)div31(min(wave_row0 + 32, row_end) - 1, p.by_g) + 1 : 0;
+  const int32_t wave_all = div31(min(wave_row0, row_end - 1), p.by_g) + 1;
+  const int32_t key_end = div31(row_end - 1, p.by_g) + 1;
+
+  Tile t;
+  t.load_q(static_cast<const T*>(p.q) + (int64_t)(start + token) * p.q_stride + (int64_t)head * p.D,
+           half, chunks);
+  t.clear();
+  clear_unused_chunks<CPR>(lds, 4 * BN, chunks);
+
+  const T* k = static_cast<const T*>(p.k) + (int64_t)start * p.k_stride + (int64_t)kvh * p.D;
+  const T* v = static_cast<const T*>(p.v) + (int64_t)start * p.v_stride + (int64_t)kvh * p.D;
+  const int32_t blocks = (key_end + BN - 1) / BN;
+
+  auto stage = [&](int32_t b) {
+    uint8_t* kt = lds + (b & 1) * 2 * Tile::kTileBytes;
+    uint8_t* vt = kt + Tile::kTileBytes;
+    const int32_t key0 = b * BN;
+    const T* kb = k + (int64_t)key0 * p.k_stride;
+    const T* vb = v + (int64_t)key0 * p.v_stride;
+    const int32_t last = key_end - 1 - key0;
+#pragma unroll
+    for (int i = 0; i < Tile::kLoads; ++i) {
+      const uint32_t c = i * 256 + tid;
+      const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle(r);
+      const uint32_t at = (uint32_t)min((int32_t)r, last);
+      const uint32_t dst = (i * 256 + wave * 64) * 16;
+      if (chunk < chunks) {
+        copy_chunk_to_lds(kb + (at * (uint32_t)p.k_stride + 8 * chunk), kt + dst);
+        copy_chunk_to_lds(vb + (at * (uint32_t)p.v_stride + 8 * chunk), vt + dst);
+      }
+    }
+  };
+
+  stage(0);
+  for (int32_t b = 0; b < blocks; ++b) {
+    wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
+    if (b + 1 < blocks) stage(b + 1);
+    const uint8_t* kt = lds + (b & 1) * 2 * Tile::kTileBytes;
+    const uint8_t* vt = kt + Tile::kTileBytes;
+    const int32_t key0 = b * BN;
+    if (key0 + BN <= wave_all) {
+      t.template block<false>(kt, vt, key0, seen, p.scale, lane);
+    } else if (key0 < wave_end) {
+      t.template block<true>(kt, vt, key0, seen, p.scale, lane);
+    }
+  }
+
+  const float lse = t.finish();
+  t.store(out + (int64_t)(start + token) * p.out_stride + (int64_t)head * p.D, half, chunks, on);
+  if (on && half == 0) p.lse[(int64_t)(start + token) * p.Hq + head] = lse;
+}
+
+template <typename T, int DB>
+int32_t launch(const FwdParams& p, int64_t blocks, hipStream_t s) {
+  hipLaunchKernelGGL((attn_fwd_kernel<T, DB>), dim3((unsigned)blocks), dim3(256), 0, s, p);
+  return launched();
+}
+
+template <typename T>
+int32_t launch_size(const FwdParams& p, int64_t blocks, hipStream_t s) {
+  switch ((p.D + 31) / 32) {
+    case 1: return launch<T, 1>(p, blocks, s);
+    case 2: return launch<T, 2>(p, blocks, s);
+    case 3: return launch<T, 3>(p, blocks, s);
+    case 4: return launch<T, 4>(p, blocks, s);
+    case 5:
+    case 6: return launch<T, 6>(p, blocks, s);
+    default: return launch<T, 8>(p, blocks, s);
+  }
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" int32_t attn_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
+                            int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, int64_t out_stride,
+                            const int32_t* plan, int32_t num_seqs, double scale, int32_t dtype,
+                            int32_t fill, void* stream) {
+  if (!valid_dtype16(dtype)) return ROPE_EUNSUPPORTED;
+  if (attn_plan_ints(T, num_seqs, Hq, Hkv) < 0 || !valid_head_size(D)) return ROPE_EINVAL;
+  if (!valid_scale(scale)) return ROPE_EINVAL;
+  FwdParams p;
+  if (!token_stride(q_stride, Hq, D, &p.q_stride) || !token_stride(k_stride, Hkv, D, &p.k_stride) ||
+      !token_stride(v_stride, Hkv, D, &p.v_stride) ||
+      !token_stride(out_stride, Hq, D, &p.out_stride))
+    return ROPE_EINVAL;
+  if (T == 0) return ROPE_OK;
+  if (!data_pointer(q) || !data_pointer(k) || !data_pointer(v) || !data_pointer(out) ||
+      lse == nullptr || !data_pointer(plan))
+    return ROPE_EINVAL;
+  p.G = Hq / Hkv;
+  const int64_t blocks = row_items(T, num_seqs, p.G) * Hkv;
+  if (blocks > kMaxBlocks) return ROPE_EINVAL;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.out = out;
+  p.lse = lse;
+  p.plan = plan;
+  p.items = reinterpret_cast<const int4*>(plan + kHeader);
+  p.T = (int32_t)T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.num_seqs = num_seqs;
+  p.scale = (float)(scale * kLog2e);
+  p.fill = fill;
+  p.by_hkv = make_div31(Hkv);
+  p.by_g = make_div31(p.G);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return dtype == ROPE_BF16 ? launch_size<__bf16>(p, blocks, s)
+                            : launch_size<_Float16>(p, blocks, s);
+}

@@ -1,0 +1,190 @@
+// attn_tile.h -- forward attention of one tile: 128 packed query rows (32 for each of the
+// four waves of a workgroup) against a range of keys, which the waves share through LDS.
+//
+// Mathematics: the online softmax. Keys are walked in blocks of BN; a query row keeps its
+// running maximum m, the sum l of exp(s - m) and the output O so far, and when m rises, l
+// and O are scaled by exp(m_old - m). All of it is fp32, in base 2 (the scale holds log2 e).
+// m is let stand while the new maximum is within 2^8 of it, which changes nothing but the
+// common factor of O and l, and saves the scaling of O in all but the first few blocks.
+//
+// Both products are computed transposed, S^T = K Q^T and O^T = V^T P^T: a query row is a
+// column of C, held by lanes l and l + 32, so that maximum and sum need one exchange
+// between two lanes, scaling is by one register, and P^T is already the B operand of the
+// second product (attn_common.h), never written to LDS. V^T is read by transposing LDS
+// reads.
+#pragma once
+
+#include "attn_common.h"
+
+namespace attn {
+
+constexpr float kRescale = 8.0f;  // log2 of how far a maximum may rise before O is scaled
+
+template <typename T, int DB>
+struct FwdTile {
+  static constexpr int CPR = chunks_per_row(DB);
+  static constexpr int BN = DB <= 4 ? 64 : 32;  // keys of a block
+  static constexpr int KB = BN / 32;
+  static constexpr int KS = 2 * DB;             // 16-wide steps over the head size
+  static constexpr int kTileBytes = BN * CPR * 16;
+  static constexpr int kLdsBytes = 4 * kTileBytes;  // K and V, two blocks in flight
+  static constexpr int kLoads = BN * CPR / 256;     // chunks of a thread per tile
+
+  x8<T> q[KS];
+  f32x16 o[DB];
+  float m, l;
+
+  __device__ void clear() {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+    m = -__builtin_inff();
+    l = 0.0f;
+  }
+
+  // This lane's query row as B operand; head sizes below 32 DB are filled with zeros.
+  __device__ void load_q(const T* row, uint32_t half, uint32_t chunks) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint32_t c = 2 * s + half;
+      const uint4 w = c < chunks ? *reinterpret_cast<const uint4*>(row + 8 * c) : uint4{0, 0, 0, 0};
+      q[s] = __builtin_bit_cast(x8<T>, w);
+    }
+  }
+
+  // One block of keys key0 .. key0 + BN - 1. `seen`: keys that this lane's row sees (as a
+  // count from key 0). MASKED where some row of the wave does not see the whole block.
+  template <bool MASKED>
+  __device__ void block(const uint8_t* kt, const uint8_t* vt, int32_t key0, int32_t seen, float scale,
+                        uint32_t lane) {
+    const uint32_t r = lane & 31, half = lane >> 5;
+    f32x16 s[KB];
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+#pragma unroll
+      for (int t = 0; t < KS; ++t)
+        s[b] = mfma(read_rows<T, CPR>(kt, 32 * b + r, 2 * t + half), q[t], s[b]);
+    }
+    if constexpr (MASKED) {
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int32_t key = key0 + 32 * b + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
+          if (key >= seen) s[b][i] = -__builtin_inff();
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[b][i]);
+    top = half_max(top) * scale;
+    if (__any(!(top - m <= kRescale))) {
+      const float m_new = __builtin_fmaxf(m, top);
+      const float a = m == m_new ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
+      m = m_new;
+      l *= a;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= a;
+    }
+    const float base = m == -__builtin_inff() ? 0.0f : m;  // a row that saw no key yet
+    float sum = 0.0f;
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], scale, -base));
+        sum += s[b][i];
+      }
+    l += sum;
+    x8<T> p[2 * KB];
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      p[2 * b] = narrow8<T>(s[b], 0);
+      p[2 * b + 1] = narrow8<T>(s[b], 1);
+    }
+    uint32_t bad = 0;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int t = 0; t < 2 * KB; ++t) {
+        x8<T> v = read_columns<T, CPR>(vt, 16 * t, d, lane);
+        if constexpr (MASKED) {
+          bad |= nonfinite<T>(v);
+          v = cleaned<T>(v);
+        }
+        o[d] = mfma(v, p[t], o[d]);
+      }
+    if constexpr (MASKED) {
+      if (__any(bad != 0)) add_nonfinite(vt, key0, seen, lane);
+    }
+  }
+
+  // The non-finite values of a block of V, added to the rows that see them (what is
+  // infinite or NaN stays so whatever its weight).
+  __device__ void add_nonfinite(const uint8_t* vt, int32_t key0, int32_t seen, uint32_t lane) {
+    const uint32_t half = lane >> 5;
+    for (int32_t j = 0; j < BN; ++j) {
+      const bool on = key0 + j < seen;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t e = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
+          const T* at = reinterpret_cast<const T*>(vt + j * (CPR * 16) +
+                                                   (((e >> 3) ^ swizzle(j)) << 4)) + (e & 7);
+          const float v = (float)*at;
+          if (on && !(__builtin_fabsf(v) < __builtin_inff())) o[d][i] += v;
+        }
+    }
+  }
+
+  // Normalizes and writes this lane's part of its row: with lane l + 32's (l - 32's), 16
+  // bytes a store. Returns the row's log-sum-exp.
+  __device__ float finish() {
+    l = half_sum(l);
+    const float r = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] *= r;
+    const float ln2 = 0.693147180559945309f;
+    return l > 0.0f || l != l ? (m + __builtin_log2f(l)) * ln2 : -__builtin_inff();
+  }
+  __device__ void store(T* row, uint32_t half, uint32_t chunks, bool on) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {  // columns 32 d + 16 g .. + 15
+        const uint32_t a0 = narrow2<T>(o[d][8 * g], o[d][8 * g + 1]);
+        const uint32_t a1 = narrow2<T>(o[d][8 * g + 2], o[d][8 * g + 3]);
+        const uint32_t b0 = narrow2<T>(o[d][8 * g + 4], o[d][8 * g + 5]);
+        const uint32_t b1 = narrow2<T>(o[d][8 * g + 6], o[d][8 * g + 7]);
+        const auto x = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+        const auto y = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+        const uint32_t c = 4 * d + 2 * g + half;
+        if (on && c < chunks) *reinterpret_cast<u32x4*>(row + 8 * c) = (u32x4){x[0], y[0], x[1], y[1]};
+      }
+  }
+};
+
+// The chunks of a tile's rows that no load fills (head sizes below CPR chunks) are zeroed
+// once: products of them with q's zeros must not be NaN.
+template <int CPR>
+__device__ inline void clear_unused_chunks(uint8_t* tiles, uint32_t rows, uint32_t chunks) {
+  if (chunks == CPR) return;
+  for (uint32_t i = threadIdx.x; i < rows * CPR; i += blockDim.x) {
+    const uint32_t r = i / CPR, c = i % CPR;
+    if (c >= chunks)
+      *reinterpret_cast<u32x4*>(tiles + r * (CPR * 16) + ((c ^ swizzle(r)) << 4)) =
+          (u32x4){0, 0, 0, 0};
+  }
+}
+
+}  // namespace attn
