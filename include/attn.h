@@ -13,8 +13,8 @@
  *     s_ij = scale * sum_d q_id k_jd,  lse_i = ln sum_j exp(s_ij),
  *     out_i = sum_j exp(s_ij - lse_i) v_j
  * A query that sees no key (a negative position) gets out = 0 and lse = -inf. Keys that a
- * query does not see have no influence on its forward outputs, whatever they hold
- * (infinities and NaN among it).
+ * query does not see have no influence on its outputs, whatever they hold
+ * (infinities and NaN among it), and queries that do not see a key none on its gradients.
  * Products are formed on the matrix cores from the storage type into fp32; the softmax and
  * its sums are fp32; the weights are rounded to the storage type before they meet V, and
  * outputs once at the end. Results do not depend on the order of execution: no atomics.
@@ -82,13 +82,12 @@ int32_t attn_fwd(const void* q, const void* k, const void* v, void* out, float* 
  *     dP_ij = dout_i . v_j,  D_i = dout_i . out_i,  dS_ij = P_ij (dP_ij - D_i),
  *     dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
  * with i over the queries of every head that reads key/value head j's head.
- *  delta       device float [T][Hq], scratch (D_i)
+ *  scratch     device float [2][T][Hq]
  *  dq, dk, dv  device, written; token strides as the others'
  *  fill        as in attn_fwd: 1 writes zeros to the gradients of rows of no sequence
- * D is at most 128. Unlike the forward, a non-finite value may reach the gradients of rows
- * that do not see it, within the 128 rows around it. */
+ * D is at most 128. */
 int32_t attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out,
-                 const float* lse, float* delta, void* dq, void* dk, void* dv, int64_t T,
+                 const float* lse, float* scratch, void* dq, void* dk, void* dv, int64_t T,
                  int32_t Hq, int32_t Hkv, int32_t D, int64_t dout_stride, int64_t q_stride,
                  int64_t k_stride, int64_t v_stride, int64_t out_stride, int64_t dq_stride,
                  int64_t dk_stride, int64_t dv_stride, const int32_t* plan, int32_t num_seqs,

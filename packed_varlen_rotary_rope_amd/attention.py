@@ -35,7 +35,8 @@ def _load() -> ctypes.CDLL:
     lib.attn_plan.argtypes = [vp, i32, vp, i64, i32, i32, vp, i64, vp]
     lib.attn_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, i32, i64, i64, i64, i64, vp, i32, dbl,
                              i32, i32, vp]
-    for name in ("attn_plan", "attn_fwd"):
+    lib.attn_bwd.argtypes = [vp] * 10 + [i64, i32, i32, i32] + [i64] * 8 + [vp, i32, dbl, i32, i32, vp]
+    for name in ("attn_plan", "attn_fwd", "attn_bwd"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -180,3 +181,40 @@ def attn_fwd(q, k, v, plan: AttnPlan, scale=None, out=None, lse=None):
                              float(D ** -0.5 if scale is None else scale), _DTYPE_CODE[q.dtype],
                              int(fill), _stream(q.device)), "attn_fwd")
     return out, lse
+
+
+def attn_bwd(dout, q, k, v, out, lse, plan: AttnPlan, scale=None, dq=None, dk=None, dv=None):
+    """Gradients of attn_fwd for the upstream gradient dout [T, Hq, D], from its inputs and
+    outputs and the same scale; D up to 128. Deterministic (no atomics). New gradients have
+    zeros in rows of no sequence; given dq, dk and dv (all three, e.g. parts of one fused
+    gradient) keep theirs as they are. Returns (dq, dk, dv)."""
+    plan._match(q, k, v)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    _head_size(D, 128)
+    for t, name in ((dout, "dout"), (out, "out")):
+        _like(t, q, (T, Hq, D), name)
+    if lse.dtype != torch.float32 or lse.device != q.device or tuple(lse.shape) != (T, Hq) or \
+            not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 [{T}, {Hq}] tensor on {q.device}")
+    given = [g is not None for g in (dq, dk, dv)]
+    if any(given) != all(given):
+        raise ValueError("give all of dq, dk and dv, or none")
+    fill = not any(given)
+    if fill:
+        dq = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        dk = torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device)
+        dv = torch.empty_like(dk)
+    _like(dq, q, (T, Hq, D), "dq")
+    _like(dk, q, (T, Hkv, D), "dk")
+    _like(dv, q, (T, Hkv, D), "dv")
+    strides = [_heads_last(t, name) for t, name in (
+        (dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"), (dq, "dq"), (dk, "dk"), (dv, "dv"))]
+    scratch = torch.empty((2, T, Hq), dtype=torch.float32, device=q.device)
+    with torch.cuda.device(q.device):
+        _check(_lib.attn_bwd(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(scratch),
+                             _ptr(dq), _ptr(dk), _ptr(dv), T, Hq, Hkv, D, *strides,
+                             _ptr(plan.buffer), plan.num_seqs,
+                             float(D ** -0.5 if scale is None else scale), _DTYPE_CODE[q.dtype],
+                             int(fill), _stream(q.device)), "attn_bwd")
+    return dq, dk, dv

@@ -25,6 +25,11 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+template <bool B>
+struct Constant {
+  static constexpr bool value = B;
+};
+
 template <typename T>
 struct Vec;
 template <>
@@ -106,6 +111,10 @@ typedef const __attribute__((address_space(1))) void gvoid;
 __device__ inline void copy_chunk_to_lds(const void* src, const uint8_t* dst) {
   __builtin_amdgcn_global_load_lds((gvoid*)(uintptr_t)src, (lds_void*)(dst), 16,
                                    0, 0);
+}
+
+__device__ inline void copy_word_to_lds(const void* src, const uint8_t* dst) {  // 4 bytes a lane
+  __builtin_amdgcn_global_load_lds((gvoid*)(uintptr_t)src, (lds_void*)(dst), 4, 0, 0);
 }
 
 // Waits until this wave's copies into LDS have landed, then for the other waves of the

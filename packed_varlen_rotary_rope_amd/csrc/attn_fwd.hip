@@ -74,8 +74,8 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
   const int32_t key_end = div31(row_end - 1, p.by_g) + 1;
 
   Tile t;
-  t.load_q(static_cast<const T*>(p.q) + (int64_t)(start + token) * p.q_stride + (int64_t)head * p.D,
-           half, chunks);
+  load_row<T>(t.q, static_cast<const T*>(p.q) + (int64_t)(start + token) * p.q_stride +
+                       (int64_t)head * p.D, half, chunks);
   t.clear();
   clear_unused_chunks<CPR>(lds, 4 * BN, chunks);
 
@@ -118,7 +118,8 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
   }
 
   const float lse = t.finish();
-  t.store(out + (int64_t)(start + token) * p.out_stride + (int64_t)head * p.D, half, chunks, on);
+  store_row<T, DB>(t.o, out + (int64_t)(start + token) * p.out_stride + (int64_t)head * p.D, half,
+                   chunks, on);
   if (on && half == 0) p.lse[(int64_t)(start + token) * p.Hq + head] = lse;
 }
 

@@ -20,6 +20,54 @@ namespace attn {
 
 constexpr float kRescale = 8.0f;  // log2 of how far a maximum may rise before O is scaled
 
+// One row as B operand, a column of the product: chunks past the head size are zeros.
+template <typename T, int KS>
+__device__ inline void load_row(x8<T> (&f)[KS], const T* row, uint32_t half, uint32_t chunks) {
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    const uint32_t c = 2 * s + half;
+    const u32x4 w =
+        c < chunks ? *reinterpret_cast<const u32x4*>(row + 8 * c) : (u32x4){0, 0, 0, 0};
+    f[s] = __builtin_bit_cast(x8<T>, w);
+  }
+}
+
+// Writes a column of C as a row, 16 bytes a store: lanes l and l + 32 hold quarters of 16
+// elements in turn, and exchange them to hold halves.
+template <typename T, int DB>
+__device__ inline void store_row(const f32x16 (&o)[DB], T* row, uint32_t half, uint32_t chunks,
+                                 bool on) {
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {  // columns 32 d + 16 g .. + 15
+      const uint32_t a0 = narrow2<T>(o[d][8 * g], o[d][8 * g + 1]);
+      const uint32_t a1 = narrow2<T>(o[d][8 * g + 2], o[d][8 * g + 3]);
+      const uint32_t b0 = narrow2<T>(o[d][8 * g + 4], o[d][8 * g + 5]);
+      const uint32_t b1 = narrow2<T>(o[d][8 * g + 6], o[d][8 * g + 7]);
+      const auto x = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+      const auto y = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+      const uint32_t c = 4 * d + 2 * g + half;
+      if (on && c < chunks) *reinterpret_cast<u32x4*>(row + 8 * c) = (u32x4){x[0], y[0], x[1], y[1]};
+    }
+}
+
+// Adds the non-finite values of row j of a tile to this lane's column of C, if it is on.
+template <typename T, int DB, int CPR>
+__device__ inline void add_nonfinite_row(f32x16 (&o)[DB], const uint8_t* tile, uint32_t j, bool on,
+                                         uint32_t half) {
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t e = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
+      const T* at = reinterpret_cast<const T*>(tile + j * (CPR * 16) +
+                                               (((e >> 3) ^ swizzle(j)) << 4)) + (e & 7);
+      const float v = (float)*at;
+      if (on && !(__builtin_fabsf(v) < __builtin_inff())) o[d][i] += v;
+    }
+}
+
 template <typename T, int DB>
 struct FwdTile {
   static constexpr int CPR = chunks_per_row(DB);
@@ -41,16 +89,6 @@ struct FwdTile {
       for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
     m = -__builtin_inff();
     l = 0.0f;
-  }
-
-  // This lane's query row as B operand; head sizes below 32 DB are filled with zeros.
-  __device__ void load_q(const T* row, uint32_t half, uint32_t chunks) {
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const uint32_t c = 2 * s + half;
-      const uint4 w = c < chunks ? *reinterpret_cast<const uint4*>(row + 8 * c) : uint4{0, 0, 0, 0};
-      q[s] = __builtin_bit_cast(x8<T>, w);
-    }
   }
 
   // One block of keys key0 .. key0 + BN - 1. `seen`: keys that this lane's row sees (as a
@@ -122,31 +160,14 @@ struct FwdTile {
         o[d] = mfma(v, p[t], o[d]);
       }
     if constexpr (MASKED) {
-      if (__any(bad != 0)) add_nonfinite(vt, key0, seen, lane);
+      // what is infinite or NaN stays so whatever its weight
+      if (__any(bad != 0))
+        for (int32_t j = 0; j < BN; ++j)
+          add_nonfinite_row<T, DB, CPR>(o, vt, j, key0 + j < seen, half);
     }
   }
 
-  // The non-finite values of a block of V, added to the rows that see them (what is
-  // infinite or NaN stays so whatever its weight).
-  __device__ void add_nonfinite(const uint8_t* vt, int32_t key0, int32_t seen, uint32_t lane) {
-    const uint32_t half = lane >> 5;
-    for (int32_t j = 0; j < BN; ++j) {
-      const bool on = key0 + j < seen;
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t e = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
-          const T* at = reinterpret_cast<const T*>(vt + j * (CPR * 16) +
-                                                   (((e >> 3) ^ swizzle(j)) << 4)) + (e & 7);
-          const float v = (float)*at;
-          if (on && !(__builtin_fabsf(v) < __builtin_inff())) o[d][i] += v;
-        }
-    }
-  }
-
-  // Normalizes and writes this lane's part of its row: with lane l + 32's (l - 32's), 16
-  // bytes a store. Returns the row's log-sum-exp.
+  // Normalizes O and returns the row's log-sum-exp.
   __device__ float finish() {
     l = half_sum(l);
     const float r = l > 0.0f || l != l ? 1.0f / l : 0.0f;
@@ -156,21 +177,6 @@ struct FwdTile {
       for (int i = 0; i < 16; ++i) o[d][i] *= r;
     const float ln2 = 0.693147180559945309f;
     return l > 0.0f || l != l ? (m + __builtin_log2f(l)) * ln2 : -__builtin_inff();
-  }
-  __device__ void store(T* row, uint32_t half, uint32_t chunks, bool on) {
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {  // columns 32 d + 16 g .. + 15
-        const uint32_t a0 = narrow2<T>(o[d][8 * g], o[d][8 * g + 1]);
-        const uint32_t a1 = narrow2<T>(o[d][8 * g + 2], o[d][8 * g + 3]);
-        const uint32_t b0 = narrow2<T>(o[d][8 * g + 4], o[d][8 * g + 5]);
-        const uint32_t b1 = narrow2<T>(o[d][8 * g + 6], o[d][8 * g + 7]);
-        const auto x = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
-        const auto y = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
-        const uint32_t c = 4 * d + 2 * g + half;
-        if (on && c < chunks) *reinterpret_cast<u32x4*>(row + 8 * c) = (u32x4){x[0], y[0], x[1], y[1]};
-      }
   }
 };
 

@@ -96,3 +96,44 @@ def check_lse(got, lse, D, worst):
     tol = 1.01 * (D * 2.0 ** -24 * worst + (4.0 + lse.abs().masked_fill(lse == float("-inf"), 0)) * 2.0 ** -22
                   + 4096 * 2.0 ** -24)
     check(got, lse, tol, "lse")
+
+
+def backward(do, q, k, v, seqs, scale, dtype):
+    """(dq, dk, dv) and their bounds.
+
+    P is formed again from the scores and the rounded lse: relative error rp = e + |lse| 2^-22
+    + 2^-21. dP errs by D 2^-24 sum |do v|, and D_i by sum |do| times what the rounded
+    forward output is off (the forward's bound). dS = P (dP - D_i) is rounded once, and so
+    is P for dV; sums over c terms err by c 2^-24 of the sum of magnitudes; outputs are
+    rounded once."""
+    u = half_step(dtype)
+    G = q.shape[1] // k.shape[1]
+    D = q.shape[2]
+    grads = [torch.zeros(x.shape, dtype=F64, device=q.device) for x in (q, k, v)]
+    tols = [torch.zeros_like(x) for x in grads]
+    for a, n in seqs:
+        if n == 0:
+            continue
+        sl = slice(a, a + n)
+        for h in range(q.shape[1]):
+            g = h // G
+            qh, kh, vh, dh = (x.to(F64) for x in (q[sl, h], k[sl, g], v[sl, g], do[sl, h]))
+            o, lse, p, rel = head_forward(qh, kh, vh, scale, 0)
+            spread = p @ vh.abs()
+            tol_o = 1.01 * (u * (spread + o.abs()) + rel * spread) + tiny(dtype)
+            rp = rel + lse.abs()[:, None] * 2.0 ** -22 + 2.0 ** -21
+            dp, delta = dh @ vh.T, (dh * o).sum(-1, keepdim=True)
+            e_dp = D * 2.0 ** -24 * (dh.abs() @ vh.abs().T)
+            e_delta = (dh.abs() * (tol_o + D * 2.0 ** -24 * o.abs())).sum(-1, keepdim=True)
+            ds = p * (dp - delta)
+            e_ds = (u + rp) * ds.abs() + p * (e_dp + e_delta) * (1 + rp) + tiny(dtype)
+            e_p = (u + rp) * p + tiny(dtype)
+            c = (n * G + 64) * 2.0 ** -24
+            grads[0][sl, h] = scale * (ds @ kh)
+            tols[0][sl, h] = 1.01 * scale * (e_ds @ kh.abs() + c * (ds.abs() @ kh.abs()))
+            grads[1][sl, g] += scale * (ds.T @ qh)
+            tols[1][sl, g] += 1.01 * scale * (e_ds.T @ qh.abs() + c * (ds.abs().T @ qh.abs()))
+            grads[2][sl, g] += p.T @ dh
+            tols[2][sl, g] += 1.01 * (e_p.T @ dh.abs() + c * (p.T @ dh.abs()))
+    tols = [t + 1.01 * u * x.abs() + tiny(dtype) for t, x in zip(tols, grads)]
+    return grads, tols

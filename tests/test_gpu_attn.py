@@ -68,3 +68,18 @@ def test_forward(rope, case):
     want, wlse, tol = ref.forward(q, k, v, ref.sequences(cu, T), scale)
     ref.check(out, want, tol, "out")
     ref.check_lse(lse, wlse, D, worst_score(q, k, scale))
+
+
+@pytest.mark.parametrize("case", [c for c in SHAPES if c[4] <= 128],
+                         ids=lambda c: f"T{c[1]}_{c[2]}_{c[3]}_{c[4]}_{str(c[5])[6:]}")
+def test_backward(rope, case):
+    cu, T, Hq, Hkv, D, dtype = case
+    print(f"[attn_bwd] {case}", flush=True)
+    q, k, v = batch(T, Hq, Hkv, D, dtype, seed=len(cu) + D)
+    do = normal((T, Hq, D), 77, dtype)
+    plan = rope.attn_plan(int32(cu), T, Hq, Hkv)
+    out, lse = rope.attn_fwd(q, k, v, plan)
+    got = rope.attn_bwd(do, q, k, v, out, lse, plan)
+    want, tols = ref.backward(do, q, k, v, ref.sequences(cu, T), D ** -0.5, dtype)
+    for name, g, w, tol in zip(("dq", "dk", "dv"), got, want, tols):
+        ref.check(g, w, tol, name)
