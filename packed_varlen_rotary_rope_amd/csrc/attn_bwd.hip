@@ -132,8 +132,8 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   const T* v = static_cast<const T*>(p.v) + (int64_t)start * p.v_stride + (int64_t)kvh * p.D;
   const int32_t blocks = (key_end + BN - 1) / BN;
   auto stage = [&](int32_t b) {
-    uint8_t* kt = lds + (b & 1) * 2 * kTileBytes;
-    uint8_t* vt = kt + kTileBytes;
+    const uint32_t kd = lds_address(lds) + (b & 1) * 2 * kTileBytes;
+    const uint32_t vd = kd + kTileBytes;
     const int32_t key0 = b * BN;
     const T* kb = k + (int64_t)key0 * p.k_stride;
     const T* vb = v + (int64_t)key0 * p.v_stride;
@@ -145,8 +145,8 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
       const uint32_t at = (uint32_t)min((int32_t)r, last);
       const uint32_t dst = (i * 256 + wave * 64) * 16;
       if (chunk < chunks) {
-        copy_chunk_to_lds(kb + (at * (uint32_t)p.k_stride + 8 * chunk), kt + dst);
-        copy_chunk_to_lds(vb + (at * (uint32_t)p.v_stride + 8 * chunk), vt + dst);
+        copy_chunk_to_lds(kb + (at * (uint32_t)p.k_stride + 8 * chunk), kd + dst);
+        copy_chunk_to_lds(vb + (at * (uint32_t)p.v_stride + 8 * chunk), vd + dst);
       }
     }
   };
@@ -188,6 +188,8 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   };
 
   stage(0);
+  settle<T>(qf);
+  settle<T>(df);
   for (int32_t b = 0; b < blocks; ++b) {
     wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
     if (b + 1 < blocks) stage(b + 1);
@@ -264,8 +266,7 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_keys_kernel(const BwdParams p
   const int32_t blocks = (rows - row_begin + BM - 1) / BM;
 
   auto stage = [&](int32_t b) {
-    uint8_t* qt = lds + (b & 1) * kStage;
-    uint8_t* gt = qt + kTileBytes;
+    const uint32_t qd = lds_address(lds) + (b & 1) * kStage, gd = qd + kTileBytes;
     const int32_t row0 = row_begin + b * BM;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -275,14 +276,14 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_keys_kernel(const BwdParams p
       const uint32_t t = div31(at, p.by_g), h = at - t * p.G;
       const uint32_t dst = (i * 256 + wave * 64) * 16;
       if (chunk < chunks) {
-        copy_chunk_to_lds(q + (int64_t)t * p.q_stride + (h * p.D + 8 * chunk), qt + dst);
-        copy_chunk_to_lds(g + (int64_t)t * p.dout_stride + (h * p.D + 8 * chunk), gt + dst);
+        copy_chunk_to_lds(q + (int64_t)t * p.q_stride + (h * p.D + 8 * chunk), qd + dst);
+        copy_chunk_to_lds(g + (int64_t)t * p.dout_stride + (h * p.D + 8 * chunk), gd + dst);
       }
     }
     if (wave == 0) {  // lse and D of the rows: 32 words each
       const uint32_t at = min(row0 + (int32_t)(lane & 31), rows - 1);
       const uint32_t t = div31(at, p.by_g), h = at - t * p.G;
-      copy_word_to_lds((half ? p.delta : p.lse2) + stat0 + (int64_t)t * p.Hq + h, gt + kTileBytes);
+      copy_word_to_lds((half ? p.delta : p.lse2) + stat0 + (int64_t)t * p.Hq + h, gd + kTileBytes);
     }
   };
 
@@ -341,6 +342,8 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_keys_kernel(const BwdParams p
   };
 
   stage(0);
+  settle<T>(kf);
+  settle<T>(vf);
   for (int32_t b = 0; b < blocks; ++b) {
     wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
     if (b + 1 < blocks) stage(b + 1);

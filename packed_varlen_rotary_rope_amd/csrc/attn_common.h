@@ -106,21 +106,36 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef const __attribute__((address_space(1))) void gvoid;
 
-// One 16-byte chunk per lane from global memory into LDS, no registers between: lane l's
-// chunk lands at dst + 16 l (dst the same for the whole wave); idle lanes write nothing.
-__device__ inline void copy_chunk_to_lds(const void* src, const uint8_t* dst) {
-  __builtin_amdgcn_global_load_lds((gvoid*)(uintptr_t)src, (lds_void*)(dst), 16,
-                                   0, 0);
+// One 16-byte chunk (4-byte word) per lane from global memory into LDS, no registers
+// between: lane l's lands at dst + 16 l (4 l), dst the same for the whole wave; idle lanes
+// write nothing. In assembly because the compiler otherwise waits for every copy in flight
+// before each transposed read of LDS, also of the half that no copy writes. m0 holds the
+// LDS address and needs one wait state. Whoever reads the data waits first (wait_copies).
+__device__ inline uint32_t lds_address(const uint8_t* p) {
+  return (uint32_t)(uintptr_t)(lds_void*)p;
+}
+__device__ inline void copy_chunk_to_lds(const void* src, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :
+               : "v"(src), "s"(dst)
+               : "memory");
+}
+__device__ inline void copy_word_to_lds(const void* src, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+               :
+               : "v"(src), "s"(dst)
+               : "memory");
 }
 
-__device__ inline void copy_word_to_lds(const void* src, const uint8_t* dst) {  // 4 bytes a lane
-  __builtin_amdgcn_global_load_lds((gvoid*)(uintptr_t)src, (lds_void*)(dst), 4, 0, 0);
+// Waits until at most LEFT of this wave's copies (and loads) are in flight, the newest.
+template <int LEFT>
+__device__ inline void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(LEFT) : "memory");
 }
-
 // Waits until this wave's copies into LDS have landed, then for the other waves of the
 // workgroup (and so for theirs).
 __device__ inline void wait_copies_and_sync() {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  wait_copies<0>();
   __syncthreads();
 }
 

@@ -84,8 +84,8 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
   const int32_t blocks = (key_end + BN - 1) / BN;
 
   auto stage = [&](int32_t b) {
-    uint8_t* kt = lds + (b & 1) * 2 * Tile::kTileBytes;
-    uint8_t* vt = kt + Tile::kTileBytes;
+    const uint32_t kd = lds_address(lds) + (b & 1) * 2 * Tile::kTileBytes;
+    const uint32_t vd = kd + Tile::kTileBytes;
     const int32_t key0 = b * BN;
     const T* kb = k + (int64_t)key0 * p.k_stride;
     const T* vb = v + (int64_t)key0 * p.v_stride;
@@ -97,13 +97,14 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
       const uint32_t at = (uint32_t)min((int32_t)r, last);
       const uint32_t dst = (i * 256 + wave * 64) * 16;
       if (chunk < chunks) {
-        copy_chunk_to_lds(kb + (at * (uint32_t)p.k_stride + 8 * chunk), kt + dst);
-        copy_chunk_to_lds(vb + (at * (uint32_t)p.v_stride + 8 * chunk), vt + dst);
+        copy_chunk_to_lds(kb + (at * (uint32_t)p.k_stride + 8 * chunk), kd + dst);
+        copy_chunk_to_lds(vb + (at * (uint32_t)p.v_stride + 8 * chunk), vd + dst);
       }
     }
   };
 
   stage(0);
+  settle<T>(t.q);
   for (int32_t b = 0; b < blocks; ++b) {
     wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
     if (b + 1 < blocks) stage(b + 1);

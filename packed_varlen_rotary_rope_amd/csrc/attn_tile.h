@@ -32,6 +32,18 @@ __device__ inline void load_row(x8<T> (&f)[KS], const T* row, uint32_t half, uin
   }
 }
 
+// Waits for loaded operands before a loop: at their first use inside it the compiler would
+// wait again in every round, for the round's copies into LDS too.
+template <typename T, int KS>
+__device__ inline void settle(x8<T> (&f)[KS]) {
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    u32x4 w = __builtin_bit_cast(u32x4, f[s]);
+    asm volatile("" : "+v"(w));
+    f[s] = __builtin_bit_cast(x8<T>, w);
+  }
+}
+
 // Writes a column of C as a row, 16 bytes a store: lanes l and l + 32 hold quarters of 16
 // elements in turn, and exchange them to hold halves.
 template <typename T, int DB>
