@@ -93,6 +93,63 @@ int32_t attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
                  int64_t dk_stride, int64_t dv_stride, const int32_t* plan, int32_t num_seqs,
                  double scale, int32_t dtype, int32_t fill, void* stream);
 
+/* ---- paged cache ------------------------------------------------------------------- *
+ *
+ * A cache is two tensors [num_pages][page_size][Hkv][D] (keys and values) of one layout:
+ * page_stride, slot_stride and head_stride in elements, the D elements of a row contiguous,
+ * so pages may hold their heads in either order or be parts of a larger allocation. Position
+ * p of sequence s lies in page block_table[s * table_stride + p / page_size], slot p %
+ * page_size. kv_lens[s] counts the tokens that sequence s holds, the new ones included; the
+ * new tokens are rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 of q, k and v, so token i of them
+ * is at position kv_lens[s] - n + i. A page number outside 0 .. num_pages - 1 is no page. */
+
+/* Writes the new tokens' keys and values into the cache, the keys rotated as rope_qk_fwd
+ * rotates them at their position, and the new queries, rotated, to q_out. One launch.
+ *  q, q_out    device [T][Hq][D]; both NULL (or Hq 0): keys and values only. q_out may be q.
+ *              Rows at no position (of no sequence, or at a negative one) are copied as
+ *              they are.
+ *  k, v        device [T][Hkv][D], read; tokens at no position, behind the table's last
+ *              page or on no page are not written to the cache
+ *  D           even, 2 .. 512; dtype any rope_dtype; any strides and alignment (the widest
+ *              access that they allow is used)
+ *  theta, pos_scale  as in rope_qk_apply_ex
+ * Two tokens of one call that share a cache row leave one of them there. */
+int32_t kv_append(const void* q, void* q_out, const void* k, const void* v, void* k_cache,
+                  void* v_cache, int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int64_t q_stride,
+                  int64_t q_out_stride, int64_t k_stride, int64_t v_stride, int32_t num_pages,
+                  int32_t page_size, int64_t page_stride, int64_t slot_stride, int64_t head_stride,
+                  const int32_t* block_table, int32_t max_pages, int64_t table_stride,
+                  const int32_t* cu_seqlens, int32_t num_seqs, const int32_t* kv_lens, double theta,
+                  double pos_scale, int32_t dtype, void* stream);
+
+/* int32 words of a paged plan and floats of attn_paged's workspace, or -1. */
+int64_t paged_plan_ints(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv);
+int64_t paged_workspace_floats(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D);
+
+/* Writes the plan of one step of a batch: which rows attend to which keys, and how the keys
+ * are split over the chip. One small launch, which serves every layer of the step.
+ * cu_seqlens and kv_lens as above, read now: later changes of kv_lens do not reach the
+ * plan. Other arguments as in attn_plan. */
+int32_t paged_plan(const int32_t* cu_seqlens, int32_t num_seqs, const int32_t* kv_lens, int64_t T,
+                   int32_t Hq, int32_t Hkv, int32_t* plan, int64_t plan_ints, void* stream);
+
+/* Attention of the new tokens over the cache, causal among themselves: one token of a
+ * sequence (decode), a chunk of a prompt, or both in one batch.
+ *  q, out, lse as in attn_fwd
+ *  workspace   device float[paged_workspace_floats(...)], 16-byte aligned, scratch: calls
+ *              that may run at the same time need one each
+ *  plan        written by paged_plan for the same T, num_seqs, Hq and Hkv
+ *  max_pages   entries of a sequence's row of block_table; keys behind them, and keys on no
+ *              page, are seen by no query
+ *  fill        as in attn_fwd
+ * The cache is 16-byte aligned with strides that are multiples of 8 elements. */
+int32_t attn_paged(const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
+                   float* workspace, int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int64_t q_stride,
+                   int64_t out_stride, int32_t num_pages, int32_t page_size, int64_t page_stride,
+                   int64_t slot_stride, int64_t head_stride, const int32_t* block_table,
+                   int32_t max_pages, int64_t table_stride, const int32_t* plan, int32_t num_seqs,
+                   double scale, int32_t dtype, int32_t fill, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

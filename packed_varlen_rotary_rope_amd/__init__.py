@@ -27,7 +27,7 @@ __all__ = [
     "qk_apply_padded_", "valid_prefix", "qk_fwd_pos_", "qk_bwd_pos_",
     "positions", "cos_sin", "cos_sin_table", "inv_freq", "abi_version", "LIB_PATH", "INDEX_AUTO", "INDEX_32",
     "INDEX_64", "glu_fwd", "glu_bwd", "GLU_KINDS", "AttnPlan", "attn_plan", "attn_fwd",
-    "attn_bwd",
+    "attn_bwd", "PagedPlan", "paged_plan", "attn_paged", "kv_append_",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librope_qk.so")
@@ -433,4 +433,6 @@ def glu_bwd(kind: str, dh, e, g, de=None, dg=None, index_mode: int = INDEX_AUTO)
 
 # ---------------------------------------------------------------- attention
 
-from .attention import AttnPlan, attn_bwd, attn_fwd, attn_plan  # noqa: E402
+from .attention import (  # noqa: E402
+    AttnPlan, PagedPlan, attn_bwd, attn_fwd, attn_paged, attn_plan, kv_append_, paged_plan,
+)

@@ -1,8 +1,9 @@
 """Attention around the rotary embedding: causal attention over packed sequences (forward
-and backward).
+and backward), the append of new keys and values to a paged cache (rotated on the way), and
+attention over that cache.
 
 Thin binding over the C ABI of ``include/attn.h`` (libattn.so, built by build_attn.py from
-``csrc/attn_*.hip``), as the package's other entry points are: it checks
+``csrc/attn_*.hip`` and ``csrc/kv_append.hip``), as the package's other entry points are: it checks
 tensor metadata and marshals pointers, sizes and the current HIP stream. There is no
 fallback: if the library is missing, importing this module raises. The public names are
 exported by the package itself; differentiable wrappers live in ``functional``.
@@ -20,7 +21,6 @@ import torch
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn.so")
 
 _DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_KEY_TILE = 128
 
 
 def _load() -> ctypes.CDLL:
@@ -36,7 +36,16 @@ def _load() -> ctypes.CDLL:
     lib.attn_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, i32, i64, i64, i64, i64, vp, i32, dbl,
                              i32, i32, vp]
     lib.attn_bwd.argtypes = [vp] * 10 + [i64, i32, i32, i32] + [i64] * 8 + [vp, i32, dbl, i32, i32, vp]
-    for name in ("attn_plan", "attn_fwd", "attn_bwd"):
+    lib.kv_append.argtypes = ([vp] * 6 + [i64, i32, i32, i32] + [i64] * 4 + [i32, i32] + [i64] * 3 +
+                              [vp, i32, i64, vp, i32, vp, dbl, dbl, i32, vp])
+    lib.paged_plan_ints.argtypes = [i64, i32, i32, i32]
+    lib.paged_plan_ints.restype = i64
+    lib.paged_workspace_floats.argtypes = [i64, i32, i32, i32, i32]
+    lib.paged_workspace_floats.restype = i64
+    lib.paged_plan.argtypes = [vp, i32, vp, i64, i32, i32, vp, i64, vp]
+    lib.attn_paged.argtypes = ([vp] * 6 + [i64, i32, i32, i32, i64, i64, i32, i32] + [i64] * 3 +
+                               [vp, i32, i64, vp, i32, dbl, i32, i32, vp])
+    for name in ("attn_plan", "attn_fwd", "attn_bwd", "kv_append", "paged_plan", "attn_paged"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -72,7 +81,7 @@ def _gpu(device: torch.device) -> None:
         raise TypeError("expected tensors on a GPU")
 
 
-def _heads_last(t, name: str, dtypes=(torch.bfloat16, torch.float16)) -> int:
+def _token_rows(t, name: str, dtypes) -> int:
     """Token stride of a [T, H, D] tensor whose tokens hold their heads contiguously."""
     _gpu(t.device)
     if t.dtype not in dtypes:
@@ -82,13 +91,24 @@ def _heads_last(t, name: str, dtypes=(torch.bfloat16, torch.float16)) -> int:
     T, H, D = t.shape
     if t.numel() == 0:
         return H * D
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous "
                          "(stride(2) == 1 and stride(1) == D)")
-    stride = t.stride(0) if T > 1 else H * D
-    if t.data_ptr() % 16 or stride * t.element_size() % 16:
+    return t.stride(0) if T > 1 else H * D
+
+
+def _heads_last(t, name: str) -> int:
+    """_token_rows of a 16-bit tensor whose rows are aligned for 16-byte accesses."""
+    stride = _token_rows(t, name, (torch.bfloat16, torch.float16))
+    if t.data_ptr() % 16 or stride % 8:
         raise ValueError(f"{name}: data pointer and token stride must be multiples of 16 bytes")
     return stride
+
+
+def _statistic(lse, q, T, Hq) -> None:
+    if lse.dtype != torch.float32 or lse.device != q.device or tuple(lse.shape) != (T, Hq) or \
+            not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 [{T}, {Hq}] tensor on {q.device}")
 
 
 def _head_size(D: int, most: int) -> None:
@@ -171,9 +191,7 @@ def attn_fwd(q, k, v, plan: AttnPlan, scale=None, out=None, lse=None):
         out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     _like(out, q, (T, Hq, D), "out")
-    if lse.dtype != torch.float32 or lse.device != q.device or tuple(lse.shape) != (T, Hq) or \
-            not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous float32 [{T}, {Hq}] tensor on {q.device}")
+    _statistic(lse, q, T, Hq)
     out_stride = _heads_last(out, "out")
     with torch.cuda.device(q.device):
         _check(_lib.attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), T, Hq, k.shape[1], D,
@@ -194,9 +212,7 @@ def attn_bwd(dout, q, k, v, out, lse, plan: AttnPlan, scale=None, dq=None, dk=No
     _head_size(D, 128)
     for t, name in ((dout, "dout"), (out, "out")):
         _like(t, q, (T, Hq, D), name)
-    if lse.dtype != torch.float32 or lse.device != q.device or tuple(lse.shape) != (T, Hq) or \
-            not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous float32 [{T}, {Hq}] tensor on {q.device}")
+    _statistic(lse, q, T, Hq)
     given = [g is not None for g in (dq, dk, dv)]
     if any(given) != all(given):
         raise ValueError("give all of dq, dk and dv, or none")
@@ -218,3 +234,160 @@ def attn_bwd(dout, q, k, v, out, lse, plan: AttnPlan, scale=None, dq=None, dk=No
                              float(D ** -0.5 if scale is None else scale), _DTYPE_CODE[q.dtype],
                              int(fill), _stream(q.device)), "attn_bwd")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- paged cache
+
+def _caches(k_cache, v_cache, ref):
+    """Checked caches [num_pages, page_size, Hkv, D] of one layout; their strides."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype != ref.dtype or t.device != ref.device:
+            raise TypeError(f"{name}: dtype or device differs from the new tokens'")
+        if t.dim() != 4:
+            raise ValueError(f"{name}: expected [num_pages, page_size, Hkv, D]")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have one shape and layout")
+    if k_cache.shape[0] < 1 or k_cache.shape[1] < 1:
+        raise ValueError("the cache needs at least one page of at least one slot")
+    if k_cache.shape[3] > 1 and k_cache.stride(3) != 1:
+        raise ValueError("the D elements of a cache row must be contiguous")
+    return k_cache.stride()[:3]
+
+
+def _table(block_table, num_seqs, device):
+    if block_table.dtype != torch.int32 or block_table.device != device or block_table.dim() != 2:
+        raise TypeError(f"block_table must be an int32 [B, max_pages] tensor on {device}")
+    B, per = block_table.shape
+    if B != num_seqs:
+        raise ValueError("block_table must have one row per sequence")
+    if per > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table: a sequence's pages must be contiguous")
+    return per, block_table.stride(0) if B > 1 else per
+
+
+def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: float, q=None,
+               q_out=None, pos_scale: float = 1.0):
+    """Append the new tokens' keys (rotated) and values to a paged cache, in place, and rotate
+    their queries, in one launch. k, v [T, Hkv, D] and q [T, Hq, D] (bf16, f16 or f32; views
+    whose tokens hold their heads contiguously) are the new tokens of B sequences, rows
+    cu_seqlens[s] .. cu_seqlens[s+1] - 1 (int32[B+1]) of sequence s, which holds kv_lens[s]
+    tokens with them (int32[B]): token i of n goes to position kv_lens[s] - n + i, in page
+    block_table[s, position // page_size] (int32 [B, max_pages]) of the caches [num_pages,
+    page_size, Hkv, D]. Keys and queries are rotated as qk_apply_ex_ does at that position.
+    Tokens at a negative position, of no sequence, behind the table or on a page number that
+    is no page are not appended. Returns the rotated q, in q_out (a new tensor if None; may be
+    q itself), or None without q."""
+    dtypes = (torch.float32, torch.bfloat16, torch.float16)
+    if k.dim() != 3 or k.shape != v.shape:
+        raise ValueError("expected k and v [T, Hkv, D]")
+    if v.dtype != k.dtype or v.device != k.device:
+        raise TypeError("k and v must share one dtype and device")
+    dev = k.device
+    strides = [_token_rows(t, name, dtypes) for t, name in ((k, "k"), (v, "v"))]
+    T, Hkv, D = k.shape
+    Hq, q_stride, out_stride = 0, 0, 0
+    if q is not None:
+        if q.dtype != k.dtype or q.device != dev:
+            raise TypeError("q: dtype or device differs from k")
+        if q.dim() != 3 or (q.shape[0], q.shape[2]) != (T, D):
+            raise ValueError("expected q [T, Hq, D] with k's T and D")
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        q_stride = _token_rows(q, "q", dtypes)
+        out_stride = _token_rows(_like(q_out, q, q.shape, "q_out"), "q_out", dtypes)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    cache_strides = _caches(k_cache, v_cache, k)
+    if tuple(k_cache.shape[2:]) != (Hkv, D):
+        raise ValueError("the cache must have k's heads and head size")
+    cu = _index(cu_seqlens, "cu_seqlens", dev)
+    num_seqs = cu.numel() - 1
+    if num_seqs < 0:
+        raise ValueError("cu_seqlens needs at least one entry")
+    lens = _index(kv_lens, "kv_lens", dev, num_seqs)
+    per, table_stride = _table(block_table, num_seqs, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.kv_append(_ptr(q), _ptr(q_out), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), T,
+                              Hq, Hkv, D, q_stride, out_stride, *strides, k_cache.shape[0],
+                              k_cache.shape[1], *cache_strides, _ptr(block_table), per,
+                              table_stride, _ptr(cu), num_seqs, _ptr(lens), float(theta),
+                              float(pos_scale), _DTYPE_CODE[k.dtype], _stream(dev)), "kv_append")
+    return q_out
+
+
+class PagedPlan:
+    """How one step of a batch attends to its paged cache (see paged_plan)."""
+
+    def __init__(self, T, num_seqs, num_q_heads, num_kv_heads, buffer):
+        self.T, self.num_seqs = T, num_seqs
+        self.num_q_heads, self.num_kv_heads = num_q_heads, num_kv_heads
+        self.buffer = buffer  # int32, on the GPU
+
+
+def paged_plan(cu_seqlens, kv_lens, T: int, num_q_heads: int, num_kv_heads: int, out=None) -> PagedPlan:
+    """The plan of one step over a paged cache: T new tokens, rows cu_seqlens[s] ..
+    cu_seqlens[s+1] - 1 of sequence s (int32[B+1] on the GPU), which holds kv_lens[s] tokens
+    with them (int32[B], read now). One small launch, no host synchronization; it serves every
+    layer of the step. `out`: a plan of the same sizes to be written over (for the next step,
+    or in a captured graph)."""
+    dev = cu_seqlens.device
+    _gpu(dev)
+    cu = _index(cu_seqlens, "cu_seqlens", dev)
+    num_seqs = cu.numel() - 1
+    if num_seqs < 0:
+        raise ValueError("cu_seqlens needs at least one entry")
+    lens = _index(kv_lens, "kv_lens", dev, num_seqs)
+    T, Hq, Hkv = int(T), int(num_q_heads), int(num_kv_heads)
+    words = _lib.paged_plan_ints(T, num_seqs, Hq, Hkv)
+    if words < 0:
+        raise ValueError(f"no plan for T = {T}, {num_seqs} sequences, {Hq} query and {Hkv} "
+                         "key/value heads (the query heads must be a multiple)")
+    if out is None:
+        out = PagedPlan(T, num_seqs, Hq, Hkv, torch.empty(words, dtype=torch.int32, device=dev))
+    elif (out.T, out.num_seqs, out.num_q_heads, out.num_kv_heads, out.buffer.device) != \
+            (T, num_seqs, Hq, Hkv, dev):
+        raise ValueError("out: a plan of other sizes or of another device")
+    with torch.cuda.device(dev):
+        _check(_lib.paged_plan(_ptr(cu), num_seqs, _ptr(lens), T, Hq, Hkv, _ptr(out.buffer), words,
+                               _stream(dev)), "paged_plan")
+    return out
+
+
+def attn_paged(q, k_cache, v_cache, block_table, plan: PagedPlan, scale=None, out=None, lse=None):
+    """Attention of the new tokens q [T, Hq, D] (bf16 or f16, D a multiple of 8 up to 256) over
+    the paged caches [num_pages, page_size, Hkv, D] that hold their sequences (kv_append_),
+    causal among themselves; block_table as there, plan from paged_plan. Keys behind the table
+    or on a page number that is no page are seen by no query. Returns (out [T, Hq, D], lse
+    float32 [T, Hq]); a query that sees no key, and rows of no sequence, get 0 (-inf in lse) in
+    new outputs; a given `out` and `lse` keep rows of no sequence as they are."""
+    q_stride = _heads_last(q, "q")
+    T, Hq, D = q.shape
+    _head_size(D, 256)
+    if T != plan.T or Hq != plan.num_q_heads or q.device != plan.buffer.device:
+        raise ValueError("the plan was made for other new tokens, query heads or another device")
+    cache_strides = _caches(k_cache, v_cache, q)
+    num_pages, page_size, Hkv, cache_d = k_cache.shape
+    if Hkv != plan.num_kv_heads or cache_d != D:
+        raise ValueError("the cache must have the plan's key/value heads and q's head size")
+    if any(st % 8 for st in cache_strides) or k_cache.data_ptr() % 16 or v_cache.data_ptr() % 16:
+        raise ValueError("the cache's data pointers and strides must be multiples of 16 bytes")
+    per, table_stride = _table(block_table, plan.num_seqs, q.device)
+    if (out is None) != (lse is None):
+        raise ValueError("give both out and lse, or neither")
+    fill = out is None
+    if fill:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    out_stride = _heads_last(_like(out, q, (T, Hq, D), "out"), "out")
+    _statistic(lse, q, T, Hq)
+    space = torch.empty(_lib.paged_workspace_floats(T, plan.num_seqs, Hq, Hkv, D),
+                        dtype=torch.float32, device=q.device)
+    with torch.cuda.device(q.device):
+        _check(_lib.attn_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(space),
+                               T, Hq, Hkv, D, q_stride, out_stride, num_pages, page_size,
+                               *cache_strides, _ptr(block_table), per, table_stride,
+                               _ptr(plan.buffer), plan.num_seqs,
+                               float(D ** -0.5 if scale is None else scale), _DTYPE_CODE[q.dtype],
+                               int(fill), _stream(q.device)), "attn_paged")
+    return out, lse

@@ -14,7 +14,7 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", name) for name in
-        ("attn_plan.hip", "attn_fwd.hip", "attn_bwd.hip")]
+        ("attn_plan.hip", "attn_fwd.hip", "attn_bwd.hip", "attn_paged.hip", "kv_append.hip")]
 LIB_PATH = os.path.join(PKG, "libattn.so")
 ARCH = "gfx950"
 

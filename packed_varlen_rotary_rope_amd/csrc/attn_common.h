@@ -99,6 +99,7 @@ __device__ inline float half_sum(float x) {
 // 4 different pairs of slots.
 __device__ inline uint32_t swizzle(uint32_t r) { return (r & 3) << 1 | (r >> 2 & 1); }
 
+constexpr int keys_per_block(int db) { return db <= 4 ? 64 : 32; }
 constexpr int chunks_per_row(int db) { return db <= 2 ? 8 : db <= 4 ? 16 : 32; }
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
@@ -117,13 +118,13 @@ __device__ inline uint32_t lds_address(const uint8_t* p) {
 __device__ inline void copy_chunk_to_lds(const void* src, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :
-               : "v"(src), "s"(dst)
+               : "v"(src), "s"(__builtin_amdgcn_readfirstlane(dst))
                : "memory");
 }
 __device__ inline void copy_word_to_lds(const void* src, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
                :
-               : "v"(src), "s"(dst)
+               : "v"(src), "s"(__builtin_amdgcn_readfirstlane(dst))
                : "memory");
 }
 

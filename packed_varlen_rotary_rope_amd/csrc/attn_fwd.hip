@@ -26,9 +26,10 @@ struct FwdParams {
 
 template <typename T, int DB>
 __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const FwdParams p) {
-  using Tile = FwdTile<T, DB>;
-  constexpr int CPR = Tile::CPR, BN = Tile::BN;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[Tile::kLdsBytes];
+  constexpr int BN = keys_per_block(DB);
+  using Tile = FwdTile<T, DB, BN>;
+  constexpr int CPR = Tile::CPR, kLoads = BN * CPR / 256;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * Tile::kTileBytes];  // two blocks in flight
 
   const uint32_t index = div31(blockIdx.x, p.by_hkv);
   const uint32_t kvh = blockIdx.x - index * p.Hkv;
@@ -91,7 +92,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
     const T* vb = v + (int64_t)key0 * p.v_stride;
     const int32_t last = key_end - 1 - key0;
 #pragma unroll
-    for (int i = 0; i < Tile::kLoads; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       const uint32_t c = i * 256 + tid;
       const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle(r);
       const uint32_t at = (uint32_t)min((int32_t)r, last);
@@ -112,9 +113,9 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
     const uint8_t* vt = kt + Tile::kTileBytes;
     const int32_t key0 = b * BN;
     if (key0 + BN <= wave_all) {
-      t.template block<false>(kt, vt, key0, seen, p.scale, lane);
+      t.template block<false>(kt, vt, key0, seen, 0, p.scale, lane);
     } else if (key0 < wave_end) {
-      t.template block<true>(kt, vt, key0, seen, p.scale, lane);
+      t.template block<true>(kt, vt, key0, seen, 0, p.scale, lane);
     }
   }
 

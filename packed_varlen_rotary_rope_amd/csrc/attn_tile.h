@@ -18,6 +18,10 @@
 
 namespace attn {
 
+__device__ inline float log_sum_exp(float m, float l) {  // from base 2
+  return l > 0.0f || l != l ? (m + __builtin_log2f(l)) * 0.693147180559945309f : -__builtin_inff();
+}
+
 constexpr float kRescale = 8.0f;  // log2 of how far a maximum may rise before O is scaled
 
 // One row as B operand, a column of the product: chunks past the head size are zeros.
@@ -80,15 +84,13 @@ __device__ inline void add_nonfinite_row(f32x16 (&o)[DB], const uint8_t* tile, u
     }
 }
 
-template <typename T, int DB>
+// The running state of 32 query rows of a wave, against blocks of BN keys.
+template <typename T, int DB, int BN>
 struct FwdTile {
   static constexpr int CPR = chunks_per_row(DB);
-  static constexpr int BN = DB <= 4 ? 64 : 32;  // keys of a block
   static constexpr int KB = BN / 32;
-  static constexpr int KS = 2 * DB;             // 16-wide steps over the head size
+  static constexpr int KS = 2 * DB;  // 16-wide steps over the head size
   static constexpr int kTileBytes = BN * CPR * 16;
-  static constexpr int kLdsBytes = 4 * kTileBytes;  // K and V, two blocks in flight
-  static constexpr int kLoads = BN * CPR / 256;     // chunks of a thread per tile
 
   x8<T> q[KS];
   f32x16 o[DB];
@@ -103,13 +105,9 @@ struct FwdTile {
     l = 0.0f;
   }
 
-  // One block of keys key0 .. key0 + BN - 1. `seen`: keys that this lane's row sees (as a
-  // count from key 0). MASKED where some row of the wave does not see the whole block.
-  template <bool MASKED>
-  __device__ void block(const uint8_t* kt, const uint8_t* vt, int32_t key0, int32_t seen, float scale,
-                        uint32_t lane) {
+  // S^T of a block of keys.
+  __device__ void scores(f32x16 (&s)[KB], const uint8_t* kt, uint32_t lane) {
     const uint32_t r = lane & 31, half = lane >> 5;
-    f32x16 s[KB];
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
 #pragma unroll
@@ -118,13 +116,21 @@ struct FwdTile {
       for (int t = 0; t < KS; ++t)
         s[b] = mfma(read_rows<T, CPR>(kt, 32 * b + r, 2 * t + half), q[t], s[b]);
     }
+  }
+
+  // Scores to weights, narrowed; m, l and o follow. Keys key0 + j at or behind `seen` (as a
+  // count from key 0) are hidden where MASKED, and those whose bit of `hidden` is set.
+  template <bool MASKED>
+  __device__ void weights(f32x16 (&s)[KB], x8<T> (&p)[2 * KB], int32_t key0, int32_t seen,
+                          uint64_t hidden, float scale, uint32_t lane) {
+    const uint32_t half = lane >> 5;
     if constexpr (MASKED) {
 #pragma unroll
       for (int b = 0; b < KB; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int32_t key = key0 + 32 * b + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
-          if (key >= seen) s[b][i] = -__builtin_inff();
+          const int32_t j = 32 * b + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
+          if (key0 + j >= seen || (hidden >> j & 1)) s[b][i] = -__builtin_inff();
         }
     }
     float top = s[0][0];
@@ -153,12 +159,17 @@ struct FwdTile {
         sum += s[b][i];
       }
     l += sum;
-    x8<T> p[2 * KB];
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
       p[2 * b] = narrow8<T>(s[b], 0);
       p[2 * b + 1] = narrow8<T>(s[b], 1);
     }
+  }
+
+  // O^T += V^T P^T.
+  template <bool MASKED>
+  __device__ void accumulate(const x8<T> (&p)[2 * KB], const uint8_t* vt, int32_t key0, int32_t seen,
+                             uint64_t hidden, uint32_t lane) {
     uint32_t bad = 0;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -175,8 +186,18 @@ struct FwdTile {
       // what is infinite or NaN stays so whatever its weight
       if (__any(bad != 0))
         for (int32_t j = 0; j < BN; ++j)
-          add_nonfinite_row<T, DB, CPR>(o, vt, j, key0 + j < seen, half);
+          add_nonfinite_row<T, DB, CPR>(o, vt, j, key0 + j < seen && !(hidden >> j & 1), lane >> 5);
     }
+  }
+
+  template <bool MASKED>
+  __device__ void block(const uint8_t* kt, const uint8_t* vt, int32_t key0, int32_t seen,
+                        uint64_t hidden, float scale, uint32_t lane) {
+    f32x16 s[KB];
+    x8<T> p[2 * KB];
+    scores(s, kt, lane);
+    weights<MASKED>(s, p, key0, seen, hidden, scale, lane);
+    accumulate<MASKED>(p, vt, key0, seen, hidden, lane);
   }
 
   // Normalizes O and returns the row's log-sum-exp.
@@ -187,8 +208,7 @@ struct FwdTile {
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[d][i] *= r;
-    const float ln2 = 0.693147180559945309f;
-    return l > 0.0f || l != l ? (m + __builtin_log2f(l)) * ln2 : -__builtin_inff();
+    return log_sum_exp(m, l);
   }
 };
 

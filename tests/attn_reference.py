@@ -35,13 +35,17 @@ def half_step(dtype):
     return torch.finfo(dtype).eps / 2
 
 
-def head_forward(q, k, v, scale, before):
-    """One head: q [n, D] at positions before .. before + n - 1, k and v [m, D]. Returns
-    (out, lse, weights, bound of out, bound of the relative error of the weights)."""
+def head_forward(q, k, v, scale, before, gone=None):
+    """One head: q [n, D] at positions before .. before + n - 1, k and v [m, D]; keys of the
+    mask `gone` [m] are seen by nobody. Returns (out, lse, weights, bound of the relative
+    error of the weights)."""
     n, D = q.shape
     m = k.shape[0]
     q, k, v = q.to(F64), k.to(F64), v.to(F64)
     hidden = torch.arange(m, device=q.device)[None] > before + torch.arange(n, device=q.device)[:, None]
+    if gone is not None:
+        hidden = hidden | gone[None]
+        k, v = k.masked_fill(gone[:, None], 0.0), v.masked_fill(gone[:, None], 0.0)
     s = (q @ k.T * scale).masked_fill(hidden, float("-inf"))
     lse = torch.logsumexp(s, -1) if m else torch.full((n,), float("-inf"), dtype=F64, device=q.device)
     p = torch.exp(s - torch.where(lse == float("-inf"), 0.0, lse)[:, None])
@@ -68,6 +72,32 @@ def forward(q, k, v, seqs, scale):
         for h in range(Hq):
             o, l, p, rel = head_forward(q[a:a + n, h], k[a:a + n, h // G], v[a:a + n, h // G], scale, 0)
             spread = p @ v[a:a + n, h // G].to(F64).abs()
+            out[a:a + n, h], lse[a:a + n, h] = o, l
+            tol[a:a + n, h] = 1.01 * (u * (spread + o.abs()) + rel * spread)
+    return out, lse, tol + tiny(q.dtype)
+
+
+def paged(q, k_cache, v_cache, table, cu, lens, scale):
+    """(out, lse, bound of out) of the new tokens over a paged cache; keys behind the table or
+    on no page are seen by nobody."""
+    T, Hq, D = q.shape
+    pages, page, Hkv, _ = k_cache.shape
+    u = half_step(q.dtype)
+    out = torch.zeros((T, Hq, D), dtype=F64, device=q.device)
+    tol = torch.zeros_like(out)
+    lse = torch.full((T, Hq), float("-inf"), dtype=F64, device=q.device)
+    for s, (a, n) in enumerate(sequences(cu, T)):
+        m = min(max(int(lens[s]), 0), table.shape[1] * page)
+        if n == 0 or m == 0:
+            continue
+        at = torch.arange(m, device=q.device)
+        number = table[s].to(q.device).long()[at // page]
+        gone = (number < 0) | (number >= pages)
+        number = number.masked_fill(gone, 0)
+        for h in range(Hq):
+            k, v = k_cache[number, at % page, h // (Hq // Hkv)], v_cache[number, at % page, h // (Hq // Hkv)]
+            o, l, p, rel = head_forward(q[a:a + n, h], k, v, scale, int(lens[s]) - n, gone)
+            spread = p @ v.to(F64).masked_fill(gone[:, None], 0.0).abs()
             out[a:a + n, h], lse[a:a + n, h] = o, l
             tol[a:a + n, h] = 1.01 * (u * (spread + o.abs()) + rel * spread)
     return out, lse, tol + tiny(q.dtype)
