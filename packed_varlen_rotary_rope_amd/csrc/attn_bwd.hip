@@ -19,6 +19,8 @@
 namespace attn {
 namespace {
 
+constexpr int32_t kExactKeys = 256;  // tiles up to here form D_i from P and dP
+
 struct BwdParams {
   const void* dout;
   const void* q;
@@ -116,10 +118,6 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   const int64_t at_stat = at_row * p.Hq + head;
   float lse2 = p.lse[at_stat] * (float)kLog2e;
   if (lse2 == -__builtin_inff()) lse2 = 0.0f;  // every score is -inf: all weights are 0
-  if (on && half == 0) {
-    p.lse2[at_stat] = lse2;
-    p.delta[at_stat] = delta;
-  }
 
   f32x16 dq[DB];
 #pragma unroll
@@ -151,24 +149,36 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
     }
   };
 
-  auto block = [&](auto masked, const uint8_t* kt, const uint8_t* vt, int32_t key0) {
+  // P and dP of 32 keys; what is hidden gets P = dP = 0.
+  auto weights = [&](auto masked, const uint8_t* kt, const uint8_t* vt, int32_t key0, int b, f32x16& s,
+                     f32x16& dp) {
     constexpr bool MASKED = decltype(masked)::value;
-    const uint32_t r = lane & 31;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      s = mfma(read_rows<T, CPR>(kt, 32 * b + (lane & 31), 2 * t + half), qf[t], s);
+      dp = mfma(read_rows<T, CPR>(vt, 32 * b + (lane & 31), 2 * t + half), df[t], dp);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2));
+      if constexpr (MASKED) {
+        const int32_t key = key0 + 32 * b + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
+        if (key >= seen) s[i] = dp[i] = 0.0f;
+      }
+    }
+  };
+  auto block = [&](auto masked, const uint8_t* kt, int32_t key0) {
+    constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       f32x16 s, dp;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
-#pragma unroll
-      for (int t = 0; t < KS; ++t) {
-        s = mfma(read_rows<T, CPR>(kt, 32 * b + r, 2 * t + half), qf[t], s);
-        dp = mfma(read_rows<T, CPR>(vt, 32 * b + r, 2 * t + half), df[t], dp);
-      }
+      weights(masked, kt, kt + kTileBytes, key0, b, s, dp);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2));
-        s[i] = w * (dp[i] - delta);
-        if constexpr (MASKED) {
+        s[i] = s[i] * (dp[i] - delta);
+        if constexpr (MASKED) {  // also where D_i is not finite
           const int32_t key = key0 + 32 * b + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
           if (key >= seen) s[i] = 0.0f;
         }
@@ -190,17 +200,45 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   stage(0);
   settle<T>(qf);
   settle<T>(df);
-  for (int32_t b = 0; b < blocks; ++b) {
+  int32_t b = 0;
+  auto arrive = [&] {
     wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
     if (b + 1 < blocks) stage(b + 1);
-    const uint8_t* kt = lds + (b & 1) * 2 * kTileBytes;
-    const uint8_t* vt = kt + kTileBytes;
-    const int32_t key0 = b * BN;
-    if (key0 + BN <= wave_all) {
-      block(Constant<false>(), kt, vt, key0);
-    } else if (key0 < wave_end) {
-      block(Constant<true>(), kt, vt, key0);
+    return lds + (b & 1) * 2 * kTileBytes;
+  };
+  // D_i from the rounded output errs by half a step of it, which is most where a row sees few
+  // keys, and as much there as the rounding of dS. Such tiles form sum_j P_ij dP_ij first.
+  if (key_end <= kExactKeys) {
+    float sum = 0.0f;
+    for (; b < blocks; ++b) {
+      const uint8_t* kt = arrive();
+      if (b * BN >= wave_end) continue;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        f32x16 s, dp;
+        weights(Constant<true>(), kt, kt + kTileBytes, b * BN, c, s, dp);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(s[i], dp[i], sum);
+      }
     }
+    delta = half_sum(sum);
+    __syncthreads();  // the last block has been read
+    b = 0;
+    stage(0);
+  }
+  if (on && half == 0) {
+    p.lse2[at_stat] = lse2;
+    p.delta[at_stat] = delta;
+  }
+  // two loops, as in the forward
+  const int32_t all = wave_end > 0 ? wave_all / BN : 0;
+  for (; b < all; ++b) {
+    const uint8_t* kt = arrive();
+    block(Constant<false>(), kt, b * BN);
+  }
+  for (; b < blocks; ++b) {
+    const uint8_t* kt = arrive();
+    if (b * BN < wave_end) block(Constant<true>(), kt, b * BN);
   }
 #pragma unroll
   for (int d = 0; d < DB; ++d)
@@ -264,10 +302,16 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_keys_kernel(const BwdParams p
   const int64_t stat0 = (int64_t)start * p.Hq + kvh * p.G;
   const int32_t row_begin = key0 * p.G / BM * BM;
   const int32_t blocks = (rows - row_begin + BM - 1) / BM;
+  // A last block that rows end in goes first, so that the partly masked blocks of a wave (this
+  // one and those on its diagonal) are a first loop and the others a second.
+  const int32_t tail = (rows - row_begin) % BM != 0;
+  auto first_row = [&](int32_t i) {
+    return row_begin + (tail ? (i == 0 ? blocks - 1 : i - 1) : i) * BM;
+  };
 
   auto stage = [&](int32_t b) {
     const uint32_t qd = lds_address(lds) + (b & 1) * kStage, gd = qd + kTileBytes;
-    const int32_t row0 = row_begin + b * BM;
+    const int32_t row0 = first_row(b);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const uint32_t c = i * 256 + tid;
@@ -344,16 +388,21 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_keys_kernel(const BwdParams p
   stage(0);
   settle<T>(kf);
   settle<T>(vf);
-  for (int32_t b = 0; b < blocks; ++b) {
+  int32_t b = 0;
+  auto arrive = [&] {
     wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
     if (b + 1 < blocks) stage(b + 1);
-    const uint8_t* qt = lds + (b & 1) * kStage;
-    const int32_t row0 = row_begin + b * BM;
-    if (row0 >= wave_all && row0 + BM <= rows) {
-      if (wave_first < rows) block(Constant<false>(), qt, row0);
-    } else if (row0 + BM > wave_first) {
-      block(Constant<true>(), qt, row0);
-    }
+    return lds + (b & 1) * kStage;
+  };
+  const int32_t masked =
+      wave_first < rows ? min(blocks, tail + max(0, wave_all - row_begin + BM - 1) / BM) : blocks;
+  for (; b < masked; ++b) {
+    const uint8_t* qt = arrive();
+    if (first_row(b) + BM > wave_first && wave_first < rows) block(Constant<true>(), qt, first_row(b));
+  }
+  for (; b < blocks; ++b) {
+    const uint8_t* qt = arrive();
+    block(Constant<false>(), qt, first_row(b));
   }
 #pragma unroll
   for (int d = 0; d < DB; ++d)

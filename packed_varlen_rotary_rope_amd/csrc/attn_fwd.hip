@@ -106,17 +106,23 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
 
   stage(0);
   settle<T>(t.q);
-  for (int32_t b = 0; b < blocks; ++b) {
+  // Two loops, so that neither body's registers are moved for the other's sake. Waves may be
+  // in different ones: each passes one barrier per block in either.
+  const int32_t all = wave_end > 0 ? wave_all / BN : 0;  // blocks that every row of the wave sees
+  int32_t b = 0;
+  auto arrive = [&] {
     wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
     if (b + 1 < blocks) stage(b + 1);
-    const uint8_t* kt = lds + (b & 1) * 2 * Tile::kTileBytes;
-    const uint8_t* vt = kt + Tile::kTileBytes;
-    const int32_t key0 = b * BN;
-    if (key0 + BN <= wave_all) {
-      t.template block<false>(kt, vt, key0, seen, 0, p.scale, lane);
-    } else if (key0 < wave_end) {
-      t.template block<true>(kt, vt, key0, seen, 0, p.scale, lane);
-    }
+    return lds + (b & 1) * 2 * Tile::kTileBytes;
+  };
+  for (; b < all; ++b) {
+    const uint8_t* kt = arrive();
+    t.template block<false>(kt, kt + Tile::kTileBytes, b * BN, seen, 0, p.scale, lane);
+  }
+  for (; b < blocks; ++b) {
+    const uint8_t* kt = arrive();
+    if (b * BN < wave_end)
+      t.template block<true>(kt, kt + Tile::kTileBytes, b * BN, seen, 0, p.scale, lane);
   }
 
   const float lse = t.finish();

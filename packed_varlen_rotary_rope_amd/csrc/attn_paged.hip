@@ -385,7 +385,11 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
       stage(0);
     }
     settle<T>(t.q);
-    for (int32_t b = 0; b < blocks; ++b) {
+    // Two loops, so that neither body's registers are moved for the other's sake; the first
+    // ends at the first block that is not wholly seen, or that has keys on no page.
+    const int32_t all = wave_end > 0 ? max(0, wave_all - item.key0) / BN : 0;
+    int32_t b = 0;
+    auto arrive = [&] {
       const int32_t key0 = item.key0 + b * BN;
       wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
       hidden = hidden_next;
@@ -394,13 +398,17 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
         src.fetch_pages(p, key0 + 2 * BN, b & 1, lane);
         stage(b + 1);
       }
-      const uint8_t* kt = lds + (b & 1) * 2 * kTileBytes;
-      const uint8_t* vt = kt + kTileBytes;
-      if (key0 + BN <= wave_all && hidden == 0) {
-        t.template block<false>(kt, vt, key0, seen, 0, p.scale, lane);
-      } else if (key0 < wave_end) {
-        t.template block<true>(kt, vt, key0, seen, hidden, p.scale, lane);
-      }
+      return lds + (b & 1) * 2 * kTileBytes;
+    };
+    for (; b < all && hidden_next == 0; ++b) {
+      const uint8_t* kt = arrive();
+      t.template block<false>(kt, kt + kTileBytes, item.key0 + b * BN, seen, 0, p.scale, lane);
+    }
+    for (; b < blocks; ++b) {
+      const uint8_t* kt = arrive();
+      const int32_t key0 = item.key0 + b * BN;
+      if (key0 < wave_end)
+        t.template block<true>(kt, kt + kTileBytes, key0, seen, hidden, p.scale, lane);
     }
     if (item.slot < 0) {
       const float lse = t.finish();
@@ -460,9 +468,10 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
       stage(kb, kt, 0);
       if (!kOneBuffer) stage(vb, vt, 0);
     }
-    for (int32_t b = 0; b < blocks; ++b) {
+    auto round = [&](auto masked, int32_t b) {
+      constexpr bool MASKED = decltype(masked)::value;
       const int32_t key0 = first + 128 * b;
-      const bool masked = key0 + 32 > wave_all || hidden_next != 0, more = b + 1 < blocks;
+      const bool more = b + 1 < blocks;
       hidden = hidden_next;
       f32x16 s[1];
       x8<T> w[2];
@@ -475,18 +484,22 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
         src.fetch_pages(p, key0 + 256, b & 1, lane);
         if (!kOneBuffer) stage(kb, kt, (b + 1) & 1);
       }
-      if (masked) t.template weights<true>(s, w, key0, seen, hidden, p.scale, lane);
-      else t.template weights<false>(s, w, key0, seen, 0, p.scale, lane);
+      t.template weights<MASKED>(s, w, key0, seen, hidden, p.scale, lane);
       if (more && !kOneBuffer) wait_copies<kLoads + 1>();
       else wait_copies<0>();
-      if (masked) t.template accumulate<true>(w, vt, key0, seen, hidden, lane);
-      else t.template accumulate<false>(w, vt, key0, seen, 0, lane);
+      t.template accumulate<MASKED>(w, vt, key0, seen, hidden, lane);
       reads_done();
       if (more) {
         if (kOneBuffer) stage(kb, kt, (b + 1) & 1);
         else stage(vb, vt, (b + 1) & 1);
       }
-    }
+    };
+    // blocks that every row sees whole, then the others (two loops, as above)
+    const int32_t whole = max(0, wave_all - first) / 32;
+    const int32_t all = wave_all >= first + 32 ? min(blocks, (whole - 1) / 4 + 1) : 0;
+    int32_t b = 0;
+    for (; b < all && hidden_next == 0; ++b) round(Constant<false>(), b);
+    for (; b < blocks; ++b) round(Constant<true>(), b);
   }
 
   // Join the waves: O scaled to the common maximum goes to LDS four blocks of columns at a
@@ -564,33 +577,50 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
 template <typename T>
 __global__ __launch_bounds__(256) void paged_join_kernel(const PagedParams p) {
   const uint32_t index = div31(blockIdx.x, p.by_hkv);
-  const uint32_t kvh = blockIdx.x - index * p.Hkv;
+  const uint32_t kvh = blockIdx.x - index * p.Hkv, part = blockIdx.y;
   if (!plan_matches(p) || (int32_t)index >= p.plan[1]) return;
   const Join j = p.joins[index];
   if (j.q0 < 0 || j.row0 < 0 || j.rows <= 0 || j.rows > kRowTile || j.units < (j.rows + 31) / 32 ||
       j.splits < 0 || j.slot < 0 || j.slot + (int64_t)j.splits * j.units > p.units ||
       j.q0 + (j.row0 + j.rows - 1) / p.G >= p.T)
     return;
+  const int32_t rows = min(32, j.rows - 32 * (int32_t)part);
   const uint32_t groups = p.D >> 2;
-  for (uint32_t i = threadIdx.x; i < j.rows * groups; i += 256) {
+  const int64_t step = (int64_t)j.units * p.Hkv * 32;
+  const int64_t unit0 = ((int64_t)(j.slot + part) * p.Hkv + kvh) * 32;
+  for (int32_t i = threadIdx.x; i < rows * (int32_t)groups; i += 256) {
     const uint32_t y = i / groups, e = 4 * (i - y * groups);
-    const int64_t step = (int64_t)j.units * p.Hkv * 32;
-    const int64_t unit = ((int64_t)(j.slot + (y >> 5)) * p.Hkv + kvh) * 32 + (y & 31);
-    float m = -__builtin_inff();
-    for (int32_t s = 0; s < j.splits; ++s)
-      m = __builtin_fmaxf(m, p.part_ml[2 * (unit + s * step)]);
-    float l = 0.0f;
+    const float* ml = p.part_ml + 2 * (unit0 + y);
+    const float* o = p.part_o + (unit0 + y) * p.D + e;
+    float m = -__builtin_inff(), l = 0.0f;
     f32x4 x = {0, 0, 0, 0};
-    for (int32_t s = 0; s < j.splits; ++s) {
-      const int64_t u = unit + s * step;
-      const float ms = p.part_ml[2 * u];
-      const float f = ms == m ? 1.0f : __builtin_amdgcn_exp2f(ms - m);
-      l = __builtin_fmaf(p.part_ml[2 * u + 1], f, l);
-      const f32x4 part = *reinterpret_cast<const f32x4*>(p.part_o + u * p.D + e);
+    for (int32_t s0 = 0; s0 < j.splits; s0 += 8) {  // eight splits' loads at a time
+      f32x2 w[8];
+      f32x4 v[8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = __builtin_fmaf(part[c], f, x[c]);
+      for (int u = 0; u < 8; ++u) {
+        const int64_t s = min(s0 + u, j.splits - 1);
+        w[u] = *reinterpret_cast<const f32x2*>(ml + 2 * s * step);
+        v[u] = *reinterpret_cast<const f32x4*>(o + s * step * p.D);
+      }
+      float top = m;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) top = __builtin_fmaxf(top, w[u][0]);
+      const float f0 = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+      m = top;
+      l *= f0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] *= f0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (s0 + u >= j.splits) break;
+        const float f = w[u][0] == m ? 1.0f : __builtin_amdgcn_exp2f(w[u][0] - m);
+        l = __builtin_fmaf(w[u][1], f, l);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = __builtin_fmaf(v[u][c], f, x[c]);
+      }
     }
-    const int32_t packed = j.row0 + y, tok = div31(packed, p.by_g);
+    const int32_t packed = j.row0 + 32 * part + y, tok = div31(packed, p.by_g);
     const int32_t h = kvh * p.G + (packed - tok * p.G);
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
     const u32x2 word = {narrow2<T>(x[0] * inv, x[1] * inv), narrow2<T>(x[2] * inv, x[3] * inv)};
@@ -606,7 +636,8 @@ int32_t launch(const PagedParams& p, const Sizes& sizes, hipStream_t s) {
                      s, p);
   const int32_t st = launched();
   if (st != ROPE_OK) return st;
-  hipLaunchKernelGGL((paged_join_kernel<T>), dim3((unsigned)(sizes.joins * p.Hkv)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((paged_join_kernel<T>), dim3((unsigned)(sizes.joins * p.Hkv), kRowTile / 32),
+                     dim3(256), 0, s, p);
   return launched();
 }
 
