@@ -78,11 +78,15 @@ int32_t attn_fwd(const void* q, const void* k, const void* v, void* out, float* 
                  int64_t v_stride, int64_t out_stride, const int32_t* plan, int32_t num_seqs,
                  double scale, int32_t dtype, int32_t fill, void* stream);
 
+/* Floats of attn_bwd's scratch, or -1 for bad arguments. */
+int64_t attn_bwd_scratch_floats(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D);
+
 /* Its gradients, from dout and what attn_fwd read and wrote:
  *     dP_ij = dout_i . v_j,  D_i = dout_i . out_i,  dS_ij = P_ij (dP_ij - D_i),
  *     dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
  * with i over the queries of every head that reads key/value head j's head.
- *  scratch     device float [2][T][Hq]
+ *  scratch     device float[attn_bwd_scratch_floats(...)], 16-byte aligned: calls that may
+ *              run at the same time need one each
  *  dq, dk, dv  device, written; token strides as the others'
  *  fill        as in attn_fwd: 1 writes zeros to the gradients of rows of no sequence
  * D is at most 128. */

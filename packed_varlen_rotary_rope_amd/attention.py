@@ -36,6 +36,8 @@ def _load() -> ctypes.CDLL:
     lib.attn_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, i32, i64, i64, i64, i64, vp, i32, dbl,
                              i32, i32, vp]
     lib.attn_bwd.argtypes = [vp] * 10 + [i64, i32, i32, i32] + [i64] * 8 + [vp, i32, dbl, i32, i32, vp]
+    lib.attn_bwd_scratch_floats.argtypes = [i64, i32, i32, i32, i32]
+    lib.attn_bwd_scratch_floats.restype = i64
     lib.kv_append.argtypes = ([vp] * 6 + [i64, i32, i32, i32] + [i64] * 4 + [i32, i32] + [i64] * 3 +
                               [vp, i32, i64, vp, i32, vp, dbl, dbl, i32, vp])
     lib.paged_plan_ints.argtypes = [i64, i32, i32, i32]
@@ -135,8 +137,9 @@ class AttnPlan:
     def _match(self, q, k, v):
         if q.dim() != 3 or k.dim() != 3 or q.shape[0] != self.T:
             raise ValueError(f"expected q [{self.T}, Hq, D] and k, v [{self.T}, Hkv, D]")
-        if q.shape[1] * self.num_kv_heads != k.shape[1] * self.num_q_heads:
-            raise ValueError("the plan was made for another ratio of query to key/value heads")
+        if (q.shape[1], k.shape[1]) != (self.num_q_heads, self.num_kv_heads):
+            raise ValueError(f"the plan was made for {self.num_q_heads} query and "
+                             f"{self.num_kv_heads} key/value heads")
         if k.shape[0] != self.T or k.shape[2] != q.shape[2] or v.shape != k.shape:
             raise ValueError("k and v must be [T, Hkv, D] with q's T and D")
         if k.dtype != q.dtype or v.dtype != q.dtype:
@@ -149,7 +152,7 @@ def attn_plan(cu_seqlens, T: int, num_q_heads: int, num_kv_heads: int, seqused=N
     """The plan of a packed batch of T rows whose sequence s is the rows cu_seqlens[s] ..
     cu_seqlens[s+1] - 1 (int32[B+1] on the GPU; with `seqused`, int32[B], only the first
     seqused[s] of them): one small launch, no host synchronization. It serves every layer
-    of the batch, forward and backward, and any head counts of the same ratio.
+    of the batch, forward and backward.
     `out`: a plan of the same sizes to be written over (for a captured graph's replays)."""
     dev = cu_seqlens.device
     _gpu(dev)
@@ -165,8 +168,8 @@ def attn_plan(cu_seqlens, T: int, num_q_heads: int, num_kv_heads: int, seqused=N
                          "key/value heads (the query heads must be a multiple)")
     if out is None:
         out = AttnPlan(T, num_seqs, Hq, Hkv, torch.empty(words, dtype=torch.int32, device=dev))
-    elif (out.T, out.num_seqs, out.buffer.device) != (T, num_seqs, dev) or \
-            out.num_q_heads * Hkv != Hq * out.num_kv_heads:
+    elif (out.T, out.num_seqs, out.num_q_heads, out.num_kv_heads, out.buffer.device) != \
+            (T, num_seqs, Hq, Hkv, dev):
         raise ValueError("out: a plan of other sizes or of another device")
     with torch.cuda.device(dev):
         _check(_lib.attn_plan(_ptr(cu), num_seqs, _ptr(su), T, Hq, Hkv, _ptr(out.buffer), words,
@@ -226,7 +229,8 @@ def attn_bwd(dout, q, k, v, out, lse, plan: AttnPlan, scale=None, dq=None, dk=No
     _like(dv, q, (T, Hkv, D), "dv")
     strides = [_heads_last(t, name) for t, name in (
         (dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"), (dq, "dq"), (dk, "dk"), (dv, "dv"))]
-    scratch = torch.empty((2, T, Hq), dtype=torch.float32, device=q.device)
+    scratch = torch.empty(_lib.attn_bwd_scratch_floats(T, plan.num_seqs, Hq, Hkv, D),
+                          dtype=torch.float32, device=q.device)
     with torch.cuda.device(q.device):
         _check(_lib.attn_bwd(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(scratch),
                              _ptr(dq), _ptr(dk), _ptr(dv), T, Hq, Hkv, D, *strides,

@@ -14,6 +14,7 @@
 // the other side is shared through LDS, read along rows and, by transposing reads, along
 // columns. S and dP are formed twice, 14 flops per pair and element of D instead of 10;
 // the price of having no fp32 sums of dQ in memory.
+#include "attn_packed.h"
 #include "attn_tile.h"
 
 namespace attn {
@@ -34,7 +35,11 @@ struct BwdParams {
   void* dk;
   void* dv;
   const int32_t* plan;
-  const int4* items;
+  const RowItem* row_items;
+  const KeyItem* key_items;
+  const KeyJoin* joins;
+  float* part;    // scratch: [slot][Hkv][dK, dV][128][D], of tiles whose rows are split
+  int64_t units;  // its slots
   int64_t dout_stride, q_stride, k_stride, v_stride, out_stride, dq_stride, dk_stride, dv_stride;
   int32_t T, Hq, Hkv, G, D, num_seqs;
   float scale, scale2;  // scale2: times log2 e
@@ -43,14 +48,16 @@ struct BwdParams {
 };
 
 // The item of this workgroup, or n = 0 where there is none.
-__device__ inline int4 find_item(const BwdParams& p, int list, uint32_t* kvh) {
+template <typename I>
+__device__ inline I find_item(const BwdParams& p, const I* items, int list, uint32_t* kvh) {
   const uint32_t index = div31(blockIdx.x, p.by_hkv);
   *kvh = blockIdx.x - index * p.Hkv;
-  const int4 none = make_int4(0, 0, 0, 0);
-  if (p.plan[2] != p.T || p.plan[3] != p.G || p.plan[4] != p.num_seqs) return none;
-  if ((int32_t)index >= p.plan[list]) return none;
-  const int4 item = p.items[index];
-  return item.x < 0 || item.y <= 0 || item.x > p.T - item.y ? none : item;
+  I item;
+  item.n = 0;
+  if (!plan_matches(p) || (int32_t)index >= p.plan[list]) return item;
+  item = items[index];
+  if (item.start < 0 || item.n <= 0 || item.start > p.T - item.n) item.n = 0;
+  return item;
 }
 
 // Zeros to `n` rows of `heads` heads from head0.
@@ -67,24 +74,25 @@ __device__ inline void clear_rows(T* x, int32_t start, int32_t n, int64_t stride
 
 template <typename T, int DB>
 __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p) {
-  constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BN = 64;
+  constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BN = 32;
   constexpr int kTileBytes = BN * CPR * 16, kLoads = BN * CPR / 256;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * kTileBytes];
+  constexpr int kStages = 5;  // 80 KB at most: two workgroups on a CU
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * 2 * kTileBytes];
 
   uint32_t kvh;
-  const int4 item = find_item(p, 0, &kvh);
-  const int32_t start = item.x, n = item.y;
+  const RowItem item = find_item(p, p.row_items, 0, &kvh);
+  const int32_t start = item.start, n = item.n;
   if (n == 0) return;
   const uint32_t tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t chunks = p.D >> 3;
-  if (item.w != 0) {
+  if (item.gap != 0) {
     if (p.fill) clear_rows(static_cast<T*>(p.dq), start, n, p.dq_stride, kvh * p.G, p.G, chunks);
     return;
   }
 
   const int32_t rows = n * p.G;
-  const int32_t row0 = item.z;
+  const int32_t row0 = item.row0;
   if (row0 < 0 || row0 >= rows) return;
   const int32_t row_end = min(row0 + kRowTile, rows);
   const int32_t wave_row0 = row0 + 32 * wave;
@@ -120,17 +128,13 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   if (lse2 == -__builtin_inff()) lse2 = 0.0f;  // every score is -inf: all weights are 0
 
   f32x16 dq[DB];
-#pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) dq[d][i] = 0.0f;
-  clear_unused_chunks<CPR>(lds, 4 * BN, chunks);
+  clear_unused_chunks<CPR>(lds, kStages * 2 * BN, chunks);
 
   const T* k = static_cast<const T*>(p.k) + (int64_t)start * p.k_stride + (int64_t)kvh * p.D;
   const T* v = static_cast<const T*>(p.v) + (int64_t)start * p.v_stride + (int64_t)kvh * p.D;
   const int32_t blocks = (key_end + BN - 1) / BN;
-  auto stage = [&](int32_t b) {
-    const uint32_t kd = lds_address(lds) + (b & 1) * 2 * kTileBytes;
+  auto stage = [&](int32_t b) __attribute__((always_inline)) {
+    const uint32_t kd = lds_address(lds) + b % kStages * 2 * kTileBytes;
     const uint32_t vd = kd + kTileBytes;
     const int32_t key0 = b * BN;
     const T* kb = k + (int64_t)key0 * p.k_stride;
@@ -139,7 +143,7 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const uint32_t c = i * 256 + tid;
-      const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle(r);
+      const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle<CPR>(r);
       const uint32_t at = (uint32_t)min((int32_t)r, last);
       const uint32_t dst = (i * 256 + wave * 64) * 16;
       if (chunk < chunks) {
@@ -150,62 +154,59 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   };
 
   // P and dP of 32 keys; what is hidden gets P = dP = 0.
-  auto weights = [&](auto masked, const uint8_t* kt, const uint8_t* vt, int32_t key0, int b, f32x16& s,
-                     f32x16& dp) {
-    constexpr bool MASKED = decltype(masked)::value;
+  auto weights = [&](auto mode, const uint8_t* kt, int32_t key0, f32x16& s, f32x16& dp) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
-      s = mfma(read_rows<T, CPR>(kt, 32 * b + (lane & 31), 2 * t + half), qf[t], s);
-      dp = mfma(read_rows<T, CPR>(vt, 32 * b + (lane & 31), 2 * t + half), df[t], dp);
+      s = mfma(read_rows<T, CPR>(kt, lane & 31, 2 * t + half), qf[t], s);
+      dp = mfma(read_rows<T, CPR>(kt + kTileBytes, lane & 31, 2 * t + half), df[t], dp);
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2));
-      if constexpr (MASKED) {
-        const int32_t key = key0 + 32 * b + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
+      if constexpr (decltype(mode)::value != kWhole) {
+        const int32_t key = key0 + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
         if (key >= seen) s[i] = dp[i] = 0.0f;
       }
     }
   };
-  auto block = [&](auto masked, const uint8_t* kt, int32_t key0) {
-    constexpr bool MASKED = decltype(masked)::value;
+  auto block = [&](auto mode, const uint8_t* kt, int32_t key0) __attribute__((always_inline)) {
+    f32x16 s, dp;
+    weights(mode, kt, key0, s, dp);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f32x16 s, dp;
-      weights(masked, kt, kt + kTileBytes, key0, b, s, dp);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[i] = s[i] * (dp[i] - delta);
-        if constexpr (MASKED) {  // also where D_i is not finite
-          const int32_t key = key0 + 32 * b + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
-          if (key >= seen) s[i] = 0.0f;
-        }
+    for (int i = 0; i < 16; ++i) {
+      s[i] = s[i] * (dp[i] - delta);
+      if constexpr (decltype(mode)::value != kWhole) {  // also where D_i is not finite
+        const int32_t key = key0 + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
+        if (key >= seen) s[i] = 0.0f;
       }
+    }
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const x8<T> ds = narrow8<T>(s, t);
+    for (int t = 0; t < 2; ++t) {
+      const x8<T> ds = narrow8<T>(s, t);
 #pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          x8<T> kc = read_columns<T, CPR>(kt, 32 * b + 16 * t, d, lane);
-          // a key that is seen and not finite has made dS NaN or 0 already
-          if constexpr (MASKED) kc = cleaned<T>(kc);
-          dq[d] = mfma(kc, ds, dq[d]);
-        }
+      for (int d = 0; d < DB; ++d) {
+        x8<T> kc = read_columns<T, CPR>(kt, 16 * t, d, lane);
+        // a key that is seen and not finite has made dS NaN or 0 already
+        if constexpr (decltype(mode)::value == kCareful) kc = cleaned<T>(kc);
+        dq[d] = mfma(kc, ds, dq[d]);
       }
     }
   };
 
-  stage(0);
+  int32_t b = 0;
+  auto first_stages = [&]() __attribute__((always_inline)) {
+    for (int32_t i = 0; i < min(blocks, kStages - 1); ++i) stage(i);
+  };
+  auto arrive = [&]() __attribute__((always_inline)) {
+    wait_ring<kStages, 2 * kLoads>(blocks - 1 - b);
+    if (b + kStages - 1 < blocks) stage(b + kStages - 1);
+    return lds + b % kStages * 2 * kTileBytes;
+  };
+  first_stages();
   settle<T>(qf);
   settle<T>(df);
-  int32_t b = 0;
-  auto arrive = [&] {
-    wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
-    if (b + 1 < blocks) stage(b + 1);
-    return lds + (b & 1) * 2 * kTileBytes;
-  };
   // D_i from the rounded output errs by half a step of it, which is most where a row sees few
   // keys, and as much there as the rounding of dS. Such tiles form sum_j P_ij dP_ij first.
   if (key_end <= kExactKeys) {
@@ -213,32 +214,41 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
     for (; b < blocks; ++b) {
       const uint8_t* kt = arrive();
       if (b * BN >= wave_end) continue;
+      f32x16 s, dp;
+      weights(Constant<kMasked>(), kt, b * BN, s, dp);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        f32x16 s, dp;
-        weights(Constant<true>(), kt, kt + kTileBytes, b * BN, c, s, dp);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(s[i], dp[i], sum);
-      }
+      for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(s[i], dp[i], sum);
     }
     delta = half_sum(sum);
     __syncthreads();  // the last block has been read
     b = 0;
-    stage(0);
+    first_stages();
   }
   if (on && half == 0) {
     p.lse2[at_stat] = lse2;
     p.delta[at_stat] = delta;
   }
-  // two loops, as in the forward
+  // two loops, and a second walk where it is needed, as in the forward
   const int32_t all = wave_end > 0 ? wave_all / BN : 0;
-  for (; b < all; ++b) {
-    const uint8_t* kt = arrive();
-    block(Constant<false>(), kt, b * BN);
-  }
-  for (; b < blocks; ++b) {
-    const uint8_t* kt = arrive();
-    if (b * BN < wave_end) block(Constant<true>(), kt, b * BN);
+  auto walk = [&](auto mode) __attribute__((always_inline)) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dq[d][i] = 0.0f;
+    for (; b < all; ++b) {
+      const uint8_t* kt = arrive();
+      block(Constant<kWhole>(), kt, b * BN);
+    }
+    for (; b < blocks; ++b) {
+      const uint8_t* kt = arrive();
+      if (b * BN < wave_end) block(mode, kt, b * BN);
+    }
+  };
+  walk(Constant<kMasked>());
+  if (any_wave(any_nonfinite(dq), lds)) {
+    b = 0;
+    first_stages();
+    walk(Constant<kCareful>());
   }
 #pragma unroll
   for (int d = 0; d < DB; ++d)
@@ -249,29 +259,29 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
 }
 
 template <typename T, int DB>
-__global__ __launch_bounds__(256, 1) void attn_bwd_keys_kernel(const BwdParams p) {
-  constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BM = 32;
+__global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(const BwdParams p) {
+  constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BM = kRowBlock;
   constexpr int kTileBytes = BM * CPR * 16, kLoads = BM * CPR / 256;
-  constexpr int kStatBytes = 2 * BM * 4, kStage = 2 * kTileBytes + kStatBytes;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  constexpr int kStatBytes = 2 * BM * 4, kStage = 2 * kTileBytes + kStatBytes, kStages = 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage];
 
   uint32_t kvh;
-  const int4 item = find_item(p, 1, &kvh);
-  const int32_t start = item.x, n = item.y;
+  const KeyItem item = find_item(p, p.key_items, 1, &kvh);
+  const int32_t start = item.start, n = item.n;
   if (n == 0) return;
   const uint32_t tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t chunks = p.D >> 3;
   T* dk_out = static_cast<T*>(p.dk);
   T* dv_out = static_cast<T*>(p.dv);
-  if (item.w != 0) {
+  if (item.gap != 0) {
     if (p.fill) {
       clear_rows(dk_out, start, n, p.dk_stride, kvh, 1, chunks);
       clear_rows(dv_out, start, n, p.dv_stride, kvh, 1, chunks);
     }
     return;
   }
-  const int32_t key0 = item.z;
+  const int32_t key0 = item.key0;
   if (key0 < 0 || key0 >= n) return;
 
   const int32_t rows = n * p.G;
@@ -290,32 +300,29 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_keys_kernel(const BwdParams p
   load_row<T>(vf, static_cast<const T*>(p.v) + (int64_t)(start + at_key) * p.v_stride +
                       (int64_t)kvh * p.D, half, chunks);
   f32x16 dk[DB], dv[DB];
-#pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.0f;
-  for (int b = 0; b < 2; ++b) clear_unused_chunks<CPR>(lds + b * kStage, 2 * BM, chunks);
+  for (int b = 0; b < kStages; ++b) clear_unused_chunks<CPR>(lds + b * kStage, 2 * BM, chunks);
 
   const T* q = static_cast<const T*>(p.q) + (int64_t)start * p.q_stride + (int64_t)kvh * p.G * p.D;
   const T* g = static_cast<const T*>(p.dout) + (int64_t)start * p.dout_stride +
                (int64_t)kvh * p.G * p.D;
   const int64_t stat0 = (int64_t)start * p.Hq + kvh * p.G;
-  const int32_t row_begin = key0 * p.G / BM * BM;
-  const int32_t blocks = (rows - row_begin + BM - 1) / BM;
+  if (item.block0 < 0 || item.block_end > (rows + BM - 1) / BM || item.slot >= p.units) return;
+  const int32_t row_begin = item.block0 * BM;
+  const int32_t blocks = item.block_end - item.block0;
   // A last block that rows end in goes first, so that the partly masked blocks of a wave (this
   // one and those on its diagonal) are a first loop and the others a second.
-  const int32_t tail = (rows - row_begin) % BM != 0;
-  auto first_row = [&](int32_t i) {
+  const int32_t tail = blocks > 0 && item.block_end * BM > rows;
+  auto first_row = [&](int32_t i) __attribute__((always_inline)) {
     return row_begin + (tail ? (i == 0 ? blocks - 1 : i - 1) : i) * BM;
   };
 
-  auto stage = [&](int32_t b) {
-    const uint32_t qd = lds_address(lds) + (b & 1) * kStage, gd = qd + kTileBytes;
+  auto stage = [&](int32_t b) __attribute__((always_inline)) {
+    const uint32_t qd = lds_address(lds) + b % kStages * kStage, gd = qd + kTileBytes;
     const int32_t row0 = first_row(b);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const uint32_t c = i * 256 + tid;
-      const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle(r);
+      const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle<CPR>(r);
       const uint32_t at = min(row0 + (int32_t)r, rows - 1);
       const uint32_t t = div31(at, p.by_g), h = at - t * p.G;
       const uint32_t dst = (i * 256 + wave * 64) * 16;
@@ -324,85 +331,150 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_keys_kernel(const BwdParams p
         copy_chunk_to_lds(g + (int64_t)t * p.dout_stride + (h * p.D + 8 * chunk), gd + dst);
       }
     }
-    if (wave == 0) {  // lse and D of the rows: 32 words each
+    {  // lse and D of the rows, 32 words each; by every wave, for equal counts of copies
       const uint32_t at = min(row0 + (int32_t)(lane & 31), rows - 1);
       const uint32_t t = div31(at, p.by_g), h = at - t * p.G;
       copy_word_to_lds((half ? p.delta : p.lse2) + stat0 + (int64_t)t * p.Hq + h, gd + kTileBytes);
     }
   };
 
-  auto block = [&](auto masked, const uint8_t* qt, int32_t row0) {
-    constexpr bool MASKED = decltype(masked)::value;
-    const uint8_t* gt = qt + kTileBytes;
-    const float* stat = reinterpret_cast<const float*>(gt + kTileBytes);
-    const uint32_t r = lane & 31;
-    f32x16 s, dp;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
-#pragma unroll
-    for (int t = 0; t < KS; ++t) {
-      s = mfma(read_rows<T, CPR>(qt, r, 2 * t + half), kf[t], s);
-      dp = mfma(read_rows<T, CPR>(gt, r, 2 * t + half), vf[t], dp);
-    }
+  // The loop is pipelined over two blocks, because a wave is alone on its SIMD: while the
+  // matrix unit forms S and dP of the next block, the vector unit turns this block's into P
+  // and dS, a slice of them per step; then dV and dK follow. `order()` keeps the steps apart
+  // for the scheduler, with LDS read two steps ahead of its use.
+  f32x16 s, dp;         // of the block at hand, then of the next one
+  f32x4 lse2[4], delta[4];
+  auto order = [] { __builtin_amdgcn_sched_barrier(0); };
+  auto read_stats = [&](const uint8_t* qt) __attribute__((always_inline)) {
+    const float* stat = reinterpret_cast<const float*>(qt + 2 * kTileBytes);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const f32x4 lse2 = *reinterpret_cast<const f32x4*>(stat + 8 * j + 4 * half);
-      const f32x4 delta = *reinterpret_cast<const f32x4*>(stat + 32 + 8 * j + 4 * half);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 4 * j + e;
-        float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2[e]));
-        float d = w * (dp[i] - delta[e]);
-        if constexpr (MASKED) {
-          const int32_t at = row0 + 8 * j + 4 * (int32_t)half + e;
-          if (at < first || at >= rows) w = d = 0.0f;
-        }
-        s[i] = w;
-        dp[i] = d;
-      }
-    }
-    uint32_t bad = 0;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const x8<T> w = narrow8<T>(s, t), ds = narrow8<T>(dp, t);
-#pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        x8<T> gc = read_columns<T, CPR>(gt, 16 * t, d, lane);
-        x8<T> qc = read_columns<T, CPR>(qt, 16 * t, d, lane);
-        if constexpr (MASKED) {
-          bad |= nonfinite<T>(gc);
-          gc = cleaned<T>(gc);
-          qc = cleaned<T>(qc);  // one that sees the key has made dS NaN or 0 already
-        }
-        dv[d] = mfma(gc, w, dv[d]);
-        dk[d] = mfma(qc, ds, dk[d]);
-      }
-    }
-    if constexpr (MASKED) {
-      if (__any(bad != 0))
-        for (int32_t j = 0; j < BM; ++j)
-          add_nonfinite_row<T, DB, CPR>(dv, gt, j, row0 + j >= first && row0 + j < rows, half);
+      lse2[j] = *reinterpret_cast<const f32x4*>(stat + 8 * j + 4 * half);
+      delta[j] = *reinterpret_cast<const f32x4*>(stat + 32 + 8 * j + 4 * half);
     }
   };
+  // S and dP of the block at `qt`; `slice(t)` is called in step t of KS.
+  auto scores = [&](const uint8_t* qt, f32x16& s_out, f32x16& dp_out, auto slice) __attribute__((always_inline)) {
+    x8<T> qr[KS], gr[KS];
+    auto read = [&](int t) __attribute__((always_inline)) {
+      qr[t] = read_rows<T, CPR>(qt, lane & 31, 2 * t + half);
+      gr[t] = read_rows<T, CPR>(qt + kTileBytes, lane & 31, 2 * t + half);
+    };
+    read(0);
+    read(1);
+    f32x16 a, c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a[i] = c[i] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      order();
+      if (t + 2 < KS) read(t + 2);
+      slice(t);
+      a = mfma(qr[t], kf[t], a);
+      c = mfma(gr[t], vf[t], c);
+    }
+    order();
+    s_out = a;
+    dp_out = c;
+  };
+  auto round = [&](auto mode, const uint8_t* qt, const uint8_t* next, int32_t row0) __attribute__((always_inline)) {
+    constexpr int MODE = decltype(mode)::value;
+    const uint8_t* gt = qt + kTileBytes;
+    f32x16 w, ds, s_next, dp_next;
+    scores(next, s_next, dp_next, [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 16 * t / KS; i < 16 * (t + 1) / KS; ++i) {
+        const int j = i / 4, e = i % 4;
+        w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2[j][e]));
+        ds[i] = w[i] * (dp[i] - delta[j][e]);
+        if constexpr (MODE != kWhole) {
+          const int32_t at = row0 + 8 * j + 4 * (int32_t)half + e;
+          if (at < first || at >= rows) w[i] = ds[i] = 0.0f;
+        }
+      }
+    });
+    s = s_next;
+    dp = dp_next;
+    read_stats(next);
+    x8<T> gc[2 * DB], qc[2 * DB];  // by step: 16 rows t = step / DB, columns d = step % DB
+    auto read = [&](int x) __attribute__((always_inline)) {
+      gc[x] = read_columns<T, CPR>(gt, 16 * (x / DB), x % DB, lane);
+      qc[x] = read_columns<T, CPR>(qt, 16 * (x / DB), x % DB, lane);
+    };
+    read(0);
+    read(1);
+    x8<T> wb, db;
+#pragma unroll
+    for (int x = 0; x < 2 * DB; ++x) {
+      order();
+      if (x + 2 < 2 * DB) read(x + 2);
+      if (x % DB == 0) {
+        wb = narrow8<T>(w, x / DB);
+        db = narrow8<T>(ds, x / DB);
+      }
+      if constexpr (MODE == kCareful) {
+        gc[x] = cleaned<T>(gc[x]);
+        qc[x] = cleaned<T>(qc[x]);  // one that sees the key has made dS NaN or 0 already
+      }
+      dv[x % DB] = mfma(gc[x], wb, dv[x % DB]);
+      dk[x % DB] = mfma(qc[x], db, dk[x % DB]);
+    }
+    order();
+    if constexpr (MODE == kCareful)
+      for (int32_t j = 0; j < BM; ++j)
+        add_nonfinite_row<T, DB, CPR>(dv, gt, j, row0 + j >= first && row0 + j < rows, half);
+  };
 
-  stage(0);
-  settle<T>(kf);
-  settle<T>(vf);
-  int32_t b = 0;
-  auto arrive = [&] {
-    wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
-    if (b + 1 < blocks) stage(b + 1);
-    return lds + (b & 1) * kStage;
+  auto buffer = [&](int32_t b) __attribute__((always_inline)) { return lds + b % kStages * kStage; };
+  // Before block b is finished its successor has arrived, and the buffer of its predecessor is
+  // free. Behind the last block the scores of whatever a buffer holds are formed and not used.
+  auto arrive = [&](int32_t b) __attribute__((always_inline)) {
+    if (b + 1 >= blocks) return;
+    wait_ring<kStages - 1, 2 * kLoads + 1>(blocks - 2 - b);
+    if (b + kStages - 1 < blocks) stage(b + kStages - 1);
   };
   const int32_t masked =
       wave_first < rows ? min(blocks, tail + max(0, wave_all - row_begin + BM - 1) / BM) : blocks;
-  for (; b < masked; ++b) {
-    const uint8_t* qt = arrive();
-    if (first_row(b) + BM > wave_first && wave_first < rows) block(Constant<true>(), qt, first_row(b));
-  }
-  for (; b < blocks; ++b) {
-    const uint8_t* qt = arrive();
-    block(Constant<false>(), qt, first_row(b));
+  auto walk = [&](auto mode) __attribute__((always_inline)) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.0f;
+    if (blocks <= 0) return;
+    for (int32_t i = 0; i < min(blocks, kStages - 1); ++i) stage(i);
+    settle<T>(kf);
+    settle<T>(vf);
+    wait_ring<kStages, 2 * kLoads + 1>(blocks - 1);
+    scores(buffer(0), s, dp, [](int) {});
+    read_stats(buffer(0));
+    int32_t b = 0;
+    for (; b < masked; ++b) {
+      arrive(b);
+      round(mode, buffer(b), buffer(b + 1), first_row(b));
+    }
+    for (; b < blocks; ++b) {
+      arrive(b);
+      round(Constant<kWhole>(), buffer(b), buffer(b + 1), first_row(b));
+    }
+  };
+  walk(Constant<kMasked>());
+  if (any_wave(any_nonfinite(dk) || any_nonfinite(dv), lds)) walk(Constant<kCareful>());
+
+  if (item.slot >= 0) {
+    float* part = p.part + ((int64_t)item.slot * p.Hkv + kvh) * 2 * kKeyTile * p.D +
+                  (32 * wave + (lane & 31)) * p.D;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t e = 32 * d + 8 * j + 4 * half;
+        if (!on || e >= (uint32_t)p.D) continue;
+        *reinterpret_cast<f32x4*>(part + e) =
+            (f32x4){dk[d][4 * j], dk[d][4 * j + 1], dk[d][4 * j + 2], dk[d][4 * j + 3]};
+        *reinterpret_cast<f32x4*>(part + kKeyTile * p.D + e) =
+            (f32x4){dv[d][4 * j], dv[d][4 * j + 1], dv[d][4 * j + 2], dv[d][4 * j + 3]};
+      }
+    return;
   }
 #pragma unroll
   for (int d = 0; d < DB; ++d)
@@ -413,27 +485,69 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_keys_kernel(const BwdParams p
   store_row<T, DB>(dv, dv_out + at_row * p.dv_stride + (int64_t)kvh * p.D, half, chunks, on);
 }
 
+// Adds the partial sums of a split tile, in the order of its rows: one workgroup per tile,
+// key/value head and 32 keys.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_bwd_join_kernel(const BwdParams p) {
+  const uint32_t index = div31(blockIdx.x, p.by_hkv);
+  const uint32_t kvh = blockIdx.x - index * p.Hkv;
+  if (!plan_matches(p) || (int32_t)index >= p.plan[6]) return;
+  const KeyJoin j = p.joins[index];
+  if (j.start < 0 || j.n <= 0 || j.start > p.T - j.n || j.key0 < 0 || j.slot < 0 || j.splits < 0 ||
+      j.slot + (int64_t)j.splits > p.units)
+    return;
+  const int32_t first = 32 * blockIdx.y, keys = min(32, j.n - j.key0 - first);
+  const int32_t groups = p.D >> 2, size = kKeyTile * p.D;
+  const int64_t step = (int64_t)p.Hkv * 2 * size;
+  for (int32_t i = threadIdx.x; i < 2 * keys * groups; i += 256) {
+    const int32_t which = i >= keys * groups, of = i - which * keys * groups;
+    const int32_t y = of / groups, e = 4 * (of - y * groups);
+    const float* part = p.part + ((int64_t)j.slot * p.Hkv + kvh) * 2 * size + which * size +
+                        (first + y) * p.D + e;
+    f32x4 x = {0, 0, 0, 0};
+    for (int32_t s0 = 0; s0 < j.splits; s0 += 8) {  // eight loads at a time
+      f32x4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        v[u] = *reinterpret_cast<const f32x4*>(part + min(s0 + u, j.splits - 1) * step);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (s0 + u >= j.splits) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] += v[u][c];
+      }
+    }
+    const float f = which ? 1.0f : p.scale;
+    T* row = static_cast<T*>(which ? p.dv : p.dk) +
+             (int64_t)(j.start + j.key0 + first + y) * (which ? p.dv_stride : p.dk_stride) +
+             (int64_t)kvh * p.D + e;
+    *reinterpret_cast<u32x2*>(row) =
+        (u32x2){narrow2<T>(x[0] * f, x[1] * f), narrow2<T>(x[2] * f, x[3] * f)};
+  }
+}
+
 template <typename T, int DB>
-int32_t launch(BwdParams p, hipStream_t s) {
-  const int4* rows = reinterpret_cast<const int4*>(p.plan + kHeader);
-  p.items = rows;
-  hipLaunchKernelGGL((attn_bwd_rows_kernel<T, DB>),
-                     dim3((unsigned)(row_items(p.T, p.num_seqs, p.G) * p.Hkv)), dim3(256), 0, s, p);
-  const int32_t st = launched();
+int32_t launch(const BwdParams& p, const PackedSizes& z, hipStream_t s) {
+  hipLaunchKernelGGL((attn_bwd_rows_kernel<T, DB>), dim3((unsigned)(z.rows * p.Hkv)), dim3(256), 0, s,
+                     p);
+  int32_t st = launched();
   if (st != ROPE_OK) return st;
-  p.items = rows + row_items(p.T, p.num_seqs, p.G);
-  hipLaunchKernelGGL((attn_bwd_keys_kernel<T, DB>),
-                     dim3((unsigned)(key_items(p.T, p.num_seqs) * p.Hkv)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_bwd_keys_kernel<T, DB>), dim3((unsigned)(z.keys * p.Hkv)), dim3(256), 0, s,
+                     p);
+  st = launched();
+  if (st != ROPE_OK) return st;
+  hipLaunchKernelGGL((attn_bwd_join_kernel<T>), dim3((unsigned)(z.joins * p.Hkv), kKeyTile / 32),
+                     dim3(256), 0, s, p);
   return launched();
 }
 
 template <typename T>
-int32_t launch_size(const BwdParams& p, hipStream_t s) {
+int32_t launch_size(const BwdParams& p, const PackedSizes& z, hipStream_t s) {
   switch ((p.D + 31) / 32) {
-    case 1: return launch<T, 1>(p, s);
-    case 2: return launch<T, 2>(p, s);
-    case 3: return launch<T, 3>(p, s);
-    default: return launch<T, 4>(p, s);
+    case 1: return launch<T, 1>(p, z, s);
+    case 2: return launch<T, 2>(p, z, s);
+    case 3: return launch<T, 3>(p, z, s);
+    default: return launch<T, 4>(p, z, s);
   }
 }
 
@@ -441,6 +555,12 @@ int32_t launch_size(const BwdParams& p, hipStream_t s) {
 }  // namespace attn
 
 using namespace attn;
+
+extern "C" int64_t attn_bwd_scratch_floats(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv,
+                                           int32_t D) {
+  if (!valid_batch(T, num_seqs, Hq, Hkv) || !valid_head_size(D) || D > 128) return -1;
+  return packed_sizes(T, num_seqs, Hq, Hkv).units * Hkv * 2 * kKeyTile * D + 2 * T * Hq;
+}
 
 extern "C" int32_t attn_bwd(const void* dout, const void* q, const void* k, const void* v,
                             const void* out, const float* lse, float* scratch, void* dq, void* dk,
@@ -466,21 +586,27 @@ extern "C" int32_t attn_bwd(const void* dout, const void* q, const void* k, cons
   const void* data[] = {dout, q, k, v, out, dq, dk, dv, plan};
   for (const void* x : data)
     if (!data_pointer(x)) return ROPE_EINVAL;
-  if (lse == nullptr || scratch == nullptr) return ROPE_EINVAL;
+  if (lse == nullptr || !data_pointer(scratch)) return ROPE_EINVAL;
   p.G = Hq / Hkv;
-  if (row_items(T, num_seqs, p.G) * Hkv > kMaxBlocks) return ROPE_EINVAL;
+  const PackedSizes z = packed_sizes(T, num_seqs, Hq, Hkv);
+  if (z.rows * Hkv > kMaxBlocks || z.keys * Hkv > kMaxBlocks) return ROPE_EINVAL;
   p.dout = dout;
   p.q = q;
   p.k = k;
   p.v = v;
   p.out = out;
   p.lse = lse;
-  p.lse2 = scratch;
-  p.delta = scratch + T * Hq;
+  p.part = scratch;
+  p.units = z.units;
+  p.lse2 = scratch + z.units * Hkv * 2 * kKeyTile * D;
+  p.delta = p.lse2 + T * Hq;
   p.dq = dq;
   p.dk = dk;
   p.dv = dv;
   p.plan = plan;
+  p.row_items = reinterpret_cast<const RowItem*>(plan + kHeader);
+  p.key_items = reinterpret_cast<const KeyItem*>(p.row_items + z.rows);
+  p.joins = reinterpret_cast<const KeyJoin*>(p.key_items + z.keys);
   p.T = (int32_t)T;
   p.Hq = Hq;
   p.Hkv = Hkv;
@@ -492,5 +618,5 @@ extern "C" int32_t attn_bwd(const void* dout, const void* q, const void* k, cons
   p.by_hkv = make_div31(Hkv);
   p.by_g = make_div31(p.G);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return dtype == ROPE_BF16 ? launch_size<__bf16>(p, s) : launch_size<_Float16>(p, s);
+  return dtype == ROPE_BF16 ? launch_size<__bf16>(p, z, s) : launch_size<_Float16>(p, z, s);
 }

@@ -25,10 +25,28 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-template <bool B>
+template <int N>
 struct Constant {
-  static constexpr bool value = B;
+  static constexpr int value = N;
 };
+
+// Whether x holds in any lane of the workgroup's four waves. lds: 16 bytes
+// that may be overwritten once every wave has come here.
+__device__ inline bool any_wave(bool x, uint8_t* lds) {
+  const uint32_t mine = __any(x);
+  uint32_t* flags = reinterpret_cast<uint32_t*>(lds);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) flags[threadIdx.x >> 6] = mine;
+  __syncthreads();
+  const uint32_t found =
+      __builtin_amdgcn_readfirstlane(flags[0] | flags[1] | flags[2] | flags[3]);
+  if (found) __syncthreads();  // read by all before it is overwritten
+  return found != 0;
+}
+
+// How a block of keys (rows) is treated: every pair is seen; some are hidden; some are hidden
+// and operands may not be finite.
+enum Mode : int { kWhole, kMasked, kCareful };
 
 template <typename T>
 struct Vec;
@@ -92,12 +110,17 @@ __device__ inline float half_sum(float x) {
 
 // ---- LDS tiles ---------------------------------------------------------------------------
 // A tile is a number of rows of CPR 16-byte chunks (8 elements). Chunk c of row r lies in
-// slot c ^ swizzle(r) of its row, so that neither way of reading a tile meets bank
-// conflicts: row-major reads (lanes 0..31 read one chunk of 32 rows) find 8 consecutive
-// rows in 8 different slots, and transposed reads (ds_read_b64_tr_b16: 16 lanes read 4
-// rows x 32 bytes, and each ends up with 4 rows of one column) find 4 consecutive rows in
-// 4 different pairs of slots.
-__device__ inline uint32_t swizzle(uint32_t r) { return (r & 3) << 1 | (r >> 2 & 1); }
+// slot c ^ swizzle(r) of its row. LDS serves 256 bytes (16 slots) a cycle, and neither way of
+// reading a tile may ask for one slot twice: row-major reads (16 lanes read one chunk of 16
+// rows) find 16 consecutive rows in 16 different slots, and transposed reads
+// (ds_read_b64_tr_b16: 32 lanes read 4 rows x 64 bytes) find 4 consecutive rows in 4 different
+// groups of 4 slots. Rows of 8 chunks lie two to a 256-byte line. (With both reads on 8 of
+// the 16 slots, the dK/dV pass of a packed batch took 446 us and not 402.)
+template <int CPR>
+__device__ inline uint32_t swizzle(uint32_t r) {
+  if constexpr (CPR == 8) return (r >> 1 & 1) << 2 | (r >> 2 & 3);
+  return (r & 3) << 2 | (r >> 2 & 3);
+}
 
 constexpr int keys_per_block(int db) { return db <= 4 ? 64 : 32; }
 constexpr int chunks_per_row(int db) { return db <= 2 ? 8 : db <= 4 ? 16 : 32; }
@@ -133,17 +156,31 @@ template <int LEFT>
 __device__ inline void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "n"(LEFT) : "memory");
 }
-// Waits until this wave's copies into LDS have landed, then for the other waves of the
-// workgroup (and so for theirs).
+// Waits until this wave's copies into LDS have landed but for the newest LEFT, then for the
+// other waves of the workgroup (and so for theirs). The barrier is the bare one: a
+// workgroup's fence would wait for every copy in flight.
+template <int LEFT>
 __device__ inline void wait_copies_and_sync() {
-  wait_copies<0>();
-  __syncthreads();
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(LEFT) : "memory");
+}
+
+// A ring of STAGES buffers that a workgroup fills block by block, COPIES copies a wave and
+// block: waits for a block while up to STAGES - 2 younger ones stay in flight. `younger`:
+// how many were begun. Behind it the buffer of the block before is free in every wave.
+template <int STAGES, int COPIES>
+__device__ inline void wait_ring(int32_t younger) {
+  static_assert(STAGES >= 2 && STAGES <= 6 && (STAGES - 2) * COPIES < 64, "vmcnt holds 6 bits");
+  if (STAGES >= 6 && younger >= 4) wait_copies_and_sync<STAGES >= 6 ? 4 * COPIES : 0>();
+  else if (STAGES >= 5 && younger >= 3) wait_copies_and_sync<STAGES >= 5 ? 3 * COPIES : 0>();
+  else if (STAGES >= 4 && younger >= 2) wait_copies_and_sync<STAGES >= 4 ? 2 * COPIES : 0>();
+  else if (STAGES >= 3 && younger >= 1) wait_copies_and_sync<STAGES >= 3 ? COPIES : 0>();
+  else wait_copies_and_sync<0>();
 }
 
 // Row-major operand: chunk c of row r.
 template <typename T, int CPR>
 __device__ inline x8<T> read_rows(const uint8_t* tile, uint32_t r, uint32_t c) {
-  return *reinterpret_cast<const x8<T>*>(tile + r * (CPR * 16) + ((c ^ swizzle(r)) << 4));
+  return *reinterpret_cast<const x8<T>*>(tile + r * (CPR * 16) + ((c ^ swizzle<CPR>(r)) << 4));
 }
 
 // Transposed operand A of a product over rows: lane l gets column 32 db + l % 32, rows
@@ -153,9 +190,9 @@ __device__ inline x8<T> read_columns(const uint8_t* tile, uint32_t r0, uint32_t 
   const uint32_t i = lane & 15;
   const uint32_t c = 4 * db + 2 * (lane >> 4 & 1) + (i >> 1 & 1);
   const uint32_t r = r0 + 4 * (lane >> 5) + (i >> 2);
-  const uint8_t* a = tile + r * (CPR * 16) + ((c ^ swizzle(r)) << 4) + 8 * (i & 1);
+  const uint8_t* a = tile + r * (CPR * 16) + ((c ^ swizzle<CPR>(r)) << 4) + 8 * (i & 1);
   const uint8_t* b =
-      tile + (r + 8) * (CPR * 16) + ((c ^ swizzle(r + 8)) << 4) + 8 * (i & 1);
+      tile + (r + 8) * (CPR * 16) + ((c ^ swizzle<CPR>(r + 8)) << 4) + 8 * (i & 1);
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a));
   const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(b));
   const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
@@ -163,17 +200,19 @@ __device__ inline x8<T> read_columns(const uint8_t* tile, uint32_t r0, uint32_t 
 }
 
 // ---- non-finite values in masked places --------------------------------------------------
-// A masked pair has weight 0, but 0 * inf and 0 * NaN are NaN: where a tile is partly
-// masked, its operand is looked over (nonfinite), and a tile that holds such values goes
-// through a slower path that multiplies cleaned operands and adds those values only where
-// they are seen.
-template <typename T>
-__device__ inline uint32_t nonfinite(x8<T> v) {  // bits 15 and 31: some element not finite
-  const u32x4 w = __builtin_bit_cast(u32x4, v);
-  uint32_t acc = 0;
+// A hidden pair has weight 0, but 0 * inf and 0 * NaN are NaN. The kernels take operands as
+// they are, look at the sums in the end, and where one is not finite, walk once more in
+// kCareful mode: partly masked blocks are then multiplied with cleaned operands, and the values
+// that are not finite are added only where they are seen. (Looking every masked block over
+// beforehand cost it two to three times its other vector instructions.)
+template <int DB>
+__device__ inline bool any_nonfinite(const f32x16 (&o)[DB]) {  // in this lane
+  float x = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) acc |= (w[j] & Vec<T>::kExpMask) + Vec<T>::kExpOne;
-  return acc & 0x80008000u;
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x = __builtin_fmaf(o[d][i], 0.0f, x);
+  return x != x;
 }
 template <typename T>
 __device__ inline x8<T> cleaned(x8<T> v) {  // non-finite elements as 0
@@ -233,7 +272,13 @@ inline bool valid_scale(double s) {  // positive and normal once it is single pr
 }
 inline int32_t launched() { return hipGetLastError() == hipSuccess ? ROPE_OK : ROPE_ELAUNCH; }
 
-// Items of a plan's two lists, as attn_plan_ints counts them.
+// Whether a plan was made for this call's sizes (its header says for which).
+template <typename P>
+__device__ inline bool plan_matches(const P& p) {
+  return p.plan[2] == p.T && p.plan[3] == p.G && p.plan[4] == p.num_seqs && p.plan[5] == p.Hkv;
+}
+
+// Bounds of the tiles of a batch, rows of no sequence among them (128 of those a tile).
 inline int64_t row_items(int64_t T, int32_t num_seqs, int32_t G) {
   return T * G / kRowTile + 2 * (int64_t)num_seqs + 3;
 }

@@ -4,6 +4,7 @@
 // (token-major, the group's heads minor), so that the heads of a group share every key and
 // value read and a tile spans few tokens, which wastes little above the diagonal and in
 // short sequences.
+#include "attn_packed.h"
 #include "attn_tile.h"
 
 namespace attn {
@@ -16,7 +17,7 @@ struct FwdParams {
   void* out;
   float* lse;
   const int32_t* plan;
-  const int4* items;
+  const RowItem* items;
   int64_t q_stride, k_stride, v_stride, out_stride;
   int32_t T, Hq, Hkv, G, D, num_seqs;
   float scale;  // times log2 e
@@ -33,17 +34,17 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
 
   const uint32_t index = div31(blockIdx.x, p.by_hkv);
   const uint32_t kvh = blockIdx.x - index * p.Hkv;
-  if (p.plan[2] != p.T || p.plan[3] != p.G || p.plan[4] != p.num_seqs) return;
+  if (!plan_matches(p)) return;
   if ((int32_t)index >= p.plan[0]) return;
-  const int4 item = p.items[index];
-  const int32_t start = item.x, n = item.y;
+  const RowItem item = p.items[index];
+  const int32_t start = item.start, n = item.n;
   if (start < 0 || n <= 0 || start > p.T - n) return;
   const uint32_t tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t chunks = p.D >> 3;
   T* out = static_cast<T*>(p.out);
 
-  if (item.w != 0) {  // rows of no sequence
+  if (item.gap != 0) {  // rows of no sequence
     if (!p.fill) return;
     const uint32_t per_token = p.G * chunks;
     for (uint32_t i = tid; i < n * per_token; i += 256) {
@@ -59,7 +60,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
   }
 
   const int32_t rows = n * p.G;
-  const int32_t row0 = item.z;
+  const int32_t row0 = item.row0;
   if (row0 < 0 || row0 >= rows) return;
   const int32_t row_end = min(row0 + kRowTile, rows);
   const int32_t wave_row0 = row0 + 32 * wave;
@@ -77,53 +78,67 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
   Tile t;
   load_row<T>(t.q, static_cast<const T*>(p.q) + (int64_t)(start + token) * p.q_stride +
                        (int64_t)head * p.D, half, chunks);
-  t.clear();
   clear_unused_chunks<CPR>(lds, 4 * BN, chunks);
 
   const T* k = static_cast<const T*>(p.k) + (int64_t)start * p.k_stride + (int64_t)kvh * p.D;
   const T* v = static_cast<const T*>(p.v) + (int64_t)start * p.v_stride + (int64_t)kvh * p.D;
   const int32_t blocks = (key_end + BN - 1) / BN;
 
-  auto stage = [&](int32_t b) {
-    const uint32_t kd = lds_address(lds) + (b & 1) * 2 * Tile::kTileBytes;
-    const uint32_t vd = kd + Tile::kTileBytes;
-    const int32_t key0 = b * BN;
-    const T* kb = k + (int64_t)key0 * p.k_stride;
-    const T* vb = v + (int64_t)key0 * p.v_stride;
-    const int32_t last = key_end - 1 - key0;
+  // Two buffers each for K and V. A block's V is begun with the block before, and the next
+  // block's K in the middle of that, as soon as its buffer has been read by every wave, so
+  // that either has a block and a half to arrive.
+  auto stage = [&](const T* base, int64_t stride, uint32_t tile, int32_t b) __attribute__((always_inline)) {
+    const uint32_t dst = lds_address(lds) + ((b & 1) * 2 + tile) * Tile::kTileBytes;
+    const int32_t key0 = b * BN, last = key_end - 1 - key0;
+    const T* from = base + (int64_t)key0 * stride;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const uint32_t c = i * 256 + tid;
-      const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle(r);
+      const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle<CPR>(r);
       const uint32_t at = (uint32_t)min((int32_t)r, last);
-      const uint32_t dst = (i * 256 + wave * 64) * 16;
-      if (chunk < chunks) {
-        copy_chunk_to_lds(kb + (at * (uint32_t)p.k_stride + 8 * chunk), kd + dst);
-        copy_chunk_to_lds(vb + (at * (uint32_t)p.v_stride + 8 * chunk), vd + dst);
-      }
+      if (chunk < chunks)
+        copy_chunk_to_lds(from + (at * (uint32_t)stride + 8 * chunk), dst + (i * 256 + wave * 64) * 16);
     }
   };
-
-  stage(0);
-  settle<T>(t.q);
-  // Two loops, so that neither body's registers are moved for the other's sake. Waves may be
-  // in different ones: each passes one barrier per block in either.
   const int32_t all = wave_end > 0 ? wave_all / BN : 0;  // blocks that every row of the wave sees
-  int32_t b = 0;
-  auto arrive = [&] {
-    wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
-    if (b + 1 < blocks) stage(b + 1);
-    return lds + (b & 1) * 2 * Tile::kTileBytes;
+  auto walk = [&](auto mode) __attribute__((always_inline)) {
+    t.clear();
+    int32_t b = 0;
+    auto begin = [&]() __attribute__((always_inline)) {  // K of block b has arrived, and V's other buffer is free
+      if (b + 1 < blocks) {
+        wait_copies_and_sync<2 * kLoads>();
+        stage(v, p.v_stride, 1, b + 1);
+      } else {
+        wait_copies_and_sync<kLoads>();
+      }
+      return lds + (b & 1) * 2 * Tile::kTileBytes;
+    };
+    auto middle = [&]() __attribute__((always_inline)) {  // V of block b has arrived, and its K has been read
+      if (b + 1 < blocks) wait_copies_and_sync<2 * kLoads>();
+      else wait_copies_and_sync<0>();
+      if (b + 2 < blocks) stage(k, p.k_stride, 0, b + 2);
+    };
+    stage(k, p.k_stride, 0, 0);
+    stage(v, p.v_stride, 1, 0);
+    if (blocks > 1) stage(k, p.k_stride, 0, 1);
+    settle<T>(t.q);
+    // Two loops, so that neither body's registers are moved for the other's sake. Waves may be
+    // in different ones: each passes the same two barriers per block in either.
+    for (; b < all; ++b) {
+      const uint8_t* kt = begin();
+      t.template block<kWhole>(kt, kt + Tile::kTileBytes, b * BN, seen, 0, p.scale, lane, middle);
+    }
+    for (; b < blocks; ++b) {
+      const uint8_t* kt = begin();
+      if (b * BN < wave_end)
+        t.template block<Mode(decltype(mode)::value)>(kt, kt + Tile::kTileBytes, b * BN, seen, 0, p.scale,
+                                                      lane, middle);
+      else
+        middle();
+    }
   };
-  for (; b < all; ++b) {
-    const uint8_t* kt = arrive();
-    t.template block<false>(kt, kt + Tile::kTileBytes, b * BN, seen, 0, p.scale, lane);
-  }
-  for (; b < blocks; ++b) {
-    const uint8_t* kt = arrive();
-    if (b * BN < wave_end)
-      t.template block<true>(kt, kt + Tile::kTileBytes, b * BN, seen, 0, p.scale, lane);
-  }
+  walk(Constant<kMasked>());
+  if (any_wave(any_nonfinite(t.o), lds)) walk(Constant<kCareful>());
 
   const float lse = t.finish();
   store_row<T, DB>(t.o, out + (int64_t)(start + token) * p.out_stride + (int64_t)head * p.D, half,
@@ -181,7 +196,7 @@ extern "C" int32_t attn_fwd(const void* q, const void* k, const void* v, void* o
   p.out = out;
   p.lse = lse;
   p.plan = plan;
-  p.items = reinterpret_cast<const int4*>(plan + kHeader);
+  p.items = reinterpret_cast<const RowItem*>(plan + kHeader);
   p.T = (int32_t)T;
   p.Hq = Hq;
   p.Hkv = Hkv;

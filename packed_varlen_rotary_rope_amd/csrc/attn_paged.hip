@@ -17,12 +17,13 @@
 // asynchronous copy two blocks ahead, a lane turns one key's page into its row's offset, and
 // the lanes that copy that row's chunks read it from there. Rows whose page is not a page of
 // the cache are hidden from every query.
+#include "attn_packed.h"
+#include "attn_plan.h"
 #include "attn_tile.h"
 
 namespace attn {
 namespace {
 
-constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 256;
 constexpr int kSplitKeys = 64;   // splits begin at multiples of this
 constexpr int kMinBlocks = 4;    // of 64 keys, in a split
@@ -66,43 +67,13 @@ struct PlanParams {
 };
 
 struct PlanShared {
-  int32_t scan[kPlanThreads];
-  int32_t a[kPlanThreads], n[kPlanThreads], end[kPlanThreads], held[kPlanThreads];
+  SeqChunk c;
+  int32_t held[kPlanThreads];
   int32_t tiles[kPlanThreads];  // inclusive running count
-  int32_t count[kBuckets];
+  int32_t count[kBuckets];      // items per bucket, then their places
   unsigned long long total;
-  int32_t units, joins, longest;
+  int32_t units, joins, items;
 };
-
-__device__ int32_t scan_max(int32_t x, int32_t* buf) {
-  const int t = threadIdx.x;
-  buf[t] = x;
-  __syncthreads();
-  for (int d = 1; d < kPlanThreads; d <<= 1) {
-    const int32_t y = t >= d ? max(buf[t], buf[t - d]) : buf[t];
-    __syncthreads();
-    buf[t] = y;
-    __syncthreads();
-  }
-  const int32_t r = buf[t];
-  __syncthreads();
-  return r;
-}
-__device__ int32_t scan_add(int32_t x, int32_t* buf) {
-  const int t = threadIdx.x;
-  buf[t] = x;
-  __syncthreads();
-  for (int d = 1; d < kPlanThreads; d <<= 1) {
-    const int32_t y = t >= d ? buf[t] + buf[t - d] : buf[t];
-    __syncthreads();
-    buf[t] = y;
-    __syncthreads();
-  }
-  const int32_t r = buf[t];
-  __syncthreads();
-  return r;
-}
-__device__ inline int32_t ceil_div(int32_t n, int32_t d) { return n / d + (n % d != 0); }
 
 // One workgroup, three passes over the tiles: the batch's key blocks, which give the length
 // of a split; the number of items by length; the items, the longest first. Slots and the
@@ -113,62 +84,39 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(const PlanPara
   if (t < kBuckets) s.count[t] = 0;
   if (t == 0) {
     s.total = 0;
-    s.units = s.joins = s.longest = 0;
+    s.units = s.joins = s.items = 0;
   }
   __syncthreads();
-  const int32_t slots = p.num_seqs + 1;  // slot 0 owns the rows before the first sequence
-  int32_t split_blocks = 1, n_items = 0;
+  int32_t split_blocks = 1;
   for (int pass = 0; pass < 3; ++pass) {
     int32_t carry = 0;
-    for (int32_t s0 = 0; s0 < slots; s0 += kPlanThreads) {
-      const int32_t slot = s0 + t;
-      int32_t next = slot < p.num_seqs ? p.cu[slot] : p.T;
-      next = next < 0 ? 0 : next > p.T ? p.T : next;
-      next = max(scan_max(next, s.scan), carry);
-      s.scan[t] = next;
-      __syncthreads();
-      const int32_t a = t > 0 ? s.scan[t - 1] : carry;
-      carry = s.scan[kPlanThreads - 1];
-      int32_t n = 0, held = 0;
-      if (slot > 0 && slot < slots) {
-        int32_t e = p.cu[slot];
-        e = e < a ? a : e > p.T ? p.T : e;
-        n = e - a;
-        held = p.kv_lens[slot - 1];
-      }
-      const int32_t end = slot < slots ? next : a;
-      s.a[t] = a;
-      s.n[t] = n;
-      s.end[t] = end;
-      s.held[t] = held;
-      __syncthreads();
-      s.tiles[t] = scan_add(ceil_div(n * p.G, kRowTile) + ceil_div(end - a - n, kKeyTile), s.scan);
+    for (int32_t s0 = 0; s0 <= p.num_seqs; s0 += kPlanThreads) {
+      load_sequences(s.c, p.cu, p.num_seqs, p.T, s0, &carry);
+      s.held[t] = s.c.n[t] > 0 ? p.kv_lens[s0 + t - 1] : 0;
+      s.tiles[t] = block_scan<AddOp>(ceil_div(s.c.n[t] * p.G, kRowTile) +
+                                         ceil_div(s.c.end[t] - s.c.a[t] - s.c.n[t], kKeyTile),
+                                     s.c.scan);
       __syncthreads();
       const int32_t tiles = s.tiles[kPlanThreads - 1];
       for (int32_t i = t; i < tiles; i += kPlanThreads) {
-        int lo = 0, hi = kPlanThreads - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (s.tiles[mid] > i) hi = mid;
-          else lo = mid + 1;
-        }
+        const int lo = find_slot(s.tiles, i);
         const int32_t j = i - (lo > 0 ? s.tiles[lo - 1] : 0);
-        const int32_t rows = s.n[lo] * p.G;
+        const int32_t rows = s.c.n[lo] * p.G;
         Item item;
-        item.q0 = s.a[lo];
+        item.q0 = s.c.a[lo];
         item.seq = s0 + lo - 1;
         item.slot = -1;
         int32_t blocks = 0, tile_rows = 0;
         if (j >= ceil_div(rows, kRowTile)) {  // rows of no sequence
-          item.q0 += s.n[lo] + (j - ceil_div(rows, kRowTile)) * kKeyTile;
-          item.rows = -min(s.end[lo] - item.q0, kKeyTile);
+          item.q0 += s.c.n[lo] + (j - ceil_div(rows, kRowTile)) * kKeyTile;
+          item.rows = -min(s.c.end[lo] - item.q0, kKeyTile);
           item.row0 = item.before = item.key0 = item.key_end = 0;
         } else {
           item.rows = rows;
           item.row0 = j * kRowTile;
           tile_rows = min(kRowTile, rows - item.row0);
           // a held length below the new tokens' leaves the first of them without a key
-          item.before = (int32_t)max((int64_t)s.held[lo] - s.n[lo], (int64_t)INT32_MIN);
+          item.before = (int32_t)max((int64_t)s.held[lo] - s.c.n[lo], (int64_t)INT32_MIN);
           item.key0 = 0;
           const int64_t last = (int64_t)item.before + (item.row0 + tile_rows - 1) / p.G;
           item.key_end = last < 0 ? 0 : (int32_t)min(last + 1, (int64_t)kMostKeys);
@@ -180,9 +128,11 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(const PlanPara
         }
         const int32_t k = max(1, ceil_div(blocks, split_blocks));
         const int32_t len = ceil_div(blocks, k);
-        const int32_t bucket = kBuckets - 1 - (int32_t)((int64_t)len * (kBuckets - 1) / split_blocks);
-        const int32_t at = atomicAdd(&s.count[bucket], k);
-        if (pass == 1) continue;
+        const int32_t at = atomicAdd(&s.count[bucket_of<kBuckets>(len, split_blocks)], k);
+        if (pass == 1) {
+          atomicAdd(&s.items, k);
+          continue;
+        }
         if (k > 1) {
           const int32_t units = ceil_div(tile_rows, 32);
           const int32_t slot0 = atomicAdd(&s.units, k * units);
@@ -203,23 +153,14 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(const PlanPara
       }
       __syncthreads();
     }
-    __syncthreads();
     if (pass == 0) {
       const unsigned long long want = (s.total * p.Hkv + kTarget - 1) / kTarget;
       split_blocks = want < kMinBlocks ? kMinBlocks : want > INT32_MAX / 64 ? INT32_MAX / 64 : (int32_t)want;
     }
-    if (pass == 1) {  // counts to first places
-      const int32_t own = t < kBuckets ? s.count[t] : 0;
-      const int32_t incl = scan_add(own, s.scan);
-      s.scan[t] = incl;
-      __syncthreads();
-      n_items = s.scan[kPlanThreads - 1];
-      if (t < kBuckets) s.count[t] = incl - own;
-      __syncthreads();
-    }
+    if (pass == 1) counts_to_places<kBuckets>(s.count, s.c.scan);
   }
   if (t == 0) {
-    p.header[0] = n_items < p.sizes.items ? n_items : (int32_t)p.sizes.items;
+    p.header[0] = s.items < p.sizes.items ? s.items : (int32_t)p.sizes.items;
     p.header[1] = s.joins < p.sizes.joins ? s.joins : (int32_t)p.sizes.joins;
     p.header[2] = p.T;
     p.header[3] = p.G;
@@ -250,10 +191,6 @@ struct PagedParams {
   int32_t fill;
   Div31 by_hkv, by_g, by_page;
 };
-
-__device__ inline bool plan_matches(const PagedParams& p) {
-  return p.plan[2] == p.T && p.plan[3] == p.G && p.plan[4] == p.num_seqs && p.plan[5] == p.Hkv;
-}
 
 // A wave's view of the cache: rows of key blocks of BN keys, by way of the block table.
 template <int BN, int CPR>
@@ -336,7 +273,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   const int64_t most = min((int64_t)p.max_pages * p.page_size, (int64_t)kMostKeys);
   const int32_t key_end = (int32_t)min((int64_t)item.key_end, most);
   // visible keys of a token, 0 for none; within this split
-  auto seen_by = [&](int32_t tok) {
+  auto seen_by = [&](int32_t tok) __attribute__((always_inline)) {
     const int64_t s = (int64_t)item.before + tok + 1;
     return (int32_t)min(max(s, (int64_t)0), (int64_t)key_end);
   };
@@ -359,16 +296,15 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   if (!small) {
     FwdTile<T, DB, BN> t;
     load_row<T>(t.q, q_row, half, chunks);
-    t.clear();
     const int32_t blocks = keys > 0 ? (keys + BN - 1) / BN : 0;
     const PagedKeys<BN, CPR> src{table, pages[wave], offsets[wave], key_end};
     constexpr int kLoads = BN * CPR / 256;
-    auto stage = [&](int32_t b) {
+    auto stage = [&](int32_t b) __attribute__((always_inline)) {
       const uint32_t kd = lds_address(lds) + (b & 1) * 2 * kTileBytes;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const uint32_t c = i * 256 + tid;
-        const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle(r);
+        const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle<CPR>(r);
         const uint32_t dst = kd + (i * 256 + wave * 64) * 16;
         if (chunk < chunks) {
           copy_chunk_to_lds(src.row(kb, b & 1, r) + 16 * chunk, dst);
@@ -376,40 +312,46 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
         }
       }
     };
-    uint64_t hidden = 0, hidden_next = 0;
-    if (blocks > 0) {
-      src.fetch_pages(p, item.key0, 0, lane);
-      wait_copies<0>();
-      hidden_next = src.find_rows(p, item.key0, 0, lane);
-      src.fetch_pages(p, item.key0 + BN, 1, lane);
-      stage(0);
-    }
-    settle<T>(t.q);
     // Two loops, so that neither body's registers are moved for the other's sake; the first
     // ends at the first block that is not wholly seen, or that has keys on no page.
     const int32_t all = wave_end > 0 ? max(0, wave_all - item.key0) / BN : 0;
-    int32_t b = 0;
-    auto arrive = [&] {
-      const int32_t key0 = item.key0 + b * BN;
-      wait_copies_and_sync();  // block b has arrived, and its buffer's neighbour is free
-      hidden = hidden_next;
-      if (b + 1 < blocks) {
-        hidden_next = src.find_rows(p, key0 + BN, (b + 1) & 1, lane);
-        src.fetch_pages(p, key0 + 2 * BN, b & 1, lane);
-        stage(b + 1);
+    auto walk = [&](auto mode) __attribute__((always_inline)) {
+      t.clear();
+      uint64_t hidden = 0, hidden_next = 0;
+      if (blocks > 0) {
+        src.fetch_pages(p, item.key0, 0, lane);
+        wait_copies<0>();
+        hidden_next = src.find_rows(p, item.key0, 0, lane);
+        src.fetch_pages(p, item.key0 + BN, 1, lane);
+        stage(0);
       }
-      return lds + (b & 1) * 2 * kTileBytes;
+      settle<T>(t.q);
+      int32_t b = 0;
+      auto arrive = [&]() __attribute__((always_inline)) {
+        const int32_t key0 = item.key0 + b * BN;
+        wait_copies_and_sync<0>();  // block b has arrived, and its buffer's neighbour is free
+        hidden = hidden_next;
+        if (b + 1 < blocks) {
+          hidden_next = src.find_rows(p, key0 + BN, (b + 1) & 1, lane);
+          src.fetch_pages(p, key0 + 2 * BN, b & 1, lane);
+          stage(b + 1);
+        }
+        return lds + (b & 1) * 2 * kTileBytes;
+      };
+      for (; b < all && hidden_next == 0; ++b) {
+        const uint8_t* kt = arrive();
+        t.template block<kWhole>(kt, kt + kTileBytes, item.key0 + b * BN, seen, 0, p.scale, lane, [] {});
+      }
+      for (; b < blocks; ++b) {
+        const uint8_t* kt = arrive();
+        const int32_t key0 = item.key0 + b * BN;
+        if (key0 < wave_end)
+          t.template block<Mode(decltype(mode)::value)>(kt, kt + kTileBytes, key0, seen, hidden, p.scale,
+                                                        lane, [] {});
+      }
     };
-    for (; b < all && hidden_next == 0; ++b) {
-      const uint8_t* kt = arrive();
-      t.template block<false>(kt, kt + kTileBytes, item.key0 + b * BN, seen, 0, p.scale, lane);
-    }
-    for (; b < blocks; ++b) {
-      const uint8_t* kt = arrive();
-      const int32_t key0 = item.key0 + b * BN;
-      if (key0 < wave_end)
-        t.template block<true>(kt, kt + kTileBytes, key0, seen, hidden, p.scale, lane);
-    }
+    walk(Constant<kMasked>());
+    if (any_wave(any_nonfinite(t.o), lds)) walk(Constant<kCareful>());
     if (item.slot < 0) {
       const float lse = t.finish();
       store_row<T, DB>(t.o, out_row, half, chunks, on);
@@ -442,34 +384,24 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   constexpr int kLoads = 32 * CPR / 64;
   FwdTile<T, DB, 32> t;
   load_row<T>(t.q, q_row, half, chunks);
-  t.clear();
   {
     const PagedKeys<32, CPR> src{table, pages[wave], offsets[wave], key_end};
     const uint8_t* kt = lds + wave * kTileBytes;
     const uint8_t* vt = kOneBuffer ? kt : kt + kSmallTile;
     const int32_t blocks = keys > 0 ? ((keys + 31) / 32 - (int32_t)wave + 3) / 4 : 0;
     const int32_t first = item.key0 + 32 * wave;
-    auto stage = [&](const uint8_t* base, const uint8_t* tile, int parity) {
+    auto stage = [&](const uint8_t* base, const uint8_t* tile, int parity) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const uint32_t c = i * 64 + lane;
-        const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle(r);
+        const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle<CPR>(r);
         if (chunk < chunks)
           copy_chunk_to_lds(src.row(base, parity, r) + 16 * chunk, lds_address(tile) + i * 1024);
       }
     };
     uint64_t hidden = 0, hidden_next = 0;
-    if (blocks > 0) {
-      src.fetch_pages(p, first, 0, lane);
-      settle<T>(t.q);
-      wait_copies<0>();
-      hidden_next = src.find_rows(p, first, 0, lane);
-      src.fetch_pages(p, first + 128, 1, lane);
-      stage(kb, kt, 0);
-      if (!kOneBuffer) stage(vb, vt, 0);
-    }
-    auto round = [&](auto masked, int32_t b) {
-      constexpr bool MASKED = decltype(masked)::value;
+    auto round = [&](auto mode, int32_t b) __attribute__((always_inline)) {
+      constexpr Mode MODE = Mode(decltype(mode)::value);
       const int32_t key0 = first + 128 * b;
       const bool more = b + 1 < blocks;
       hidden = hidden_next;
@@ -484,10 +416,10 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
         src.fetch_pages(p, key0 + 256, b & 1, lane);
         if (!kOneBuffer) stage(kb, kt, (b + 1) & 1);
       }
-      t.template weights<MASKED>(s, w, key0, seen, hidden, p.scale, lane);
+      t.template weights<MODE>(s, w, key0, seen, hidden, p.scale, lane);
       if (more && !kOneBuffer) wait_copies<kLoads + 1>();
       else wait_copies<0>();
-      t.template accumulate<MASKED>(w, vt, key0, seen, hidden, lane);
+      t.template accumulate<MODE>(w, vt, key0, seen, hidden, lane);
       reads_done();
       if (more) {
         if (kOneBuffer) stage(kb, kt, (b + 1) & 1);
@@ -497,9 +429,22 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
     // blocks that every row sees whole, then the others (two loops, as above)
     const int32_t whole = max(0, wave_all - first) / 32;
     const int32_t all = wave_all >= first + 32 ? min(blocks, (whole - 1) / 4 + 1) : 0;
-    int32_t b = 0;
-    for (; b < all && hidden_next == 0; ++b) round(Constant<false>(), b);
-    for (; b < blocks; ++b) round(Constant<true>(), b);
+    auto walk = [&](auto mode) __attribute__((always_inline)) {
+      t.clear();
+      if (blocks <= 0) return;
+      src.fetch_pages(p, first, 0, lane);
+      settle<T>(t.q);
+      wait_copies<0>();
+      hidden_next = src.find_rows(p, first, 0, lane);
+      src.fetch_pages(p, first + 128, 1, lane);
+      stage(kb, kt, 0);
+      if (!kOneBuffer) stage(vb, vt, 0);
+      int32_t b = 0;
+      for (; b < all && hidden_next == 0; ++b) round(Constant<kWhole>(), b);
+      for (; b < blocks; ++b) round(mode, b);
+    };
+    walk(Constant<kMasked>());
+    if (__any(any_nonfinite(t.o))) walk(Constant<kCareful>());  // this wave alone
   }
 
   // Join the waves: O scaled to the common maximum goes to LDS four blocks of columns at a

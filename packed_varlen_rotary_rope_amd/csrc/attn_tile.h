@@ -78,7 +78,7 @@ __device__ inline void add_nonfinite_row(f32x16 (&o)[DB], const uint8_t* tile, u
     for (int i = 0; i < 16; ++i) {
       const uint32_t e = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
       const T* at = reinterpret_cast<const T*>(tile + j * (CPR * 16) +
-                                               (((e >> 3) ^ swizzle(j)) << 4)) + (e & 7);
+                                               (((e >> 3) ^ swizzle<CPR>(j)) << 4)) + (e & 7);
       const float v = (float)*at;
       if (on && !(__builtin_fabsf(v) < __builtin_inff())) o[d][i] += v;
     }
@@ -119,12 +119,12 @@ struct FwdTile {
   }
 
   // Scores to weights, narrowed; m, l and o follow. Keys key0 + j at or behind `seen` (as a
-  // count from key 0) are hidden where MASKED, and those whose bit of `hidden` is set.
-  template <bool MASKED>
+  // count from key 0) are hidden unless kWhole, and those whose bit of `hidden` is set.
+  template <Mode MODE>
   __device__ void weights(f32x16 (&s)[KB], x8<T> (&p)[2 * KB], int32_t key0, int32_t seen,
                           uint64_t hidden, float scale, uint32_t lane) {
     const uint32_t half = lane >> 5;
-    if constexpr (MASKED) {
+    if constexpr (MODE != kWhole) {
 #pragma unroll
       for (int b = 0; b < KB; ++b)
 #pragma unroll
@@ -167,37 +167,33 @@ struct FwdTile {
   }
 
   // O^T += V^T P^T.
-  template <bool MASKED>
+  template <Mode MODE>
   __device__ void accumulate(const x8<T> (&p)[2 * KB], const uint8_t* vt, int32_t key0, int32_t seen,
                              uint64_t hidden, uint32_t lane) {
-    uint32_t bad = 0;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int t = 0; t < 2 * KB; ++t) {
         x8<T> v = read_columns<T, CPR>(vt, 16 * t, d, lane);
-        if constexpr (MASKED) {
-          bad |= nonfinite<T>(v);
-          v = cleaned<T>(v);
-        }
+        if constexpr (MODE == kCareful) v = cleaned<T>(v);
         o[d] = mfma(v, p[t], o[d]);
       }
-    if constexpr (MASKED) {
-      // what is infinite or NaN stays so whatever its weight
-      if (__any(bad != 0))
-        for (int32_t j = 0; j < BN; ++j)
-          add_nonfinite_row<T, DB, CPR>(o, vt, j, key0 + j < seen && !(hidden >> j & 1), lane >> 5);
-    }
+    // what is infinite or NaN stays so whatever its weight
+    if constexpr (MODE == kCareful)
+      for (int32_t j = 0; j < BN; ++j)
+        add_nonfinite_row<T, DB, CPR>(o, vt, j, key0 + j < seen && !(hidden >> j & 1), lane >> 5);
   }
 
-  template <bool MASKED>
+  // One block; `middle` is called once its scores are formed, before V is read.
+  template <Mode MODE, typename M>
   __device__ void block(const uint8_t* kt, const uint8_t* vt, int32_t key0, int32_t seen,
-                        uint64_t hidden, float scale, uint32_t lane) {
+                        uint64_t hidden, float scale, uint32_t lane, M middle) {
     f32x16 s[KB];
     x8<T> p[2 * KB];
     scores(s, kt, lane);
-    weights<MASKED>(s, p, key0, seen, hidden, scale, lane);
-    accumulate<MASKED>(p, vt, key0, seen, hidden, lane);
+    middle();
+    weights<MODE>(s, p, key0, seen, hidden, scale, lane);
+    accumulate<MODE>(p, vt, key0, seen, hidden, lane);
   }
 
   // Normalizes O and returns the row's log-sum-exp.
@@ -220,7 +216,7 @@ __device__ inline void clear_unused_chunks(uint8_t* tiles, uint32_t rows, uint32
   for (uint32_t i = threadIdx.x; i < rows * CPR; i += blockDim.x) {
     const uint32_t r = i / CPR, c = i % CPR;
     if (c >= chunks)
-      *reinterpret_cast<u32x4*>(tiles + r * (CPR * 16) + ((c ^ swizzle(r)) << 4)) =
+      *reinterpret_cast<u32x4*>(tiles + r * (CPR * 16) + ((c ^ swizzle<CPR>(r)) << 4)) =
           (u32x4){0, 0, 0, 0};
   }
 }
