@@ -36,29 +36,14 @@ struct BwdParams {
   void* dv;
   const int32_t* plan;
   const RowItem* row_items;
-  const KeyItem* key_items;
-  const KeyJoin* joins;
-  float* part;    // scratch: [slot][Hkv][dK, dV][128][D], of tiles whose rows are split
-  int64_t units;  // its slots
+  const KeyTile* key_tiles;
+  float* part;  // scratch: [2 shares][dK, dV][128][D], of tiles that are cut
   int64_t dout_stride, q_stride, k_stride, v_stride, out_stride, dq_stride, dk_stride, dv_stride;
   int32_t T, Hq, Hkv, G, D, num_seqs;
   float scale, scale2;  // scale2: times log2 e
   int32_t fill;
   Div31 by_hkv, by_g;
 };
-
-// The item of this workgroup, or n = 0 where there is none.
-template <typename I>
-__device__ inline I find_item(const BwdParams& p, const I* items, int list, uint32_t* kvh) {
-  const uint32_t index = div31(blockIdx.x, p.by_hkv);
-  *kvh = blockIdx.x - index * p.Hkv;
-  I item;
-  item.n = 0;
-  if (!plan_matches(p) || (int32_t)index >= p.plan[list]) return item;
-  item = items[index];
-  if (item.start < 0 || item.n <= 0 || item.start > p.T - item.n) item.n = 0;
-  return item;
-}
 
 // Zeros to `n` rows of `heads` heads from head0.
 template <typename T>
@@ -80,9 +65,12 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * 2 * kTileBytes];
 
   uint32_t kvh;
-  const RowItem item = find_item(p, p.row_items, 0, &kvh);
+  const uint32_t index = div31(blockIdx.x, p.by_hkv);
+  kvh = blockIdx.x - index * p.Hkv;
+  if (!plan_matches(p) || (int32_t)index >= p.plan[0]) return;
+  const RowItem item = p.row_items[index];
   const int32_t start = item.start, n = item.n;
-  if (n == 0) return;
+  if (start < 0 || n <= 0 || start > p.T - n) return;
   const uint32_t tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t chunks = p.D >> 3;
@@ -133,35 +121,47 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   const T* k = static_cast<const T*>(p.k) + (int64_t)start * p.k_stride + (int64_t)kvh * p.D;
   const T* v = static_cast<const T*>(p.v) + (int64_t)start * p.v_stride + (int64_t)kvh * p.D;
   const int32_t blocks = (key_end + BN - 1) / BN;
-  auto stage = [&](int32_t b) __attribute__((always_inline)) {
-    const uint32_t kd = lds_address(lds) + b % kStages * 2 * kTileBytes;
-    const uint32_t vd = kd + kTileBytes;
-    const int32_t key0 = b * BN;
-    const T* kb = k + (int64_t)key0 * p.k_stride;
-    const T* vb = v + (int64_t)key0 * p.v_stride;
-    const int32_t last = key_end - 1 - key0;
+  uint64_t lanes[kLoads];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint32_t c = i * 256 + tid;
-      const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle<CPR>(r);
-      const uint32_t at = (uint32_t)min((int32_t)r, last);
-      const uint32_t dst = (i * 256 + wave * 64) * 16;
-      if (chunk < chunks) {
-        copy_chunk_to_lds(kb + (at * (uint32_t)p.k_stride + 8 * chunk), kd + dst);
-        copy_chunk_to_lds(vb + (at * (uint32_t)p.v_stride + 8 * chunk), vd + dst);
-      }
-    }
+  for (int i = 0; i < kLoads; ++i) lanes[i] = __ballot(chunk_of<CPR, 256>(i, tid) < chunks);
+  constexpr int kPieces = 2 * kLoads, kPerStep = (kPieces + KS - 1) / KS;
+  auto piece = [&](int32_t b, int x) __attribute__((always_inline)) {  // x-th copy of block b
+    const int i = x / 2;
+    const int64_t stride = x % 2 ? p.v_stride : p.k_stride;
+    const int32_t key0 = min(b, blocks - 1) * BN;  // behind the last block, into buffers not used
+    const uint32_t at = min((int32_t)row_of<CPR, 256>(i, tid), key_end - 1 - key0);
+    const T* from = (x % 2 ? v : k) + (int64_t)key0 * stride;
+    copy_chunk_to_lds(from + (at * (uint32_t)stride + 8 * chunk_of<CPR, 256>(i, tid)),
+                      lds_address(lds) + (b % kStages * 2 + x % 2) * kTileBytes + (i * 256 + wave * 64) * 16,
+                      lanes[i]);
   };
 
-  // P and dP of 32 keys; what is hidden gets P = dP = 0.
+  int32_t b = 0;
+  // P and dP of the 32 keys of block b, in KS steps, which begin the copies of the block
+  // kStages - 1 further; what is hidden gets P = dP = 0.
+  auto next = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int x = s * kPerStep; x < (s + 1) * kPerStep && x < kPieces; ++x) piece(b + kStages - 1, x);
+  };
   auto weights = [&](auto mode, const uint8_t* kt, int32_t key0, f32x16& s, f32x16& dp) __attribute__((always_inline)) {
+    x8<T> kr[KS], vr[KS];
+    auto read = [&](int t) __attribute__((always_inline)) {
+      kr[t] = read_rows<T, CPR>(kt, lane & 31, 2 * t + half);
+      vr[t] = read_rows<T, CPR>(kt + kTileBytes, lane & 31, 2 * t + half);
+    };
+    read(0);
+    read(1);
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
-      s = mfma(read_rows<T, CPR>(kt, lane & 31, 2 * t + half), qf[t], s);
-      dp = mfma(read_rows<T, CPR>(kt + kTileBytes, lane & 31, 2 * t + half), df[t], dp);
+      step();
+      if (t + 2 < KS) read(t + 2);
+      next(t);
+      s = mfma(kr[t], qf[t], s);
+      dp = mfma(vr[t], df[t], dp);
     }
+    step();
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2));
@@ -182,27 +182,39 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
         if (key >= seen) s[i] = 0.0f;
       }
     }
+    x8<T> kc[2 * DB];
+    auto read = [&](int x) __attribute__((always_inline)) {
+      kc[x] = read_columns<T, CPR>(kt, 16 * (x / DB), x % DB, lane);
+    };
+    read(0);
+    read(1);
+    const x8<T> ds[2] = {narrow8<T>(s, 0), narrow8<T>(s, 1)};
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const x8<T> ds = narrow8<T>(s, t);
-#pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        x8<T> kc = read_columns<T, CPR>(kt, 16 * t, d, lane);
-        // a key that is seen and not finite has made dS NaN or 0 already
-        if constexpr (decltype(mode)::value == kCareful) kc = cleaned<T>(kc);
-        dq[d] = mfma(kc, ds, dq[d]);
+    for (int x = 0; x < 2 * DB; ++x) {
+      if (x % 2 == 0) {
+        step();
+        if (x + 2 < 2 * DB) read(x + 2);
+        if (x + 3 < 2 * DB) read(x + 3);
       }
+      // a key that is seen and not finite has made dS NaN or 0 already
+      if constexpr (decltype(mode)::value == kCareful) kc[x] = cleaned<T>(kc[x]);
+      dq[x % DB] = mfma(kc[x], ds[x / DB], dq[x % DB]);
     }
+    step();
   };
 
-  int32_t b = 0;
   auto first_stages = [&]() __attribute__((always_inline)) {
-    for (int32_t i = 0; i < min(blocks, kStages - 1); ++i) stage(i);
+    for (int32_t i = 0; i < kStages - 1; ++i)
+#pragma unroll
+      for (int x = 0; x < kPieces; ++x) piece(i, x);
   };
-  auto arrive = [&]() __attribute__((always_inline)) {
-    wait_ring<kStages, 2 * kLoads>(blocks - 1 - b);
-    if (b + kStages - 1 < blocks) stage(b + kStages - 1);
+  auto arrive = [&]() __attribute__((always_inline)) {  // block b; the buffer before it is free
+    wait_copies_and_sync<(kStages - 2) * kPieces>();
     return lds + b % kStages * 2 * kTileBytes;
+  };
+  auto skip = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) next(s);
   };
   first_stages();
   settle<T>(qf);
@@ -213,14 +225,17 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
     float sum = 0.0f;
     for (; b < blocks; ++b) {
       const uint8_t* kt = arrive();
-      if (b * BN >= wave_end) continue;
+      if (b * BN >= wave_end) {
+        skip();
+        continue;
+      }
       f32x16 s, dp;
       weights(Constant<kMasked>(), kt, b * BN, s, dp);
 #pragma unroll
       for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(s[i], dp[i], sum);
     }
     delta = half_sum(sum);
-    __syncthreads();  // the last block has been read
+    wait_copies_and_sync<0>();  // the last block has been read, and what came behind it is there
     b = 0;
     first_stages();
   }
@@ -242,7 +257,9 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
     for (; b < blocks; ++b) {
       const uint8_t* kt = arrive();
       if (b * BN < wave_end) block(mode, kt, b * BN);
+      else skip();
     }
+    wait_copies<0>();
   };
   walk(Constant<kMasked>());
   if (any_wave(any_nonfinite(dq), lds)) {
@@ -258,31 +275,104 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
                    chunks, on);
 }
 
+// ---- dK and dV -------------------------------------------------------------------------------
+//
+// The work of all tiles and key/value heads, laid end to end head by head, is cut into equal
+// shares, one for each workgroup that fits the chip, wherever the cuts fall: with the tiles of
+// one long sequence of few key/value heads as they are, most of the chip would wait for the
+// first of them. A workgroup walks its share tile by tile; a tile that is cut leaves partial
+// sums, which attn_bwd_join_kernel adds in the order of its rows.
+
+// A place in that work: tile `index` of head `kvh`, `in_tile` units from its start.
+struct Place {
+  int64_t units;  // of all tiles of a head
+  int64_t share;  // of a workgroup
+  int64_t total;
+  int32_t tiles;
+};
+__device__ inline Place place_of(const BwdParams& p, int32_t shares) {
+  Place w;
+  w.units = *reinterpret_cast<const int64_t*>(p.plan + 6);
+  w.tiles = p.plan[1];
+  w.total = w.units * p.Hkv;
+  w.share = (w.total + shares - 1) / shares;
+  if (w.share < kMinUnits) w.share = kMinUnits;
+  return w;
+}
+// The last tile whose work begins at or before `pos` (0 <= pos < units), by 64 probes a step.
+__device__ inline int32_t find_tile(const BwdParams& p, int32_t tiles, int64_t pos) {
+  const int32_t lane = threadIdx.x & 63;
+  int32_t lo = 0, n = tiles;  // the answer is in lo .. lo + n - 1
+  while (n > 1) {
+    const int32_t step = (n + 63) / 64, at = lane * step;
+    const uint64_t yes = __ballot(at < n && p.key_tiles[lo + at].first <= pos);
+    const int32_t last = 63 - __builtin_clzll(yes | 1);
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+__device__ inline int64_t end_of_tile(const BwdParams& p, const Place& w, int32_t tile) {
+  return tile + 1 < w.tiles ? p.key_tiles[tile + 1].first : w.units;
+}
+
 template <typename T, int DB>
-__global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(const BwdParams p) {
+__global__ __launch_bounds__(256, DB <= 1 ? 2 : 1) void attn_bwd_keys_kernel(const BwdParams p) {
   constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BM = kRowBlock;
   constexpr int kTileBytes = BM * CPR * 16, kLoads = BM * CPR / 256;
   constexpr int kStatBytes = 2 * BM * 4, kStage = 2 * kTileBytes + kStatBytes, kStages = 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t flags[16];
 
-  uint32_t kvh;
-  const KeyItem item = find_item(p, p.key_items, 1, &kvh);
-  const int32_t start = item.start, n = item.n;
-  if (n == 0) return;
+  if (!plan_matches(p)) return;
+  const Place work = place_of(p, gridDim.x);
+  // workgroup i runs on die i % 8: neighbouring shares, which read the same rows, on one die
+  const int32_t share = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  int64_t left = min(work.share, work.total - share * work.share);
+  if (left <= 0 || work.tiles <= 0) return;
+  uint32_t kvh = (uint32_t)(share * work.share / work.units);
+  int64_t pos = share * work.share - kvh * work.units;
+  int32_t index = find_tile(p, work.tiles, pos);
+
   const uint32_t tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t chunks = p.D >> 3;
+  for (int b = 0; b < kStages; ++b) clear_unused_chunks<CPR>(lds + b * kStage, 2 * BM, chunks);
+  uint64_t lanes[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) lanes[i] = __ballot(chunk_of<CPR, 256>(i, tid) < chunks);
+  // a row block further is dt tokens and dh heads on, one token more where the heads wrap
+  const uint32_t dt = div31(BM, p.by_g), dh = BM - dt * p.G;
+  const int64_t q_step = dt * p.q_stride + (int64_t)dh * p.D, q_wrap = p.q_stride - (int64_t)p.G * p.D;
+  const int64_t g_step = dt * p.dout_stride + (int64_t)dh * p.D, g_wrap = p.dout_stride - (int64_t)p.G * p.D;
+  const int64_t stat_step = (int64_t)dt * p.Hq + dh, stat_wrap = p.Hq - p.G;
+
+  for (; left > 0; ++index) {
+  if (pos >= work.units) {
+    pos = 0;
+    index = 0;
+    ++kvh;
+  }
+  const KeyTile tile = p.key_tiles[index];
+  const int64_t tile_end = end_of_tile(p, work, index);
+  const int64_t from = pos - tile.first, to = min(tile_end - tile.first, from + left);
+  if (to <= from) return;  // no plan of this batch's
+  const bool whole = from == 0 && to == tile_end - tile.first;
+  left -= to - from;
+  pos += to - from;
+
+  const int32_t start = tile.start, n = tile.n, key0 = tile.key0;
+  if (start < 0 || n <= 0 || start > p.T - n) continue;
   T* dk_out = static_cast<T*>(p.dk);
   T* dv_out = static_cast<T*>(p.dv);
-  if (item.gap != 0) {
+  if (tile.gap != 0) {
     if (p.fill) {
       clear_rows(dk_out, start, n, p.dk_stride, kvh, 1, chunks);
       clear_rows(dv_out, start, n, p.dv_stride, kvh, 1, chunks);
     }
-    return;
+    continue;
   }
-  const int32_t key0 = item.key0;
-  if (key0 < 0 || key0 >= n) return;
+  if (key0 < 0 || key0 >= n) continue;
 
   const int32_t rows = n * p.G;
   const int32_t wave_key0 = key0 + 32 * wave;
@@ -290,9 +380,7 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
   const bool on = key < n;
   const int32_t at_key = on ? key : n - 1;
   const int32_t first = at_key * p.G;  // the first row that sees this lane's key
-  // rows that see some key, and every key, of the wave
-  const int32_t wave_first = wave_key0 < n ? wave_key0 * p.G : rows;
-  const int32_t wave_all = min(wave_key0 + 31, n - 1) * p.G;
+  const int32_t wave_all = wave_key0 < n ? min(wave_key0 + 31, n - 1) * p.G : rows;  // the wave's every key
 
   x8<T> kf[KS], vf[KS];
   load_row<T>(kf, static_cast<const T*>(p.k) + (int64_t)(start + at_key) * p.k_stride +
@@ -300,51 +388,75 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
   load_row<T>(vf, static_cast<const T*>(p.v) + (int64_t)(start + at_key) * p.v_stride +
                       (int64_t)kvh * p.D, half, chunks);
   f32x16 dk[DB], dv[DB];
-  for (int b = 0; b < kStages; ++b) clear_unused_chunks<CPR>(lds + b * kStage, 2 * BM, chunks);
+
+  // this piece's row blocks: the tile's first kTileUnits are what it costs beside them
+  const int32_t block0 = (int32_t)max(from - kTileUnits, (int64_t)0);
+  const int32_t blocks = min((int32_t)max(to - kTileUnits, (int64_t)0), blocks_of_tile(n, key0, p.G)) - block0;
+  const int32_t row_begin = key0 * p.G / BM * BM + block0 * BM;
+  auto first_row = [&](int32_t i) __attribute__((always_inline)) { return row_begin + i * BM; };
 
   const T* q = static_cast<const T*>(p.q) + (int64_t)start * p.q_stride + (int64_t)kvh * p.G * p.D;
   const T* g = static_cast<const T*>(p.dout) + (int64_t)start * p.dout_stride +
                (int64_t)kvh * p.G * p.D;
-  const int64_t stat0 = (int64_t)start * p.Hq + kvh * p.G;
-  if (item.block0 < 0 || item.block_end > (rows + BM - 1) / BM || item.slot >= p.units) return;
-  const int32_t row_begin = item.block0 * BM;
-  const int32_t blocks = item.block_end - item.block0;
-  // A last block that rows end in goes first, so that the partly masked blocks of a wave (this
-  // one and those on its diagonal) are a first loop and the others a second.
-  const int32_t tail = blocks > 0 && item.block_end * BM > rows;
-  auto first_row = [&](int32_t i) __attribute__((always_inline)) {
-    return row_begin + (tail ? (i == 0 ? blocks - 1 : i - 1) : i) * BM;
-  };
-
-  auto stage = [&](int32_t b) __attribute__((always_inline)) {
-    const uint32_t qd = lds_address(lds) + b % kStages * kStage, gd = qd + kTileBytes;
-    const int32_t row0 = first_row(b);
+  const float* stats = (half ? p.delta : p.lse2) + (int64_t)start * p.Hq + kvh * p.G;
+  // the next block's rows of this thread: head of the group, and offsets
+  uint32_t heads[kLoads + 1];
+  int64_t q_at[kLoads], g_at[kLoads], stat_at;
+  auto seek = [&](int32_t row0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint32_t c = i * 256 + tid;
-      const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle<CPR>(r);
-      const uint32_t at = min(row0 + (int32_t)r, rows - 1);
-      const uint32_t t = div31(at, p.by_g), h = at - t * p.G;
-      const uint32_t dst = (i * 256 + wave * 64) * 16;
-      if (chunk < chunks) {
-        copy_chunk_to_lds(q + (int64_t)t * p.q_stride + (h * p.D + 8 * chunk), qd + dst);
-        copy_chunk_to_lds(g + (int64_t)t * p.dout_stride + (h * p.D + 8 * chunk), gd + dst);
+    for (int i = 0; i <= kLoads; ++i) {
+      const uint32_t at = min(row0 + (int32_t)(i < kLoads ? row_of<CPR, 256>(i, tid) : lane & 31), rows - 1);
+      const uint32_t t = div31(at, p.by_g);
+      heads[i] = at - t * p.G;
+      if (i < kLoads) {
+        q_at[i] = t * p.q_stride + (heads[i] * p.D + 8 * chunk_of<CPR, 256>(i, tid));
+        g_at[i] = t * p.dout_stride + (heads[i] * p.D + 8 * chunk_of<CPR, 256>(i, tid));
+      } else {
+        stat_at = (int64_t)t * p.Hq + heads[i];
       }
     }
-    {  // lse and D of the rows, 32 words each; by every wave, for equal counts of copies
-      const uint32_t at = min(row0 + (int32_t)(lane & 31), rows - 1);
-      const uint32_t t = div31(at, p.by_g), h = at - t * p.G;
-      copy_word_to_lds((half ? p.delta : p.lse2) + stat0 + (int64_t)t * p.Hq + h, gd + kTileBytes);
+  };
+  auto advance = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i <= kLoads; ++i) {
+      bool wrap = false;
+      if (dh != 0) {
+        heads[i] += dh;
+        wrap = heads[i] >= (uint32_t)p.G;
+        if (wrap) heads[i] -= p.G;
+      }
+      if (i < kLoads) {
+        q_at[i] += q_step + (wrap ? q_wrap : 0);
+        g_at[i] += g_step + (wrap ? g_wrap : 0);
+      } else {
+        stat_at += stat_step + (wrap ? stat_wrap : 0);
+      }
     }
+  };
+  // The x-th copy of block b; blocks are begun in order, each after a call of go_to. The last
+  // is of lse and D of the rows, 32 words each, by every wave, for equal counts of copies.
+  constexpr int kPieces = 2 * kLoads + 1, kPerStep = (kPieces + KS - 1) / KS;
+  auto go_to = [&](int32_t b) __attribute__((always_inline)) {
+    if (b == 0 || first_row(b) + BM > rows) seek(first_row(b));  // also where the rows end
+    else advance();
+  };
+  auto piece = [&](int32_t b, int x) __attribute__((always_inline)) {
+    const uint32_t qd = lds_address(lds) + b % kStages * kStage, gd = qd + kTileBytes;
+    const int i = x / 2;
+    const uint32_t dst = (i * 256 + wave * 64) * 16;
+    if (x == 2 * kLoads) copy_word_to_lds(stats + stat_at, gd + kTileBytes);
+    else if (x % 2 == 0) copy_chunk_to_lds(q + q_at[i], qd + dst, lanes[i]);
+    else copy_chunk_to_lds(g + g_at[i], gd + dst, lanes[i]);
   };
 
   // The loop is pipelined over two blocks, because a wave is alone on its SIMD: while the
   // matrix unit forms S and dP of the next block, the vector unit turns this block's into P
-  // and dS, a slice of them per step; then dV and dK follow. `order()` keeps the steps apart
-  // for the scheduler, with LDS read two steps ahead of its use.
+  // and dS, a slice of them per step; then dV and dK follow, and between their last steps the
+  // block after the next is waited for.
   f32x16 s, dp;         // of the block at hand, then of the next one
   f32x4 lse2[4], delta[4];
-  auto order = [] { __builtin_amdgcn_sched_barrier(0); };
+  x8<T> qr[KS], gr[KS];  // rows of the next block, the first two steps' from the round before
+  auto buffer = [&](int32_t b) __attribute__((always_inline)) { return lds + b % kStages * kStage; };
   auto read_stats = [&](const uint8_t* qt) __attribute__((always_inline)) {
     const float* stat = reinterpret_cast<const float*>(qt + 2 * kTileBytes);
 #pragma unroll
@@ -353,64 +465,99 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
       delta[j] = *reinterpret_cast<const f32x4*>(stat + 32 + 8 * j + 4 * half);
     }
   };
-  // S and dP of the block at `qt`; `slice(t)` is called in step t of KS.
-  auto scores = [&](const uint8_t* qt, f32x16& s_out, f32x16& dp_out, auto slice) __attribute__((always_inline)) {
-    x8<T> qr[KS], gr[KS];
-    auto read = [&](int t) __attribute__((always_inline)) {
-      qr[t] = read_rows<T, CPR>(qt, lane & 31, 2 * t + half);
-      gr[t] = read_rows<T, CPR>(qt + kTileBytes, lane & 31, 2 * t + half);
-    };
-    read(0);
-    read(1);
+  auto read_row = [&](const uint8_t* qt, int t) __attribute__((always_inline)) {
+    qr[t] = read_rows<T, CPR>(qt, lane & 31, 2 * t + half);
+    gr[t] = read_rows<T, CPR>(qt + kTileBytes, lane & 31, 2 * t + half);
+  };
+  // S and dP of the block at `qt`, whose first two steps' rows have been read; `first(t)` and
+  // `second(t)` are called in step t of KS, one before each of its two products.
+  auto scores = [&](const uint8_t* qt, f32x16& s_out, f32x16& dp_out, auto first_half, auto second_half)
+                    __attribute__((always_inline)) {
     f32x16 a, c;
 #pragma unroll
     for (int i = 0; i < 16; ++i) a[i] = c[i] = 0.0f;
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
-      order();
-      if (t + 2 < KS) read(t + 2);
-      slice(t);
+      step();
+      if (t + 2 < KS) read_row(qt, t + 2);
       a = mfma(qr[t], kf[t], a);
+      first_half(t);
+      step();
       c = mfma(gr[t], vf[t], c);
+      second_half(t);
     }
-    order();
+    step();
     s_out = a;
     dp_out = c;
   };
-  auto round = [&](auto mode, const uint8_t* qt, const uint8_t* next, int32_t row0) __attribute__((always_inline)) {
+  auto round = [&](auto mode, int32_t b) __attribute__((always_inline)) {
     constexpr int MODE = decltype(mode)::value;
+    const uint8_t* qt = buffer(b);
     const uint8_t* gt = qt + kTileBytes;
-    f32x16 w, ds, s_next, dp_next;
-    scores(next, s_next, dp_next, [&](int t) __attribute__((always_inline)) {
+    const int32_t row0 = first_row(b);
+    go_to(b + kStages - 1);
+    if (row0 + BM > rows) {  // copies of the last row behind it: no weight
 #pragma unroll
-      for (int i = 16 * t / KS; i < 16 * (t + 1) / KS; ++i) {
-        const int j = i / 4, e = i % 4;
-        w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2[j][e]));
-        ds[i] = w[i] * (dp[i] - delta[j][e]);
+      for (int i = 0; i < 16; ++i)
+        if (row0 + 8 * (i / 4) + 4 * (int32_t)half + i % 4 >= rows) lse2[i / 4][i % 4] = __builtin_inff();
+    }
+    uint32_t w[8], ds[8];  // P and dS of row pairs, narrowed
+    auto pair = [&](int x) __attribute__((always_inline)) {
+      float wx[2], dx[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int i = 2 * x + c, j = i / 4, e = i % 4;
+        wx[c] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2[j][e]));
+        dx[c] = wx[c] * (dp[i] - delta[j][e]);
         if constexpr (MODE != kWhole) {
           const int32_t at = row0 + 8 * j + 4 * (int32_t)half + e;
-          if (at < first || at >= rows) w[i] = ds[i] = 0.0f;
+          if (at < first || (MODE == kCareful && at >= rows)) wx[c] = dx[c] = 0.0f;
         }
       }
-    });
-    s = s_next;
-    dp = dp_next;
-    read_stats(next);
-    x8<T> gc[2 * DB], qc[2 * DB];  // by step: 16 rows t = step / DB, columns d = step % DB
+      w[x] = narrow2<T>(wx[0], wx[1]);
+      ds[x] = narrow2<T>(dx[0], dx[1]);
+    };
+    x8<T> gc[2 * DB], qc[2 * DB];  // by step: 16 rows x / DB, columns x % DB
     auto read = [&](int x) __attribute__((always_inline)) {
       gc[x] = read_columns<T, CPR>(gt, 16 * (x / DB), x % DB, lane);
       qc[x] = read_columns<T, CPR>(qt, 16 * (x / DB), x % DB, lane);
     };
-    read(0);
-    read(1);
+    f32x16 s_next, dp_next;
+    // eight pairs of rows over 2 KS half steps, and the copies
+    scores(buffer(b + 1), s_next, dp_next,
+           [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+             for (int x = 16 * t / (2 * KS); x < 8 * (2 * t + 1) / (2 * KS); ++x) pair(x);
+#pragma unroll
+             for (int x = t * kPerStep; x < (t + 1) * kPerStep && x < kPieces; ++x)
+               piece(b + kStages - 1, x);
+           },
+           [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+             for (int x = 8 * (2 * t + 1) / (2 * KS); x < 8 * (2 * t + 2) / (2 * KS); ++x) pair(x);
+             if (t == KS - 1) {
+               read(0);
+               read(1);
+             }
+           });
+    s = s_next;
+    dp = dp_next;
+    read_stats(buffer(b + 1));
     x8<T> wb, db;
 #pragma unroll
     for (int x = 0; x < 2 * DB; ++x) {
-      order();
+      step();
       if (x + 2 < 2 * DB) read(x + 2);
+      if (x == 2 * DB - 1) {
+        // all of block b has been read: block b + 2 has arrived, and b's buffer is free
+        wait_copies_and_sync<kPieces>();
+        read_row(buffer(b + 2), 0);
+        read_row(buffer(b + 2), 1);
+      }
       if (x % DB == 0) {
-        wb = narrow8<T>(w, x / DB);
-        db = narrow8<T>(ds, x / DB);
+        const int y = 4 * (x / DB);
+        wb = __builtin_bit_cast(x8<T>, (u32x4){w[y], w[y + 1], w[y + 2], w[y + 3]});
+        db = __builtin_bit_cast(x8<T>, (u32x4){ds[y], ds[y + 1], ds[y + 2], ds[y + 3]});
       }
       if constexpr (MODE == kCareful) {
         gc[x] = cleaned<T>(gc[x]);
@@ -418,50 +565,48 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
       }
       dv[x % DB] = mfma(gc[x], wb, dv[x % DB]);
       dk[x % DB] = mfma(qc[x], db, dk[x % DB]);
+      if constexpr (MODE == kCareful)
+        if (x == 2 * DB - 2)  // before the barrier
+          for (int32_t j = 0; j < BM; ++j)
+            add_nonfinite_row<T, DB, CPR>(dv, gt, j, row0 + j >= first && row0 + j < rows, half);
     }
-    order();
-    if constexpr (MODE == kCareful)
-      for (int32_t j = 0; j < BM; ++j)
-        add_nonfinite_row<T, DB, CPR>(dv, gt, j, row0 + j >= first && row0 + j < rows, half);
+    step();
   };
 
-  auto buffer = [&](int32_t b) __attribute__((always_inline)) { return lds + b % kStages * kStage; };
-  // Before block b is finished its successor has arrived, and the buffer of its predecessor is
-  // free. Behind the last block the scores of whatever a buffer holds are formed and not used.
-  auto arrive = [&](int32_t b) __attribute__((always_inline)) {
-    if (b + 1 >= blocks) return;
-    wait_ring<kStages - 1, 2 * kLoads + 1>(blocks - 2 - b);
-    if (b + kStages - 1 < blocks) stage(b + kStages - 1);
-  };
-  const int32_t masked =
-      wave_first < rows ? min(blocks, tail + max(0, wave_all - row_begin + BM - 1) / BM) : blocks;
+  const int32_t partly = min(max(blocks, 0), max(0, wave_all - row_begin + BM - 1) / BM);
   auto walk = [&](auto mode) __attribute__((always_inline)) {
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.0f;
     if (blocks <= 0) return;
-    for (int32_t i = 0; i < min(blocks, kStages - 1); ++i) stage(i);
+    // Blocks behind the last are begun and scored like the others, and not used.
+    for (int32_t i = 0; i < kStages - 1; ++i) {
+      go_to(i);
+#pragma unroll
+      for (int x = 0; x < kPieces; ++x) piece(i, x);
+    }
     settle<T>(kf);
     settle<T>(vf);
-    wait_ring<kStages, 2 * kLoads + 1>(blocks - 1);
-    scores(buffer(0), s, dp, [](int) {});
+    wait_copies_and_sync<kPieces>();  // blocks 0 and 1
+    read_row(buffer(0), 0);
+    read_row(buffer(0), 1);
+    scores(buffer(0), s, dp, [](int) {}, [](int) {});
     read_stats(buffer(0));
+    read_row(buffer(1), 0);
+    read_row(buffer(1), 1);
+    // in careful mode every block is masked, for the rows behind the last
+    const int32_t masked = decltype(mode)::value == kCareful ? blocks : partly;
     int32_t b = 0;
-    for (; b < masked; ++b) {
-      arrive(b);
-      round(mode, buffer(b), buffer(b + 1), first_row(b));
-    }
-    for (; b < blocks; ++b) {
-      arrive(b);
-      round(Constant<kWhole>(), buffer(b), buffer(b + 1), first_row(b));
-    }
+    for (; b < masked; ++b) round(mode, b);
+    for (; b < blocks; ++b) round(Constant<kWhole>(), b);
+    wait_copies<0>();
   };
   walk(Constant<kMasked>());
-  if (any_wave(any_nonfinite(dk) || any_nonfinite(dv), lds)) walk(Constant<kCareful>());
+  if (any_wave(any_nonfinite(dk) || any_nonfinite(dv), flags)) walk(Constant<kCareful>());
 
-  if (item.slot >= 0) {
-    float* part = p.part + ((int64_t)item.slot * p.Hkv + kvh) * 2 * kKeyTile * p.D +
+  if (!whole) {
+    float* part = p.part + (2 * (int64_t)share + (from == 0)) * 2 * kKeyTile * p.D +
                   (32 * wave + (lane & 31)) * p.D;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -474,7 +619,7 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
         *reinterpret_cast<f32x4*>(part + kKeyTile * p.D + e) =
             (f32x4){dv[d][4 * j], dv[d][4 * j + 1], dv[d][4 * j + 2], dv[d][4 * j + 3]};
       }
-    return;
+    continue;
   }
 #pragma unroll
   for (int d = 0; d < DB; ++d)
@@ -483,36 +628,43 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
   const int64_t at_row = (int64_t)(start + at_key);
   store_row<T, DB>(dk, dk_out + at_row * p.dk_stride + (int64_t)kvh * p.D, half, chunks, on);
   store_row<T, DB>(dv, dv_out + at_row * p.dv_stride + (int64_t)kvh * p.D, half, chunks, on);
+  }
 }
 
-// Adds the partial sums of a split tile, in the order of its rows: one workgroup per tile,
-// key/value head and 32 keys.
+// Adds the partial sums of the tiles that are cut: workgroup x looks at the end of share x, and
+// takes the tile there if that is the first cut in it; y takes 32 of its keys.
 template <typename T>
 __global__ __launch_bounds__(256) void attn_bwd_join_kernel(const BwdParams p) {
-  const uint32_t index = div31(blockIdx.x, p.by_hkv);
-  const uint32_t kvh = blockIdx.x - index * p.Hkv;
-  if (!plan_matches(p) || (int32_t)index >= p.plan[6]) return;
-  const KeyJoin j = p.joins[index];
-  if (j.start < 0 || j.n <= 0 || j.start > p.T - j.n || j.key0 < 0 || j.slot < 0 || j.splits < 0 ||
-      j.slot + (int64_t)j.splits > p.units)
-    return;
+  if (!plan_matches(p)) return;
+  const Place work = place_of(p, gridDim.x);
+  const int64_t share = blockIdx.x, cut = (share + 1) * work.share;
+  if (cut >= work.total || work.tiles <= 0) return;
+  const uint32_t kvh = (uint32_t)(cut / work.units);
+  const int64_t pos = cut - kvh * work.units;
+  const int32_t index = find_tile(p, work.tiles, pos);
+  const KeyTile j = p.key_tiles[index];
+  const int64_t tile_begin = cut - (pos - j.first), tile_end = tile_begin - j.first + end_of_tile(p, work, index);
+  if (pos == j.first || tile_begin < share * work.share) return;
+  if (j.gap != 0 || j.start < 0 || j.n <= 0 || j.start > p.T - j.n || j.key0 < 0) return;
+  // its pieces: the second slot of this share, then the first ones of those that follow
+  const int32_t pieces = (int32_t)min((tile_end - 1) / work.share - share + 1, (int64_t)gridDim.x - share);
   const int32_t first = 32 * blockIdx.y, keys = min(32, j.n - j.key0 - first);
   const int32_t groups = p.D >> 2, size = kKeyTile * p.D;
-  const int64_t step = (int64_t)p.Hkv * 2 * size;
   for (int32_t i = threadIdx.x; i < 2 * keys * groups; i += 256) {
     const int32_t which = i >= keys * groups, of = i - which * keys * groups;
     const int32_t y = of / groups, e = 4 * (of - y * groups);
-    const float* part = p.part + ((int64_t)j.slot * p.Hkv + kvh) * 2 * size + which * size +
-                        (first + y) * p.D + e;
+    const float* part = p.part + 2 * share * 2 * size + which * size + (first + y) * p.D + e;
     f32x4 x = {0, 0, 0, 0};
-    for (int32_t s0 = 0; s0 < j.splits; s0 += 8) {  // eight loads at a time
+    for (int32_t s0 = 0; s0 < pieces; s0 += 8) {  // eight loads at a time
       f32x4 v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        v[u] = *reinterpret_cast<const f32x4*>(part + min(s0 + u, j.splits - 1) * step);
+      for (int u = 0; u < 8; ++u) {
+        const int64_t s = min(s0 + u, pieces - 1);
+        v[u] = *reinterpret_cast<const f32x4*>(part + (2 * s + (s == 0)) * 2 * size);
+      }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        if (s0 + u >= j.splits) break;
+        if (s0 + u >= pieces) break;
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[c] += v[u][c];
       }
@@ -526,18 +678,20 @@ __global__ __launch_bounds__(256) void attn_bwd_join_kernel(const BwdParams p) {
   }
 }
 
+// Shares of the dK/dV pass: the workgroups that 256 CUs hold at once.
+inline int32_t key_shares(int32_t D) { return D <= 32 ? 512 : 256; }
+
 template <typename T, int DB>
 int32_t launch(const BwdParams& p, const PackedSizes& z, hipStream_t s) {
   hipLaunchKernelGGL((attn_bwd_rows_kernel<T, DB>), dim3((unsigned)(z.rows * p.Hkv)), dim3(256), 0, s,
                      p);
   int32_t st = launched();
   if (st != ROPE_OK) return st;
-  hipLaunchKernelGGL((attn_bwd_keys_kernel<T, DB>), dim3((unsigned)(z.keys * p.Hkv)), dim3(256), 0, s,
-                     p);
+  const unsigned shares = key_shares(p.D);
+  hipLaunchKernelGGL((attn_bwd_keys_kernel<T, DB>), dim3(shares), dim3(256), 0, s, p);
   st = launched();
   if (st != ROPE_OK) return st;
-  hipLaunchKernelGGL((attn_bwd_join_kernel<T>), dim3((unsigned)(z.joins * p.Hkv), kKeyTile / 32),
-                     dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_bwd_join_kernel<T>), dim3(shares, kKeyTile / 32), dim3(256), 0, s, p);
   return launched();
 }
 
@@ -559,7 +713,7 @@ using namespace attn;
 extern "C" int64_t attn_bwd_scratch_floats(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv,
                                            int32_t D) {
   if (!valid_batch(T, num_seqs, Hq, Hkv) || !valid_head_size(D) || D > 128) return -1;
-  return packed_sizes(T, num_seqs, Hq, Hkv).units * Hkv * 2 * kKeyTile * D + 2 * T * Hq;
+  return (int64_t)2 * key_shares(D) * 2 * kKeyTile * D + 2 * T * Hq;
 }
 
 extern "C" int32_t attn_bwd(const void* dout, const void* q, const void* k, const void* v,
@@ -589,7 +743,7 @@ extern "C" int32_t attn_bwd(const void* dout, const void* q, const void* k, cons
   if (lse == nullptr || !data_pointer(scratch)) return ROPE_EINVAL;
   p.G = Hq / Hkv;
   const PackedSizes z = packed_sizes(T, num_seqs, Hq, Hkv);
-  if (z.rows * Hkv > kMaxBlocks || z.keys * Hkv > kMaxBlocks) return ROPE_EINVAL;
+  if (z.rows * Hkv > kMaxBlocks) return ROPE_EINVAL;
   p.dout = dout;
   p.q = q;
   p.k = k;
@@ -597,16 +751,14 @@ extern "C" int32_t attn_bwd(const void* dout, const void* q, const void* k, cons
   p.out = out;
   p.lse = lse;
   p.part = scratch;
-  p.units = z.units;
-  p.lse2 = scratch + z.units * Hkv * 2 * kKeyTile * D;
+  p.lse2 = scratch + (int64_t)2 * key_shares(D) * 2 * kKeyTile * D;
   p.delta = p.lse2 + T * Hq;
   p.dq = dq;
   p.dk = dk;
   p.dv = dv;
   p.plan = plan;
   p.row_items = reinterpret_cast<const RowItem*>(plan + kHeader);
-  p.key_items = reinterpret_cast<const KeyItem*>(p.row_items + z.rows);
-  p.joins = reinterpret_cast<const KeyJoin*>(p.key_items + z.keys);
+  p.key_tiles = reinterpret_cast<const KeyTile*>(p.row_items + z.rows + z.rows % 2);
   p.T = (int32_t)T;
   p.Hq = Hq;
   p.Hkv = Hkv;

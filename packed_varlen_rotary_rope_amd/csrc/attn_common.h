@@ -131,18 +131,22 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef const __attribute__((address_space(1))) void gvoid;
 
 // One 16-byte chunk (4-byte word) per lane from global memory into LDS, no registers
-// between: lane l's lands at dst + 16 l (4 l), dst the same for the whole wave; idle lanes
-// write nothing. In assembly because the compiler otherwise waits for every copy in flight
-// before each transposed read of LDS, also of the half that no copy writes. m0 holds the
-// LDS address and needs one wait state. Whoever reads the data waits first (wait_copies).
+// between: lane l's lands at dst + 16 l (4 l), dst the same for the whole wave; lanes that are
+// not set in `lanes` write nothing. For whole waves in uniform flow: all lanes are active, and
+// are again behind it. In assembly because the compiler otherwise waits for every copy in
+// flight before each transposed read of LDS, also of a buffer that no copy writes, and breaks
+// the loop up where lanes are left out. m0 holds the LDS address and needs one wait state.
+// Whoever reads the data waits first (wait_copies).
 __device__ inline uint32_t lds_address(const uint8_t* p) {
   return (uint32_t)(uintptr_t)(lds_void*)p;
 }
-__device__ inline void copy_chunk_to_lds(const void* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-               :
-               : "v"(src), "s"(__builtin_amdgcn_readfirstlane(dst))
-               : "memory");
+__device__ inline void copy_chunk_to_lds(const void* src, uint32_t dst, uint64_t lanes) {
+  asm volatile(
+      "s_mov_b32 m0, %1\n\ts_mov_b64 exec, %2\n\tglobal_load_lds_dwordx4 %0, off\n\t"
+      "s_mov_b64 exec, -1"
+      :
+      : "v"(src), "s"(__builtin_amdgcn_readfirstlane(dst)), "s"(lanes)
+      : "memory");
 }
 __device__ inline void copy_word_to_lds(const void* src, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
@@ -176,6 +180,21 @@ __device__ inline void wait_ring(int32_t younger) {
   else if (STAGES >= 3 && younger >= 1) wait_copies_and_sync<STAGES >= 3 ? COPIES : 0>();
   else wait_copies_and_sync<0>();
 }
+
+// The chunks of a tile, 256 (one workgroup) or 64 (one wave) at a time in the order of LDS:
+// of thread t, row (i * COUNT + t) / CPR and this chunk of it.
+template <int CPR, int COUNT>
+__device__ inline uint32_t row_of(int i, uint32_t t) {
+  return (i * COUNT + t) / CPR;
+}
+template <int CPR, int COUNT>
+__device__ inline uint32_t chunk_of(int i, uint32_t t) {
+  return ((i * COUNT + t) % CPR) ^ swizzle<CPR>(row_of<CPR, COUNT>(i, t));
+}
+
+// Ends a step for the scheduler: nothing moves across. The loops below read LDS a step or two
+// ahead of its use and begin a copy or two a step, so that neither is waited for.
+__device__ inline void step() { __builtin_amdgcn_sched_barrier(0); }
 
 // Row-major operand: chunk c of row r.
 template <typename T, int CPR>

@@ -84,58 +84,52 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
   const T* v = static_cast<const T*>(p.v) + (int64_t)start * p.v_stride + (int64_t)kvh * p.D;
   const int32_t blocks = (key_end + BN - 1) / BN;
 
-  // Two buffers each for K and V. A block's V is begun with the block before, and the next
-  // block's K in the middle of that, as soon as its buffer has been read by every wave, so
-  // that either has a block and a half to arrive.
-  auto stage = [&](const T* base, int64_t stride, uint32_t tile, int32_t b) __attribute__((always_inline)) {
-    const uint32_t dst = lds_address(lds) + ((b & 1) * 2 + tile) * Tile::kTileBytes;
-    const int32_t key0 = b * BN, last = key_end - 1 - key0;
-    const T* from = base + (int64_t)key0 * stride;
+  // Two buffers each for K and V: while a block is worked on, the next one's copies are begun
+  // one a step of its scores (all at once, they would hold the wave up).
+  uint64_t lanes[kLoads];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint32_t c = i * 256 + tid;
-      const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle<CPR>(r);
-      const uint32_t at = (uint32_t)min((int32_t)r, last);
-      if (chunk < chunks)
-        copy_chunk_to_lds(from + (at * (uint32_t)stride + 8 * chunk), dst + (i * 256 + wave * 64) * 16);
-    }
+  for (int i = 0; i < kLoads; ++i) lanes[i] = __ballot(chunk_of<CPR, 256>(i, tid) < chunks);
+  auto piece = [&](int32_t b, int32_t buffer, int x) __attribute__((always_inline)) {  // x-th copy of block b
+    const int i = x / 2;
+    const int64_t stride = x % 2 ? p.v_stride : p.k_stride;
+    const int32_t key0 = b * BN;
+    const uint32_t at = min((int32_t)row_of<CPR, 256>(i, tid), key_end - 1 - key0);
+    const T* from = (x % 2 ? v : k) + (int64_t)key0 * stride;
+    copy_chunk_to_lds(from + (at * (uint32_t)stride + 8 * chunk_of<CPR, 256>(i, tid)),
+                      lds_address(lds) + (buffer * 2 + x % 2) * Tile::kTileBytes + (i * 256 + wave * 64) * 16,
+                      lanes[i]);
   };
+  constexpr int kPieces = 2 * kLoads, kPerStep = (kPieces + Tile::KS - 1) / Tile::KS;
   const int32_t all = wave_end > 0 ? wave_all / BN : 0;  // blocks that every row of the wave sees
   auto walk = [&](auto mode) __attribute__((always_inline)) {
     t.clear();
-    int32_t b = 0;
-    auto begin = [&]() __attribute__((always_inline)) {  // K of block b has arrived, and V's other buffer is free
-      if (b + 1 < blocks) {
-        wait_copies_and_sync<2 * kLoads>();
-        stage(v, p.v_stride, 1, b + 1);
-      } else {
-        wait_copies_and_sync<kLoads>();
-      }
-      return lds + (b & 1) * 2 * Tile::kTileBytes;
-    };
-    auto middle = [&]() __attribute__((always_inline)) {  // V of block b has arrived, and its K has been read
-      if (b + 1 < blocks) wait_copies_and_sync<2 * kLoads>();
-      else wait_copies_and_sync<0>();
-      if (b + 2 < blocks) stage(k, p.k_stride, 0, b + 2);
-    };
-    stage(k, p.k_stride, 0, 0);
-    stage(v, p.v_stride, 1, 0);
-    if (blocks > 1) stage(k, p.k_stride, 0, 1);
+#pragma unroll
+    for (int x = 0; x < kPieces; ++x) piece(0, 0, x);
     settle<T>(t.q);
+    int32_t b = 0;
+    // behind the last block the last key's copies go on into the buffer that is not used
+    auto next = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int x = s * kPerStep; x < (s + 1) * kPerStep && x < kPieces; ++x) piece(min(b + 1, blocks - 1), ~b & 1, x);
+    };
     // Two loops, so that neither body's registers are moved for the other's sake. Waves may be
-    // in different ones: each passes the same two barriers per block in either.
+    // in different ones: each passes one barrier per block in either.
     for (; b < all; ++b) {
-      const uint8_t* kt = begin();
-      t.template block<kWhole>(kt, kt + Tile::kTileBytes, b * BN, seen, 0, p.scale, lane, middle);
+      wait_copies_and_sync<0>();  // block b has arrived, and the other buffers are free
+      const uint8_t* kt = lds + (b & 1) * 2 * Tile::kTileBytes;
+      t.template block<kWhole>(kt, kt + Tile::kTileBytes, b * BN, seen, 0, p.scale, lane, next);
     }
     for (; b < blocks; ++b) {
-      const uint8_t* kt = begin();
+      wait_copies_and_sync<0>();
+      const uint8_t* kt = lds + (b & 1) * 2 * Tile::kTileBytes;
       if (b * BN < wave_end)
         t.template block<Mode(decltype(mode)::value)>(kt, kt + Tile::kTileBytes, b * BN, seen, 0, p.scale,
-                                                      lane, middle);
+                                                      lane, next);
       else
-        middle();
+#pragma unroll
+        for (int s = 0; s < Tile::KS; ++s) next(s);
     }
+    wait_copies<0>();
   };
   walk(Constant<kMasked>());
   if (any_wave(any_nonfinite(t.o), lds)) walk(Constant<kCareful>());

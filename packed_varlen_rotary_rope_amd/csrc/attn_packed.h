@@ -12,30 +12,30 @@ struct RowItem {
   int32_t start, n, row0, gap;
 };
 
-// Keys key0 .. key0 + 127 of the sequence, against its blocks block0 .. block_end - 1 of 32
-// packed rows. slot: of the partial sums where a tile's rows are split, else < 0.
-struct KeyItem {
-  int32_t start, n, key0, gap, block0, block_end, slot, unused;
+// Keys key0 .. key0 + 127 of the sequence, against all of its blocks of 32 packed rows that
+// see one; or, with gap set, n rows of no sequence. first: the work of the tiles before it.
+// A tile's work is kTileUnits and one unit a block (1 in all where gap is set).
+struct KeyTile {
+  int32_t start, n, key0, gap;
+  int64_t first;
+  int32_t unused[2];
 };
+static_assert(sizeof(RowItem) == 16 && sizeof(KeyTile) == 32, "words");
 
-// A tile whose rows are split: slots slot .. slot + splits - 1.
-struct KeyJoin {
-  int32_t start, n, key0, slot, splits, unused[3];
-};
-static_assert(sizeof(RowItem) == 16 && sizeof(KeyItem) == 32 && sizeof(KeyJoin) == 32, "words");
+constexpr int32_t kRowBlock = 32;   // packed rows of a step of the dK/dV pass
+constexpr int32_t kTileUnits = 8;   // what a tile costs beside its blocks, in blocks
+constexpr int32_t kMinUnits = 12;   // of a workgroup's share
 
-constexpr int32_t kRowBlock = 32;      // packed rows of a step of the dK/dV pass
-constexpr int32_t kMinRowBlocks = 16;  // of a split
-constexpr int32_t kKeyTarget = 512;    // workgroups that its work is split into, about
+// Row blocks that see a key of the tile at key0 of a sequence of n tokens.
+__host__ __device__ inline int32_t blocks_of_tile(int32_t n, int32_t key0, int32_t G) {
+  return n * G / kRowBlock + (n * G % kRowBlock != 0) - key0 * G / kRowBlock;
+}
 
 struct PackedSizes {
-  int64_t rows, keys, joins, units;
+  int64_t rows, keys;
 };
-// Every split holds more than half of the work that kKeyTarget stands for, so that there are
-// fewer than 2 kKeyTarget / Hkv of them, in at most kKeyTarget / Hkv tiles.
 inline PackedSizes packed_sizes(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv) {
-  const int64_t splits = kKeyTarget / Hkv + 1;
-  return {row_items(T, num_seqs, Hq / Hkv), key_items(T, num_seqs) + splits, splits, 2 * splits};
+  return {row_items(T, num_seqs, Hq / Hkv), key_items(T, num_seqs)};
 }
 
 inline bool valid_batch(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv) {

@@ -299,17 +299,17 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
     const int32_t blocks = keys > 0 ? (keys + BN - 1) / BN : 0;
     const PagedKeys<BN, CPR> src{table, pages[wave], offsets[wave], key_end};
     constexpr int kLoads = BN * CPR / 256;
+    uint64_t lanes[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) lanes[i] = __ballot(chunk_of<CPR, 256>(i, tid) < chunks);
     auto stage = [&](int32_t b) __attribute__((always_inline)) {
       const uint32_t kd = lds_address(lds) + (b & 1) * 2 * kTileBytes;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const uint32_t c = i * 256 + tid;
-        const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle<CPR>(r);
+        const uint32_t r = row_of<CPR, 256>(i, tid), chunk = chunk_of<CPR, 256>(i, tid);
         const uint32_t dst = kd + (i * 256 + wave * 64) * 16;
-        if (chunk < chunks) {
-          copy_chunk_to_lds(src.row(kb, b & 1, r) + 16 * chunk, dst);
-          copy_chunk_to_lds(src.row(vb, b & 1, r) + 16 * chunk, dst + kTileBytes);
-        }
+        copy_chunk_to_lds(src.row(kb, b & 1, r) + 16 * chunk, dst, lanes[i]);
+        copy_chunk_to_lds(src.row(vb, b & 1, r) + 16 * chunk, dst + kTileBytes, lanes[i]);
       }
     };
     // Two loops, so that neither body's registers are moved for the other's sake; the first
@@ -340,14 +340,14 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
       };
       for (; b < all && hidden_next == 0; ++b) {
         const uint8_t* kt = arrive();
-        t.template block<kWhole>(kt, kt + kTileBytes, item.key0 + b * BN, seen, 0, p.scale, lane, [] {});
+        t.template block<kWhole>(kt, kt + kTileBytes, item.key0 + b * BN, seen, 0, p.scale, lane, [](int) {});
       }
       for (; b < blocks; ++b) {
         const uint8_t* kt = arrive();
         const int32_t key0 = item.key0 + b * BN;
         if (key0 < wave_end)
           t.template block<Mode(decltype(mode)::value)>(kt, kt + kTileBytes, key0, seen, hidden, p.scale,
-                                                        lane, [] {});
+                                                        lane, [](int) {});
       }
     };
     walk(Constant<kMasked>());
@@ -390,14 +390,14 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
     const uint8_t* vt = kOneBuffer ? kt : kt + kSmallTile;
     const int32_t blocks = keys > 0 ? ((keys + 31) / 32 - (int32_t)wave + 3) / 4 : 0;
     const int32_t first = item.key0 + 32 * wave;
+    uint64_t lanes[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) lanes[i] = __ballot(chunk_of<CPR, 64>(i, lane) < chunks);
     auto stage = [&](const uint8_t* base, const uint8_t* tile, int parity) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const uint32_t c = i * 64 + lane;
-        const uint32_t r = c / CPR, chunk = (c % CPR) ^ swizzle<CPR>(r);
-        if (chunk < chunks)
-          copy_chunk_to_lds(src.row(base, parity, r) + 16 * chunk, lds_address(tile) + i * 1024);
-      }
+      for (int i = 0; i < kLoads; ++i)
+        copy_chunk_to_lds(src.row(base, parity, row_of<CPR, 64>(i, lane)) + 16 * chunk_of<CPR, 64>(i, lane),
+                          lds_address(tile) + i * 1024, lanes[i]);
     };
     uint64_t hidden = 0, hidden_next = 0;
     auto round = [&](auto mode, int32_t b) __attribute__((always_inline)) {
@@ -408,7 +408,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
       f32x16 s[1];
       x8<T> w[2];
       wait_copies<kOneBuffer ? 0 : kLoads>();
-      t.scores(s, kt, lane);
+      t.scores(s, kt, lane, [](int) {});
       reads_done();
       if (kOneBuffer) stage(vb, vt, b & 1);
       if (more) {

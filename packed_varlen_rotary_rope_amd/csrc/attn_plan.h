@@ -11,28 +11,32 @@ namespace attn {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
 
-struct AddOp {
-  static constexpr int32_t kZero = 0;
-  __device__ static int32_t apply(int32_t a, int32_t b) { return a + b; }
+template <typename V>
+struct Sum {
+  typedef V type;
+  static constexpr V kZero = 0;
+  __device__ static V apply(V a, V b) { return a + b; }
 };
+typedef Sum<int32_t> AddOp;
 struct MaxOp {
+  typedef int32_t type;
   static constexpr int32_t kZero = INT32_MIN;
   __device__ static int32_t apply(int32_t a, int32_t b) { return a > b ? a : b; }
 };
 
-// Inclusive scan over the workgroup; buf: kPlanWaves words, free again after a barrier.
-template <typename Op>
-__device__ inline int32_t block_scan(int32_t x, int32_t* buf) {
+// Inclusive scan over the workgroup; buf: kPlanWaves values, free again after a barrier.
+template <typename Op, typename V = typename Op::type>
+__device__ inline V block_scan(V x, V* buf) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int32_t y = __shfl_up(x, d);
+    const V y = __shfl_up(x, d);
     if (lane >= d) x = Op::apply(x, y);
   }
   __syncthreads();
   if (lane == 63) buf[wave] = x;
   __syncthreads();
-  int32_t before = Op::kZero;
+  V before = Op::kZero;
   for (int w = 0; w < wave; ++w) before = Op::apply(before, buf[w]);
   return Op::apply(before, x);
 }

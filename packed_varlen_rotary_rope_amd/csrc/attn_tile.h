@@ -105,17 +105,31 @@ struct FwdTile {
     l = 0.0f;
   }
 
-  // S^T of a block of keys.
-  __device__ void scores(f32x16 (&s)[KB], const uint8_t* kt, uint32_t lane) {
+  // S^T of a block of keys, in KS steps; `piece(t)` is called in step t.
+  template <typename P>
+  __device__ __attribute__((always_inline)) void scores(f32x16 (&s)[KB], const uint8_t* kt,
+                                                        uint32_t lane, P piece) {
     const uint32_t r = lane & 31, half = lane >> 5;
+    x8<T> k[KS][KB];
+    auto read = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
+      for (int b = 0; b < KB; ++b) k[t][b] = read_rows<T, CPR>(kt, 32 * b + r, 2 * t + half);
+    };
+    read(0);
+    read(1);
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
 #pragma unroll
-      for (int t = 0; t < KS; ++t)
-        s[b] = mfma(read_rows<T, CPR>(kt, 32 * b + r, 2 * t + half), q[t], s[b]);
+    for (int t = 0; t < KS; ++t) {
+      step();
+      if (t + 2 < KS) read(t + 2);
+      piece(t);
+#pragma unroll
+      for (int b = 0; b < KB; ++b) s[b] = mfma(k[t][b], q[t], s[b]);
     }
+    step();
   }
 
   // Scores to weights, narrowed; m, l and o follow. Keys key0 + j at or behind `seen` (as a
@@ -170,28 +184,37 @@ struct FwdTile {
   template <Mode MODE>
   __device__ void accumulate(const x8<T> (&p)[2 * KB], const uint8_t* vt, int32_t key0, int32_t seen,
                              uint64_t hidden, uint32_t lane) {
+    constexpr int N = 2 * KB * DB;  // by step: keys 16 (x / DB) .. + 15, columns 32 (x % DB) .. + 31
+    x8<T> v[N];
+    auto read = [&](int x) __attribute__((always_inline)) {
+      v[x] = read_columns<T, CPR>(vt, 16 * (x / DB), x % DB, lane);
+    };
+    read(0);
+    read(1);
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int t = 0; t < 2 * KB; ++t) {
-        x8<T> v = read_columns<T, CPR>(vt, 16 * t, d, lane);
-        if constexpr (MODE == kCareful) v = cleaned<T>(v);
-        o[d] = mfma(v, p[t], o[d]);
+    for (int x = 0; x < N; ++x) {
+      if (x % 2 == 0) {
+        step();
+        if (x + 2 < N) read(x + 2);
+        if (x + 3 < N) read(x + 3);
       }
+      if constexpr (MODE == kCareful) v[x] = cleaned<T>(v[x]);
+      o[x % DB] = mfma(v[x], p[x / DB], o[x % DB]);
+    }
+    step();
     // what is infinite or NaN stays so whatever its weight
     if constexpr (MODE == kCareful)
       for (int32_t j = 0; j < BN; ++j)
         add_nonfinite_row<T, DB, CPR>(o, vt, j, key0 + j < seen && !(hidden >> j & 1), lane >> 5);
   }
 
-  // One block; `middle` is called once its scores are formed, before V is read.
-  template <Mode MODE, typename M>
-  __device__ void block(const uint8_t* kt, const uint8_t* vt, int32_t key0, int32_t seen,
-                        uint64_t hidden, float scale, uint32_t lane, M middle) {
+  template <Mode MODE, typename P>
+  __device__ __attribute__((always_inline)) void block(const uint8_t* kt, const uint8_t* vt,
+                                                       int32_t key0, int32_t seen, uint64_t hidden,
+                                                       float scale, uint32_t lane, P piece) {
     f32x16 s[KB];
     x8<T> p[2 * KB];
-    scores(s, kt, lane);
-    middle();
+    scores(s, kt, lane, piece);
     weights<MODE>(s, p, key0, seen, hidden, scale, lane);
     accumulate<MODE>(p, vt, key0, seen, hidden, lane);
   }
