@@ -29,8 +29,8 @@ struct BwdParams {
   const void* v;
   const void* out;
   const float* lse;
-  float* lse2;   // scratch: lse * log2 e
-  float* delta;  // scratch: D_i
+  float* lse2;   // scratch: lse * log2 e and
+  float* delta;  // D_i, by key/value head and packed row: [Hkv][T * G]
   void* dq;
   void* dk;
   void* dv;
@@ -59,9 +59,10 @@ __device__ inline void clear_rows(T* x, int32_t start, int32_t n, int64_t stride
 
 template <typename T, int DB>
 __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p) {
-  constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BN = 32;
+  constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BN = DB <= 2 ? 64 : 32;
   constexpr int kTileBytes = BN * CPR * 16, kLoads = BN * CPR / 256;
-  constexpr int kStages = 5;  // 80 KB at most: two workgroups on a CU
+  // Up to 64 columns three workgroups share a CU (3 x 48 KB of LDS), above that two (80 KB).
+  constexpr int kStages = DB <= 2 ? 3 : 5;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * 2 * kTileBytes];
 
   uint32_t kvh;
@@ -137,72 +138,57 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   };
 
   int32_t b = 0;
-  // P and dP of the 32 keys of block b, in KS steps, which begin the copies of the block
-  // kStages - 1 further; what is hidden gets P = dP = 0.
+  // P and dP of 32 keys of block b; the first of them begin the copies of the block
+  // kStages - 1 further between their steps. What is hidden gets P = dP = 0.
   auto next = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
     for (int x = s * kPerStep; x < (s + 1) * kPerStep && x < kPieces; ++x) piece(b + kStages - 1, x);
   };
-  auto weights = [&](auto mode, const uint8_t* kt, int32_t key0, f32x16& s, f32x16& dp) __attribute__((always_inline)) {
-    x8<T> kr[KS], vr[KS];
-    auto read = [&](int t) __attribute__((always_inline)) {
-      kr[t] = read_rows<T, CPR>(kt, lane & 31, 2 * t + half);
-      vr[t] = read_rows<T, CPR>(kt + kTileBytes, lane & 31, 2 * t + half);
-    };
-    read(0);
-    read(1);
+  auto weights = [&](auto mode, const uint8_t* kt, int32_t key0, int c, f32x16& s, f32x16& dp)
+                     __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
-      step();
-      if (t + 2 < KS) read(t + 2);
-      next(t);
-      s = mfma(kr[t], qf[t], s);
-      dp = mfma(vr[t], df[t], dp);
+      if (c == 0) next(t);
+      s = mfma(read_rows<T, CPR>(kt, 32 * c + (lane & 31), 2 * t + half), qf[t], s);
+      dp = mfma(read_rows<T, CPR>(kt + kTileBytes, 32 * c + (lane & 31), 2 * t + half), df[t], dp);
     }
-    step();
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2));
       if constexpr (decltype(mode)::value != kWhole) {
-        const int32_t key = key0 + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
+        const int32_t key = key0 + 32 * c + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
         if (key >= seen) s[i] = dp[i] = 0.0f;
       }
     }
   };
   auto block = [&](auto mode, const uint8_t* kt, int32_t key0) __attribute__((always_inline)) {
-    f32x16 s, dp;
-    weights(mode, kt, key0, s, dp);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      s[i] = s[i] * (dp[i] - delta);
-      if constexpr (decltype(mode)::value != kWhole) {  // also where D_i is not finite
-        const int32_t key = key0 + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
-        if (key >= seen) s[i] = 0.0f;
+    for (int c = 0; c < BN / 32; ++c) {
+      f32x16 s, dp;
+      weights(mode, kt, key0, c, s, dp);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[i] = s[i] * (dp[i] - delta);
+        if constexpr (decltype(mode)::value != kWhole) {  // also where D_i is not finite
+          const int32_t key = key0 + 32 * c + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
+          if (key >= seen) s[i] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const x8<T> ds = narrow8<T>(s, t);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+          x8<T> kc = read_columns<T, CPR>(kt, 32 * c + 16 * t, d, lane);
+          // a key that is seen and not finite has made dS NaN or 0 already
+          if constexpr (decltype(mode)::value == kCareful) kc = cleaned<T>(kc);
+          dq[d] = mfma(kc, ds, dq[d]);
+        }
       }
     }
-    x8<T> kc[2 * DB];
-    auto read = [&](int x) __attribute__((always_inline)) {
-      kc[x] = read_columns<T, CPR>(kt, 16 * (x / DB), x % DB, lane);
-    };
-    read(0);
-    read(1);
-    const x8<T> ds[2] = {narrow8<T>(s, 0), narrow8<T>(s, 1)};
-#pragma unroll
-    for (int x = 0; x < 2 * DB; ++x) {
-      if (x % 2 == 0) {
-        step();
-        if (x + 2 < 2 * DB) read(x + 2);
-        if (x + 3 < 2 * DB) read(x + 3);
-      }
-      // a key that is seen and not finite has made dS NaN or 0 already
-      if constexpr (decltype(mode)::value == kCareful) kc[x] = cleaned<T>(kc[x]);
-      dq[x % DB] = mfma(kc[x], ds[x / DB], dq[x % DB]);
-    }
-    step();
   };
-
   auto first_stages = [&]() __attribute__((always_inline)) {
     for (int32_t i = 0; i < kStages - 1; ++i)
 #pragma unroll
@@ -229,10 +215,13 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
         skip();
         continue;
       }
-      f32x16 s, dp;
-      weights(Constant<kMasked>(), kt, b * BN, s, dp);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(s[i], dp[i], sum);
+      for (int c = 0; c < BN / 32; ++c) {
+        f32x16 s, dp;
+        weights(Constant<kMasked>(), kt, b * BN, c, s, dp);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(s[i], dp[i], sum);
+      }
     }
     delta = half_sum(sum);
     wait_copies_and_sync<0>();  // the last block has been read, and what came behind it is there
@@ -240,8 +229,9 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
     first_stages();
   }
   if (on && half == 0) {
-    p.lse2[at_stat] = lse2;
-    p.delta[at_stat] = delta;
+    const int64_t at = ((int64_t)kvh * p.T + start) * p.G + row;
+    p.lse2[at] = lse2;
+    p.delta[at] = delta;
   }
   // two loops, and a second walk where it is needed, as in the forward
   const int32_t all = wave_end > 0 ? wave_all / BN : 0;
@@ -317,9 +307,10 @@ __device__ inline int64_t end_of_tile(const BwdParams& p, const Place& w, int32_
 }
 
 template <typename T, int DB>
-__global__ __launch_bounds__(256, DB <= 1 ? 2 : 1) void attn_bwd_keys_kernel(const BwdParams p) {
+__global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(const BwdParams p) {
   constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BM = kRowBlock;
   constexpr int kTileBytes = BM * CPR * 16, kLoads = BM * CPR / 256;
+  constexpr bool kPipelined = DB > 2;
   constexpr int kStatBytes = 2 * BM * 4, kStage = 2 * kTileBytes + kStatBytes, kStages = 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage];
   __shared__ __attribute__((aligned(16))) uint8_t flags[16];
@@ -345,7 +336,6 @@ __global__ __launch_bounds__(256, DB <= 1 ? 2 : 1) void attn_bwd_keys_kernel(con
   const uint32_t dt = div31(BM, p.by_g), dh = BM - dt * p.G;
   const int64_t q_step = dt * p.q_stride + (int64_t)dh * p.D, q_wrap = p.q_stride - (int64_t)p.G * p.D;
   const int64_t g_step = dt * p.dout_stride + (int64_t)dh * p.D, g_wrap = p.dout_stride - (int64_t)p.G * p.D;
-  const int64_t stat_step = (int64_t)dt * p.Hq + dh, stat_wrap = p.Hq - p.G;
 
   for (; left > 0; ++index) {
   if (pos >= work.units) {
@@ -398,44 +388,37 @@ __global__ __launch_bounds__(256, DB <= 1 ? 2 : 1) void attn_bwd_keys_kernel(con
   const T* q = static_cast<const T*>(p.q) + (int64_t)start * p.q_stride + (int64_t)kvh * p.G * p.D;
   const T* g = static_cast<const T*>(p.dout) + (int64_t)start * p.dout_stride +
                (int64_t)kvh * p.G * p.D;
-  const float* stats = (half ? p.delta : p.lse2) + (int64_t)start * p.Hq + kvh * p.G;
+  const float* stats = (half ? p.delta : p.lse2) + ((int64_t)kvh * p.T + start) * p.G;
   // the next block's rows of this thread: head of the group, and offsets
-  uint32_t heads[kLoads + 1];
-  int64_t q_at[kLoads], g_at[kLoads], stat_at;
+  uint32_t heads[kLoads];
+  int64_t q_at[kLoads], g_at[kLoads];
   auto seek = [&](int32_t row0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i <= kLoads; ++i) {
-      const uint32_t at = min(row0 + (int32_t)(i < kLoads ? row_of<CPR, 256>(i, tid) : lane & 31), rows - 1);
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t at = min(row0 + (int32_t)row_of<CPR, 256>(i, tid), rows - 1);
       const uint32_t t = div31(at, p.by_g);
       heads[i] = at - t * p.G;
-      if (i < kLoads) {
-        q_at[i] = t * p.q_stride + (heads[i] * p.D + 8 * chunk_of<CPR, 256>(i, tid));
-        g_at[i] = t * p.dout_stride + (heads[i] * p.D + 8 * chunk_of<CPR, 256>(i, tid));
-      } else {
-        stat_at = (int64_t)t * p.Hq + heads[i];
-      }
+      q_at[i] = t * p.q_stride + (heads[i] * p.D + 8 * chunk_of<CPR, 256>(i, tid));
+      g_at[i] = t * p.dout_stride + (heads[i] * p.D + 8 * chunk_of<CPR, 256>(i, tid));
     }
   };
   auto advance = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i <= kLoads; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       bool wrap = false;
       if (dh != 0) {
         heads[i] += dh;
         wrap = heads[i] >= (uint32_t)p.G;
         if (wrap) heads[i] -= p.G;
       }
-      if (i < kLoads) {
-        q_at[i] += q_step + (wrap ? q_wrap : 0);
-        g_at[i] += g_step + (wrap ? g_wrap : 0);
-      } else {
-        stat_at += stat_step + (wrap ? stat_wrap : 0);
-      }
+      q_at[i] += q_step + (wrap ? q_wrap : 0);
+      g_at[i] += g_step + (wrap ? g_wrap : 0);
     }
   };
-  // The x-th copy of block b; blocks are begun in order, each after a call of go_to. The last
-  // is of lse and D of the rows, 32 words each, by every wave, for equal counts of copies.
-  constexpr int kPieces = 2 * kLoads + 1, kPerStep = (kPieces + KS - 1) / KS;
+  // The x-th copy of block b; blocks are begun in order, each after a call of go_to. The first
+  // is of lse and D of the rows, 32 words each, by the first wave: it waits for one copy more
+  // than it would have to, the other waves for what they need.
+  constexpr int kPieces = 2 * kLoads, kPerStep = (kPieces + KS - 1) / KS;
   auto go_to = [&](int32_t b) __attribute__((always_inline)) {
     if (b == 0 || first_row(b) + BM > rows) seek(first_row(b));  // also where the rows end
     else advance();
@@ -444,15 +427,17 @@ __global__ __launch_bounds__(256, DB <= 1 ? 2 : 1) void attn_bwd_keys_kernel(con
     const uint32_t qd = lds_address(lds) + b % kStages * kStage, gd = qd + kTileBytes;
     const int i = x / 2;
     const uint32_t dst = (i * 256 + wave * 64) * 16;
-    if (x == 2 * kLoads) copy_word_to_lds(stats + stat_at, gd + kTileBytes);
-    else if (x % 2 == 0) copy_chunk_to_lds(q + q_at[i], qd + dst, lanes[i]);
+    if (x == 0 && wave == 0)
+      copy_word_to_lds(stats + min(first_row(b) + (int32_t)(lane & 31), rows - 1), gd + kTileBytes);
+    if (x % 2 == 0) copy_chunk_to_lds(q + q_at[i], qd + dst, lanes[i]);
     else copy_chunk_to_lds(g + g_at[i], gd + dst, lanes[i]);
   };
 
-  // The loop is pipelined over two blocks, because a wave is alone on its SIMD: while the
-  // matrix unit forms S and dP of the next block, the vector unit turns this block's into P
-  // and dS, a slice of them per step; then dV and dK follow, and between their last steps the
-  // block after the next is waited for.
+  // Above 64 columns the accumulators leave room for one wave on a SIMD, and the loop is
+  // pipelined over two blocks: while the matrix unit forms S and dP of the next block, the
+  // vector unit turns this block's into P and dS, a slice of them per step; then dV and dK
+  // follow, and before their last step the block after the next is waited for. Up to 64
+  // columns two waves share a SIMD, and a block is finished before the next is begun.
   f32x16 s, dp;         // of the block at hand, then of the next one
   f32x4 lse2[4], delta[4];
   x8<T> qr[KS], gr[KS];  // rows of the next block, the first two steps' from the round before
@@ -496,6 +481,12 @@ __global__ __launch_bounds__(256, DB <= 1 ? 2 : 1) void attn_bwd_keys_kernel(con
     const uint8_t* gt = qt + kTileBytes;
     const int32_t row0 = first_row(b);
     go_to(b + kStages - 1);
+    if constexpr (!kPipelined) {
+      wait_copies_and_sync<(kStages - 2) * kPieces>();  // block b; the buffer before it is free
+      read_stats(qt);
+      read_row(qt, 0);
+      read_row(qt, 1);
+    }
     if (row0 + BM > rows) {  // copies of the last row behind it: no weight
 #pragma unroll
       for (int i = 0; i < 16; ++i)
@@ -522,33 +513,43 @@ __global__ __launch_bounds__(256, DB <= 1 ? 2 : 1) void attn_bwd_keys_kernel(con
       gc[x] = read_columns<T, CPR>(gt, 16 * (x / DB), x % DB, lane);
       qc[x] = read_columns<T, CPR>(qt, 16 * (x / DB), x % DB, lane);
     };
-    f32x16 s_next, dp_next;
-    // eight pairs of rows over 2 KS half steps, and the copies
-    scores(buffer(b + 1), s_next, dp_next,
-           [&](int t) __attribute__((always_inline)) {
+    auto begin_copies = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-             for (int x = 16 * t / (2 * KS); x < 8 * (2 * t + 1) / (2 * KS); ++x) pair(x);
+      for (int x = t * kPerStep; x < (t + 1) * kPerStep && x < kPieces; ++x) piece(b + kStages - 1, x);
+    };
+    if constexpr (kPipelined) {
+      f32x16 s_next, dp_next;
+      // eight pairs of rows over 2 KS half steps, and the copies
+      scores(buffer(b + 1), s_next, dp_next,
+             [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-             for (int x = t * kPerStep; x < (t + 1) * kPerStep && x < kPieces; ++x)
-               piece(b + kStages - 1, x);
-           },
-           [&](int t) __attribute__((always_inline)) {
+               for (int x = 16 * t / (2 * KS); x < 8 * (2 * t + 1) / (2 * KS); ++x) pair(x);
+               begin_copies(t);
+             },
+             [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-             for (int x = 8 * (2 * t + 1) / (2 * KS); x < 8 * (2 * t + 2) / (2 * KS); ++x) pair(x);
-             if (t == KS - 1) {
-               read(0);
-               read(1);
-             }
-           });
-    s = s_next;
-    dp = dp_next;
-    read_stats(buffer(b + 1));
+               for (int x = 8 * (2 * t + 1) / (2 * KS); x < 8 * (2 * t + 2) / (2 * KS); ++x) pair(x);
+               if (t == KS - 1) {
+                 read(0);
+                 read(1);
+               }
+             });
+      s = s_next;
+      dp = dp_next;
+      read_stats(buffer(b + 1));
+    } else {
+      scores(qt, s, dp, begin_copies, [](int) {});
+      read(0);
+      read(1);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) pair(x);
+    }
     x8<T> wb, db;
 #pragma unroll
     for (int x = 0; x < 2 * DB; ++x) {
       step();
       if (x + 2 < 2 * DB) read(x + 2);
-      if (x == 2 * DB - 1) {
+      if (kPipelined && x == 2 * DB - 1) {
         // all of block b has been read: block b + 2 has arrived, and b's buffer is free
         wait_copies_and_sync<kPieces>();
         read_row(buffer(b + 2), 0);
@@ -588,13 +589,15 @@ __global__ __launch_bounds__(256, DB <= 1 ? 2 : 1) void attn_bwd_keys_kernel(con
     }
     settle<T>(kf);
     settle<T>(vf);
-    wait_copies_and_sync<kPieces>();  // blocks 0 and 1
-    read_row(buffer(0), 0);
-    read_row(buffer(0), 1);
-    scores(buffer(0), s, dp, [](int) {}, [](int) {});
-    read_stats(buffer(0));
-    read_row(buffer(1), 0);
-    read_row(buffer(1), 1);
+    if constexpr (kPipelined) {
+      wait_copies_and_sync<kPieces>();  // blocks 0 and 1
+      read_row(buffer(0), 0);
+      read_row(buffer(0), 1);
+      scores(buffer(0), s, dp, [](int) {}, [](int) {});
+      read_stats(buffer(0));
+      read_row(buffer(1), 0);
+      read_row(buffer(1), 1);
+    }
     // in careful mode every block is masked, for the rows behind the last
     const int32_t masked = decltype(mode)::value == kCareful ? blocks : partly;
     int32_t b = 0;
@@ -679,7 +682,7 @@ __global__ __launch_bounds__(256) void attn_bwd_join_kernel(const BwdParams p) {
 }
 
 // Shares of the dK/dV pass: the workgroups that 256 CUs hold at once.
-inline int32_t key_shares(int32_t D) { return D <= 32 ? 512 : 256; }
+inline int32_t key_shares(int32_t D) { return D <= 64 ? 512 : 256; }
 
 template <typename T, int DB>
 int32_t launch(const BwdParams& p, const PackedSizes& z, hipStream_t s) {
