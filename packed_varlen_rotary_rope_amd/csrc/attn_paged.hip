@@ -269,7 +269,6 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   const bool on = row < row_end;
   const int32_t clamped = on ? row : row_end - 1;
   const int32_t token = div31(clamped, p.by_g);
-  const int32_t head = kvh * p.G + (clamped - token * p.G);
   const int64_t most = min((int64_t)p.max_pages * p.page_size, (int64_t)kMostKeys);
   const int32_t key_end = (int32_t)min((int64_t)item.key_end, most);
   // visible keys of a token, 0 for none; within this split
@@ -285,10 +284,15 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   const int32_t* table = p.table + item.seq * p.table_stride;
   const uint8_t* kb = static_cast<const uint8_t*>(p.k_cache) + kvh * p.head_bytes;
   const uint8_t* vb = static_cast<const uint8_t*>(p.v_cache) + kvh * p.head_bytes;
-  const T* q_row = static_cast<const T*>(p.q) + (int64_t)(item.q0 + token) * p.q_stride +
-                   (int64_t)head * p.D;
-  T* out_row = out + (int64_t)(item.q0 + token) * p.out_stride + (int64_t)head * p.D;
-  const int64_t at_lse = (int64_t)(item.q0 + token) * p.Hq + head;
+  // Where this lane's row is in a tensor of token stride `stride` and `unit` values a head.
+  // `anew`: formed again, so that it takes no registers in between.
+  auto row_at = [&](int64_t stride, int32_t unit, bool anew) __attribute__((always_inline)) {
+    int32_t c = clamped;
+    if (anew) asm volatile("" : "+v"(c));
+    const int32_t tok = div31(c, p.by_g);
+    return (item.q0 + tok) * stride + (int64_t)(kvh * p.G + c - tok * p.G) * unit;
+  };
+  const T* q_row = static_cast<const T*>(p.q) + row_at(p.q_stride, p.D, false);
   const int32_t keys = key_end - item.key0;
   clear_unused_chunks<CPR>(lds, 4 * BN, chunks);
   __syncthreads();  // a wave's copies may land in what another clears
@@ -302,60 +306,64 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
     uint64_t lanes[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) lanes[i] = __ballot(chunk_of<CPR, 256>(i, tid) < chunks);
-    auto stage = [&](int32_t b) __attribute__((always_inline)) {
-      const uint32_t kd = lds_address(lds) + (b & 1) * 2 * kTileBytes;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const uint32_t r = row_of<CPR, 256>(i, tid), chunk = chunk_of<CPR, 256>(i, tid);
-        const uint32_t dst = kd + (i * 256 + wave * 64) * 16;
-        copy_chunk_to_lds(src.row(kb, b & 1, r) + 16 * chunk, dst, lanes[i]);
-        copy_chunk_to_lds(src.row(vb, b & 1, r) + 16 * chunk, dst + kTileBytes, lanes[i]);
-      }
+    // the x-th copy of block b
+    auto piece = [&](int32_t b, int x) __attribute__((always_inline)) {
+      const int i = x / 2;
+      const uint32_t dst = lds_address(lds) + ((b & 1) * 2 + x % 2) * kTileBytes + (i * 256 + wave * 64) * 16;
+      copy_chunk_to_lds(src.row(x % 2 ? vb : kb, b & 1, row_of<CPR, 256>(i, tid)) + 16 * chunk_of<CPR, 256>(i, tid),
+                        dst, lanes[i]);
     };
+    constexpr int kPieces = 2 * kLoads, kPerStep = (kPieces + 2 * DB - 1) / (2 * DB);
     // Two loops, so that neither body's registers are moved for the other's sake; the first
     // ends at the first block that is not wholly seen, or that has keys on no page.
     const int32_t all = wave_end > 0 ? max(0, wave_all - item.key0) / BN : 0;
     auto walk = [&](auto mode) __attribute__((always_inline)) {
       t.clear();
-      uint64_t hidden = 0, hidden_next = 0;
-      if (blocks > 0) {
-        src.fetch_pages(p, item.key0, 0, lane);
-        wait_copies<0>();
-        hidden_next = src.find_rows(p, item.key0, 0, lane);
-        src.fetch_pages(p, item.key0 + BN, 1, lane);
-        stage(0);
-      }
+      if (blocks <= 0) return;
+      uint64_t hidden = 0;
+      src.fetch_pages(p, item.key0, 0, lane);
+      wait_copies<0>();
+      uint64_t hidden_next = src.find_rows(p, item.key0, 0, lane);
+      src.fetch_pages(p, item.key0 + BN, 1, lane);
+#pragma unroll
+      for (int x = 0; x < kPieces; ++x) piece(0, x);
       settle<T>(t.q);
       int32_t b = 0;
+      // Behind the last block the last key's copies go on into the buffer that is not used.
       auto arrive = [&]() __attribute__((always_inline)) {
         const int32_t key0 = item.key0 + b * BN;
         wait_copies_and_sync<0>();  // block b has arrived, and its buffer's neighbour is free
         hidden = hidden_next;
-        if (b + 1 < blocks) {
-          hidden_next = src.find_rows(p, key0 + BN, (b + 1) & 1, lane);
-          src.fetch_pages(p, key0 + 2 * BN, b & 1, lane);
-          stage(b + 1);
-        }
+        hidden_next = src.find_rows(p, key0 + BN, (b + 1) & 1, lane);
+        src.fetch_pages(p, key0 + 2 * BN, b & 1, lane);
         return lds + (b & 1) * 2 * kTileBytes;
+      };
+      auto next = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+        for (int x = s * kPerStep; x < (s + 1) * kPerStep && x < kPieces; ++x) piece(b + 1, x);
       };
       for (; b < all && hidden_next == 0; ++b) {
         const uint8_t* kt = arrive();
-        t.template block<kWhole>(kt, kt + kTileBytes, item.key0 + b * BN, seen, 0, p.scale, lane, [](int) {});
+        t.template block<kWhole>(kt, kt + kTileBytes, item.key0 + b * BN, seen, 0, p.scale, lane, next);
       }
       for (; b < blocks; ++b) {
         const uint8_t* kt = arrive();
         const int32_t key0 = item.key0 + b * BN;
         if (key0 < wave_end)
           t.template block<Mode(decltype(mode)::value)>(kt, kt + kTileBytes, key0, seen, hidden, p.scale,
-                                                        lane, [](int) {});
+                                                        lane, next);
+        else
+#pragma unroll
+          for (int s = 0; s < 2 * DB; ++s) next(s);
       }
+      wait_copies<0>();
     };
     walk(Constant<kMasked>());
     if (any_wave(any_nonfinite(t.o), lds)) walk(Constant<kCareful>());
     if (item.slot < 0) {
       const float lse = t.finish();
-      store_row<T, DB>(t.o, out_row, half, chunks, on);
-      if (on && half == 0) p.lse[at_lse] = lse;
+      store_row<T, DB>(t.o, out + row_at(p.out_stride, p.D, true), half, chunks, on);
+      if (on && half == 0) p.lse[row_at(p.Hq, 1, true)] = lse;
       return;
     }
     const int64_t unit = ((int64_t)(item.slot + wave) * p.Hkv + kvh) * 32 + (lane & 31);

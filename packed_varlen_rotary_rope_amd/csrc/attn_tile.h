@@ -144,7 +144,8 @@ struct FwdTile {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int32_t j = 32 * b + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
-          if (key0 + j >= seen || (hidden >> j & 1)) s[b][i] = -__builtin_inff();
+          const uint32_t bits = (uint32_t)(hidden >> (32 * b)) >> (4 * half);
+          if (key0 + j >= seen || (bits >> (8 * (i / 4) + i % 4) & 1)) s[b][i] = -__builtin_inff();
         }
     }
     float top = s[0][0];
