@@ -55,14 +55,22 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 
 
-def _check(status: int, what: str) -> None:
+_HALF = (torch.bfloat16, torch.float16)
+_ANY = (torch.float32, torch.bfloat16, torch.float16)
+
+
+def _call(device: torch.device, fn, what: str, *args) -> None:
+    """fn(*args, stream) on `device` and its current stream."""
+    index = device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
     if status != 0:
         from . import RopeError
         raise RopeError(status, what)
-
-
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _ptr(t):
@@ -99,9 +107,17 @@ def _token_rows(t, name: str, dtypes) -> int:
     return t.stride(0) if T > 1 else H * D
 
 
-def _heads_last(t, name: str) -> int:
-    """_token_rows of a 16-bit tensor whose rows are aligned for 16-byte accesses."""
-    stride = _token_rows(t, name, (torch.bfloat16, torch.float16))
+def _heads_last(t, name: str, most: int = 256) -> int:
+    """_token_rows of a 16-bit tensor whose rows are aligned for 16-byte accesses and whose head
+    size the kernels take."""
+    shape, stride = t.shape, t.stride()
+    if (len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2] and stride[0] % 8 == 0 and
+            stride[0] >= shape[1] * shape[2] and t.data_ptr() % 16 == 0 and t.is_cuda and
+            t.dtype in _HALF and shape[2] % 8 == 0 and 8 <= shape[2] <= most):
+        return stride[0]
+    stride = _token_rows(t, name, _HALF)
+    if shape[2] % 8 or not 8 <= shape[2] <= most:
+        raise ValueError(f"head size {shape[2]}: expected a multiple of 8, 8 .. {most}")
     if t.data_ptr() % 16 or stride % 8:
         raise ValueError(f"{name}: data pointer and token stride must be multiples of 16 bytes")
     return stride
@@ -111,11 +127,6 @@ def _statistic(lse, q, T, Hq) -> None:
     if lse.dtype != torch.float32 or lse.device != q.device or tuple(lse.shape) != (T, Hq) or \
             not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous float32 [{T}, {Hq}] tensor on {q.device}")
-
-
-def _head_size(D: int, most: int) -> None:
-    if D % 8 or not 8 <= D <= most:
-        raise ValueError(f"head size {D}: expected a multiple of 8, 8 .. {most}")
 
 
 def _like(t, ref, shape, name: str):
@@ -135,16 +146,18 @@ class AttnPlan:
         self.buffer = buffer  # int32, on the GPU
 
     def _match(self, q, k, v):
-        if q.dim() != 3 or k.dim() != 3 or q.shape[0] != self.T:
+        qs, ks = q.shape, k.shape
+        if len(qs) != 3 or len(ks) != 3 or qs[0] != self.T:
             raise ValueError(f"expected q [{self.T}, Hq, D] and k, v [{self.T}, Hkv, D]")
-        if (q.shape[1], k.shape[1]) != (self.num_q_heads, self.num_kv_heads):
+        if qs[1] != self.num_q_heads or ks[1] != self.num_kv_heads:
             raise ValueError(f"the plan was made for {self.num_q_heads} query and "
                              f"{self.num_kv_heads} key/value heads")
-        if k.shape[0] != self.T or k.shape[2] != q.shape[2] or v.shape != k.shape:
+        if ks[0] != self.T or ks[2] != qs[2] or v.shape != ks:
             raise ValueError("k and v must be [T, Hkv, D] with q's T and D")
-        if k.dtype != q.dtype or v.dtype != q.dtype:
+        dtype, device = q.dtype, self.buffer.device
+        if k.dtype != dtype or v.dtype != dtype:
             raise TypeError("q, k and v must share one dtype")
-        if any(t.device != self.buffer.device for t in (q, k, v)):
+        if q.device != device or k.device != device or v.device != device:
             raise TypeError("q, k, v and the plan must be on one device")
 
 
@@ -171,72 +184,69 @@ def attn_plan(cu_seqlens, T: int, num_q_heads: int, num_kv_heads: int, seqused=N
     elif (out.T, out.num_seqs, out.num_q_heads, out.num_kv_heads, out.buffer.device) != \
             (T, num_seqs, Hq, Hkv, dev):
         raise ValueError("out: a plan of other sizes or of another device")
-    with torch.cuda.device(dev):
-        _check(_lib.attn_plan(_ptr(cu), num_seqs, _ptr(su), T, Hq, Hkv, _ptr(out.buffer), words,
-                              _stream(dev)), "attn_plan")
+    else:
+        torch.autograd.graph.increment_version(out.buffer)  # a backward that saved it shall know
+    _call(dev, _lib.attn_plan, "attn_plan", _ptr(cu), num_seqs, _ptr(su), T, Hq, Hkv,
+          _ptr(out.buffer), words)
     return out
 
 
-def attn_fwd(q, k, v, plan: AttnPlan, scale=None, out=None, lse=None):
+def attn_fwd(q, k, v, plan: AttnPlan, scale=None, out=None, lse=None, zero_rest=None):
     """Causal attention of the packed batch: q [T, Hq, D], k and v [T, Hkv, D] (bf16 or f16;
     views whose tokens hold their heads contiguously, e.g. parts of a fused projection), D a
     multiple of 8 up to 256, Hq a multiple of Hkv. scale: D ** -0.5 unless given. Returns
-    (out [T, Hq, D], lse float32 [T, Hq]). Rows of no sequence are 0 (-inf in lse) in new
-    outputs; a given `out` and `lse` keep theirs as they are."""
+    (out [T, Hq, D], lse float32 [T, Hq]), in the given ones or in new ones. zero_rest: whether
+    rows of no sequence are written as 0 (-inf in lse) or left as they are; by default new
+    outputs are written and given ones left."""
     plan._match(q, k, v)
-    strides = [_heads_last(t, name) for t, name in ((q, "q"), (k, "k"), (v, "v"))]
     T, Hq, D = q.shape
-    _head_size(D, 256)
+    strides = _heads_last(q, "q"), _heads_last(k, "k"), _heads_last(v, "v")
     if (out is None) != (lse is None):
         raise ValueError("give both out and lse, or neither")
-    fill = out is None
-    if fill:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    _like(out, q, (T, Hq, D), "out")
-    _statistic(lse, q, T, Hq)
-    out_stride = _heads_last(out, "out")
-    with torch.cuda.device(q.device):
-        _check(_lib.attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), T, Hq, k.shape[1], D,
-                             *strides, out_stride, _ptr(plan.buffer), plan.num_seqs,
-                             float(D ** -0.5 if scale is None else scale), _DTYPE_CODE[q.dtype],
-                             int(fill), _stream(q.device)), "attn_fwd")
+    fill = out is None if zero_rest is None else bool(zero_rest)
+    if out is None:
+        out = q.new_empty((T, Hq, D))
+        lse = q.new_empty((T, Hq), dtype=torch.float32)
+        out_stride = 0
+    else:
+        out_stride = _heads_last(_like(out, q, (T, Hq, D), "out"), "out")
+        _statistic(lse, q, T, Hq)
+    _call(q.device, _lib.attn_fwd, "attn_fwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), T, Hq, k.shape[1], D, *strides, out_stride, plan.buffer.data_ptr(),
+          plan.num_seqs, D ** -0.5 if scale is None else float(scale), _DTYPE_CODE[q.dtype], int(fill))
     return out, lse
 
 
-def attn_bwd(dout, q, k, v, out, lse, plan: AttnPlan, scale=None, dq=None, dk=None, dv=None):
+def attn_bwd(dout, q, k, v, out, lse, plan: AttnPlan, scale=None, dq=None, dk=None, dv=None,
+             zero_rest=None):
     """Gradients of attn_fwd for the upstream gradient dout [T, Hq, D], from its inputs and
-    outputs and the same scale; D up to 128. Deterministic (no atomics). New gradients have
-    zeros in rows of no sequence; given dq, dk and dv (all three, e.g. parts of one fused
-    gradient) keep theirs as they are. Returns (dq, dk, dv)."""
+    outputs and the same scale; D up to 128. Deterministic (no atomics). Returns (dq, dk, dv), in
+    the given ones (all three, e.g. parts of one fused gradient) or in new ones. zero_rest as in
+    attn_fwd."""
     plan._match(q, k, v)
     T, Hq, D = q.shape
     Hkv = k.shape[1]
-    _head_size(D, 128)
-    for t, name in ((dout, "dout"), (out, "out")):
-        _like(t, q, (T, Hq, D), name)
+    _like(dout, q, (T, Hq, D), "dout")
+    _like(out, q, (T, Hq, D), "out")
     _statistic(lse, q, T, Hq)
+    strides = [_heads_last(t, name, 128) for t, name in (
+        (dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"))]
     given = [g is not None for g in (dq, dk, dv)]
     if any(given) != all(given):
         raise ValueError("give all of dq, dk and dv, or none")
-    fill = not any(given)
-    if fill:
-        dq = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-        dk = torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device)
-        dv = torch.empty_like(dk)
-    _like(dq, q, (T, Hq, D), "dq")
-    _like(dk, q, (T, Hkv, D), "dk")
-    _like(dv, q, (T, Hkv, D), "dv")
-    strides = [_heads_last(t, name) for t, name in (
-        (dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"), (dq, "dq"), (dk, "dk"), (dv, "dv"))]
-    scratch = torch.empty(_lib.attn_bwd_scratch_floats(T, plan.num_seqs, Hq, Hkv, D),
-                          dtype=torch.float32, device=q.device)
-    with torch.cuda.device(q.device):
-        _check(_lib.attn_bwd(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(scratch),
-                             _ptr(dq), _ptr(dk), _ptr(dv), T, Hq, Hkv, D, *strides,
-                             _ptr(plan.buffer), plan.num_seqs,
-                             float(D ** -0.5 if scale is None else scale), _DTYPE_CODE[q.dtype],
-                             int(fill), _stream(q.device)), "attn_bwd")
+    fill = not any(given) if zero_rest is None else bool(zero_rest)
+    if not any(given):
+        dq, dk, dv = q.new_empty((T, Hq, D)), q.new_empty((T, Hkv, D)), q.new_empty((T, Hkv, D))
+        strides += [0, 0, 0]
+    else:
+        strides += [_heads_last(_like(t, q, (T, h, D), name), name, 128)
+                    for t, h, name in ((dq, Hq, "dq"), (dk, Hkv, "dk"), (dv, Hkv, "dv"))]
+    scratch = q.new_empty(_lib.attn_bwd_scratch_floats(T, plan.num_seqs, Hq, Hkv, D),
+                          dtype=torch.float32)
+    _call(q.device, _lib.attn_bwd, "attn_bwd", dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          out.data_ptr(), lse.data_ptr(), scratch.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+          dv.data_ptr(), T, Hq, Hkv, D, *strides, plan.buffer.data_ptr(), plan.num_seqs,
+          D ** -0.5 if scale is None else float(scale), _DTYPE_CODE[q.dtype], int(fill))
     return dq, dk, dv
 
 
@@ -244,18 +254,19 @@ def attn_bwd(dout, q, k, v, out, lse, plan: AttnPlan, scale=None, dq=None, dk=No
 
 def _caches(k_cache, v_cache, ref):
     """Checked caches [num_pages, page_size, Hkv, D] of one layout; their strides."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != ref.dtype or t.device != ref.device:
-            raise TypeError(f"{name}: dtype or device differs from the new tokens'")
-        if t.dim() != 4:
-            raise ValueError(f"{name}: expected [num_pages, page_size, Hkv, D]")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    stride = k_cache.stride()
+    if k_cache.dtype != ref.dtype or v_cache.dtype != ref.dtype or k_cache.device != ref.device or \
+            v_cache.device != ref.device:
+        raise TypeError("k_cache or v_cache: dtype or device differs from the new tokens'")
+    if len(stride) != 4:
+        raise ValueError("k_cache: expected [num_pages, page_size, Hkv, D]")
+    if k_cache.shape != v_cache.shape or stride != v_cache.stride():
         raise ValueError("k_cache and v_cache must have one shape and layout")
     if k_cache.shape[0] < 1 or k_cache.shape[1] < 1:
         raise ValueError("the cache needs at least one page of at least one slot")
-    if k_cache.shape[3] > 1 and k_cache.stride(3) != 1:
+    if k_cache.shape[3] > 1 and stride[3] != 1:
         raise ValueError("the D elements of a cache row must be contiguous")
-    return k_cache.stride()[:3]
+    return stride[:3]
 
 
 def _table(block_table, num_seqs, device):
@@ -281,13 +292,12 @@ def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: 
     Tokens at a negative position, of no sequence, behind the table or on a page number that
     is no page are not appended. Returns the rotated q, in q_out (a new tensor if None; may be
     q itself), or None without q."""
-    dtypes = (torch.float32, torch.bfloat16, torch.float16)
     if k.dim() != 3 or k.shape != v.shape:
         raise ValueError("expected k and v [T, Hkv, D]")
     if v.dtype != k.dtype or v.device != k.device:
         raise TypeError("k and v must share one dtype and device")
     dev = k.device
-    strides = [_token_rows(t, name, dtypes) for t, name in ((k, "k"), (v, "v"))]
+    k_stride, v_stride = _token_rows(k, "k", _ANY), _token_rows(v, "v", _ANY)
     T, Hkv, D = k.shape
     Hq, q_stride, out_stride = 0, 0, 0
     if q is not None:
@@ -297,9 +307,10 @@ def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: 
             raise ValueError("expected q [T, Hq, D] with k's T and D")
         Hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-        q_stride = _token_rows(q, "q", dtypes)
-        out_stride = _token_rows(_like(q_out, q, q.shape, "q_out"), "q_out", dtypes)
+            q_out, out_stride = q.new_empty((T, Hq, D)), Hq * D
+        else:
+            out_stride = _token_rows(_like(q_out, q, q.shape, "q_out"), "q_out", _ANY)
+        q_stride = _token_rows(q, "q", _ANY)
     elif q_out is not None:
         raise ValueError("q_out without q")
     cache_strides = _caches(k_cache, v_cache, k)
@@ -311,12 +322,11 @@ def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: 
         raise ValueError("cu_seqlens needs at least one entry")
     lens = _index(kv_lens, "kv_lens", dev, num_seqs)
     per, table_stride = _table(block_table, num_seqs, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.kv_append(_ptr(q), _ptr(q_out), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), T,
-                              Hq, Hkv, D, q_stride, out_stride, *strides, k_cache.shape[0],
-                              k_cache.shape[1], *cache_strides, _ptr(block_table), per,
-                              table_stride, _ptr(cu), num_seqs, _ptr(lens), float(theta),
-                              float(pos_scale), _DTYPE_CODE[k.dtype], _stream(dev)), "kv_append")
+    _call(dev, _lib.kv_append, "kv_append", _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), T, Hq, Hkv, D, q_stride, out_stride, k_stride,
+          v_stride, k_cache.shape[0], k_cache.shape[1], *cache_strides, block_table.data_ptr(), per,
+          table_stride, cu.data_ptr(), num_seqs, lens.data_ptr(), float(theta), float(pos_scale),
+          _DTYPE_CODE[k.dtype])
     return q_out
 
 
@@ -352,46 +362,44 @@ def paged_plan(cu_seqlens, kv_lens, T: int, num_q_heads: int, num_kv_heads: int,
     elif (out.T, out.num_seqs, out.num_q_heads, out.num_kv_heads, out.buffer.device) != \
             (T, num_seqs, Hq, Hkv, dev):
         raise ValueError("out: a plan of other sizes or of another device")
-    with torch.cuda.device(dev):
-        _check(_lib.paged_plan(_ptr(cu), num_seqs, _ptr(lens), T, Hq, Hkv, _ptr(out.buffer), words,
-                               _stream(dev)), "paged_plan")
+    _call(dev, _lib.paged_plan, "paged_plan", _ptr(cu), num_seqs, _ptr(lens), T, Hq, Hkv,
+          _ptr(out.buffer), words)
     return out
 
 
-def attn_paged(q, k_cache, v_cache, block_table, plan: PagedPlan, scale=None, out=None, lse=None):
+def attn_paged(q, k_cache, v_cache, block_table, plan: PagedPlan, scale=None, out=None, lse=None,
+               zero_rest=None):
     """Attention of the new tokens q [T, Hq, D] (bf16 or f16, D a multiple of 8 up to 256) over
     the paged caches [num_pages, page_size, Hkv, D] that hold their sequences (kv_append_),
     causal among themselves; block_table as there, plan from paged_plan. Keys behind the table
     or on a page number that is no page are seen by no query. Returns (out [T, Hq, D], lse
-    float32 [T, Hq]); a query that sees no key, and rows of no sequence, get 0 (-inf in lse) in
-    new outputs; a given `out` and `lse` keep rows of no sequence as they are."""
+    float32 [T, Hq]), in the given ones or in new ones; a query that sees no key gets 0 (-inf in
+    lse). zero_rest, for rows of no sequence, as in attn_fwd."""
     q_stride = _heads_last(q, "q")
     T, Hq, D = q.shape
-    _head_size(D, 256)
     if T != plan.T or Hq != plan.num_q_heads or q.device != plan.buffer.device:
         raise ValueError("the plan was made for other new tokens, query heads or another device")
-    cache_strides = _caches(k_cache, v_cache, q)
+    page_stride, slot_stride, head_stride = _caches(k_cache, v_cache, q)
     num_pages, page_size, Hkv, cache_d = k_cache.shape
     if Hkv != plan.num_kv_heads or cache_d != D:
         raise ValueError("the cache must have the plan's key/value heads and q's head size")
-    if any(st % 8 for st in cache_strides) or k_cache.data_ptr() % 16 or v_cache.data_ptr() % 16:
+    if (page_stride | slot_stride | head_stride) % 8 or k_cache.data_ptr() % 16 or v_cache.data_ptr() % 16:
         raise ValueError("the cache's data pointers and strides must be multiples of 16 bytes")
     per, table_stride = _table(block_table, plan.num_seqs, q.device)
     if (out is None) != (lse is None):
         raise ValueError("give both out and lse, or neither")
-    fill = out is None
-    if fill:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    out_stride = _heads_last(_like(out, q, (T, Hq, D), "out"), "out")
-    _statistic(lse, q, T, Hq)
-    space = torch.empty(_lib.paged_workspace_floats(T, plan.num_seqs, Hq, Hkv, D),
-                        dtype=torch.float32, device=q.device)
-    with torch.cuda.device(q.device):
-        _check(_lib.attn_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(space),
-                               T, Hq, Hkv, D, q_stride, out_stride, num_pages, page_size,
-                               *cache_strides, _ptr(block_table), per, table_stride,
-                               _ptr(plan.buffer), plan.num_seqs,
-                               float(D ** -0.5 if scale is None else scale), _DTYPE_CODE[q.dtype],
-                               int(fill), _stream(q.device)), "attn_paged")
+    fill = out is None if zero_rest is None else bool(zero_rest)
+    if out is None:
+        out = q.new_empty((T, Hq, D))
+        lse = q.new_empty((T, Hq), dtype=torch.float32)
+        out_stride = 0
+    else:
+        out_stride = _heads_last(_like(out, q, (T, Hq, D), "out"), "out")
+        _statistic(lse, q, T, Hq)
+    space = q.new_empty(_lib.paged_workspace_floats(T, plan.num_seqs, Hq, Hkv, D), dtype=torch.float32)
+    _call(q.device, _lib.attn_paged, "attn_paged", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          out.data_ptr(), lse.data_ptr(), space.data_ptr(), T, Hq, Hkv, D, q_stride, out_stride,
+          num_pages, page_size, page_stride, slot_stride, head_stride, block_table.data_ptr(), per,
+          table_stride, plan.buffer.data_ptr(), plan.num_seqs,
+          D ** -0.5 if scale is None else float(scale), _DTYPE_CODE[q.dtype], int(fill))
     return out, lse

@@ -154,8 +154,9 @@ struct FwdTile {
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[b][i]);
     top = half_max(top) * scale;
-    if (__any(!(top - m <= kRescale))) {
-      const float m_new = __builtin_fmaxf(m, top);
+    const bool rises = !(top - m <= kRescale);
+    if (__any(rises)) {  // for the rows that need it: a row's bits do not depend on others
+      const float m_new = rises ? __builtin_fmaxf(m, top) : m;
       const float a = m == m_new ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
       m = m_new;
       l *= a;

@@ -1,5 +1,5 @@
-"""Autograd entry points over the C ABI: the packed-varlen QK rotary embedding
-and the SwiGLU / GeGLU activations as differentiable torch functions.
+"""Autograd entry points over the C ABI: the packed-varlen QK rotary embedding, the
+packed attention and the SwiGLU / GeGLU activations as differentiable torch functions.
 
 Every pass is one launch of the library's kernels on the current stream (a long
 pass: several, over consecutive ranges); this module only wires them into
@@ -10,6 +10,8 @@ torch.autograd (no arithmetic of its own).
     q, k = rope_qk(q, k, cu, theta, seqused=su,    # padded layout, launched over its
                    cu_valid=valid_prefix(cu, su), valid_tokens=n)  # n rotated tokens only
     q, k = rope_qk_table(q, k, cos_tab, sin_tab, cu_seqlens)  # cos/sin from tables
+    o = attn_qkv(qkv, Hq, Hkv, plan)               # attention of a fused QKV output
+    o = attn(q, k, v, plan)                        # plan = attn_plan(cu, T, Hq, Hkv), once a batch
     h = glu("swiglu", e, g)                        # h = silu(e) * g
     h = glu_fused("geglu", gate_up)                # e, g = halves of gate_up
 
@@ -35,7 +37,8 @@ from __future__ import annotations
 
 import torch
 
-from . import glu_bwd, glu_fwd, qk_apply_ex_, qk_apply_padded_, qk_apply_table_
+from . import (attn_bwd, attn_fwd, attn_plan, glu_bwd, glu_fwd, qk_apply_ex_, qk_apply_padded_,
+               qk_apply_table_)
 
 
 def _rotate(q, k, theta, direction, cu, su, pid, so, pos_scale, cv, valid):
@@ -200,6 +203,97 @@ def rope_qk_table(q: torch.Tensor, k: torch.Tensor, cos_tab: torch.Tensor, sin_t
     through unchanged, and so do their gradients."""
     return _RopeQKTable.apply(_own_storage(q), _own_storage(k), cos_tab, sin_tab, cu_seqlens,
                               seqused, position_ids, seq_offsets, bool(inplace_backward))
+
+
+def _rows_for_kernel(t: torch.Tensor) -> torch.Tensor:
+    """t itself where the attention kernels take its layout, else a contiguous copy (upstream
+    gradients come in any layout, expanded ones among them)."""
+    T, H, D = t.shape
+    if t.stride(2) == 1 and t.stride(1) == D and t.stride(0) % 8 == 0 and t.stride(0) >= H * D and \
+            t.data_ptr() % 16 == 0:
+        return t
+    return t.contiguous()
+
+
+def _plan_of(plan, cu_seqlens, seqused, T, Hq, Hkv):
+    if plan is None:
+        if cu_seqlens is None:
+            raise ValueError("give a plan or cu_seqlens")
+        return attn_plan(cu_seqlens, T, Hq, Hkv, seqused=seqused)
+    if cu_seqlens is not None or seqused is not None:
+        raise ValueError("a plan holds the sequences: give it or cu_seqlens (and seqused), not both")
+    return plan
+
+
+class _Attn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, plan, scale):
+        out, lse = attn_fwd(q, k, v, plan, scale)
+        # the plan's buffer too: autograd notices where it has been written over since
+        ctx.save_for_backward(q, k, v, out, lse, plan.buffer)
+        ctx.plan, ctx.scale = plan, scale
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, out, lse, _ = ctx.saved_tensors
+        dq, dk, dv = attn_bwd(_rows_for_kernel(dout), q, k, v, out, lse, ctx.plan, ctx.scale)
+        return dq, dk, dv, None, None
+
+
+def attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan=None, cu_seqlens=None,
+         scale=None, seqused=None) -> torch.Tensor:
+    """Differentiable causal attention of a packed batch: q [T, Hq, D], k and v [T, Hkv, D]
+    (bf16 or f16, views with contiguous heads, D a multiple of 8 up to 128, without gradients 256), by the sequences
+    of `plan` (``attn_plan``, made once per batch for every layer) or of cu_seqlens (with
+    optional seqused; a plan is made here then). Rows of no sequence get 0, and so do their
+    gradients. Returns [T, Hq, D]."""
+    _head_sizes(q.shape[-1], q, k, v)
+    plan = _plan_of(plan, cu_seqlens, seqused, q.shape[0], q.shape[1], k.shape[1])
+    return _Attn.apply(q, k, v, plan, None if scale is None else float(scale))
+
+
+def _head_sizes(D: int, *inputs) -> None:
+    if D > 128 and torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
+        raise ValueError(f"head size {D}: gradients are for head sizes up to 128")
+
+
+def _qkv_heads(qkv: torch.Tensor, Hq: int, Hkv: int):
+    """(q, k, v) views of a fused projection output."""
+    q, k = _qkv_split(qkv, Hq, Hkv)
+    flat = qkv.flatten(1) if qkv.dim() == 3 else qkv
+    return q, k, flat[:, (Hq + Hkv) * q.shape[2]:].unflatten(1, (Hkv, q.shape[2]))
+
+
+class _AttnQKV(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, qkv, Hq, Hkv, plan, scale):
+        q, k, v = _qkv_heads(qkv, Hq, Hkv)
+        out, lse = attn_fwd(q, k, v, plan, scale)
+        ctx.save_for_backward(qkv, out, lse, plan.buffer)
+        ctx.heads, ctx.plan, ctx.scale = (Hq, Hkv), plan, scale
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        qkv, out, lse, _ = ctx.saved_tensors
+        q, k, v = _qkv_heads(qkv, *ctx.heads)
+        grad = torch.empty_like(qkv, memory_format=torch.contiguous_format)
+        dq, dk, dv = _qkv_heads(grad, *ctx.heads)
+        attn_bwd(_rows_for_kernel(dout), q, k, v, out, lse, ctx.plan, ctx.scale, dq, dk, dv,
+                 zero_rest=True)
+        return grad, None, None, None, None
+
+
+def attn_qkv(qkv: torch.Tensor, num_q_heads: int, num_kv_heads: int, plan=None, cu_seqlens=None,
+             scale=None, seqused=None) -> torch.Tensor:
+    """attn() on the Q, K and V heads of a fused projection output, as ``rope_qkv`` takes and
+    returns it; the gradient is one tensor of its shape, which rope_qkv's backward may rotate in
+    place. Returns [T, Hq, D]."""
+    Hq, Hkv = int(num_q_heads), int(num_kv_heads)
+    _head_sizes(_qkv_split(qkv, Hq, Hkv)[0].shape[2], qkv)
+    plan = _plan_of(plan, cu_seqlens, seqused, qkv.shape[0], Hq, Hkv)
+    return _AttnQKV.apply(qkv, Hq, Hkv, plan, None if scale is None else float(scale))
 
 
 class _Glu(torch.autograd.Function):

@@ -138,3 +138,230 @@ def test_append(rope, case, form):
 
     assert same(kc, want_kc) and same(vc, want_vc)
     assert got is None if form == "keys_only" else same(got, want_q)
+
+
+def bits(t):
+    return t.contiguous().view(torch.int32 if t.dtype == F32 else torch.int16)
+
+
+def same(a, b):
+    return torch.equal(bits(a), bits(b))
+
+
+@pytest.mark.parametrize("new,held", [([1, 1], [500, 77]), ([300, 1], [500, 77]), ([40], [120])])
+def test_pages_that_are_none(rope, new, held):
+    """Page numbers out of range anywhere in a sequence, and tables shorter than what a sequence
+    holds: those keys are seen by nobody, the others as ever."""
+    print(f"[pages] {new} {held}", flush=True)
+    Hq, Hkv, D, page = 8, 2, 64, 16
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    k, v, table = pool(held, page, Hkv, D, BF16, 4)
+    table[0, 1], table[0, 3], table[-1, 2] = -1, k.shape[0], 2 ** 31 - 1
+    q = normal((cu[-1], Hq, D), 3, BF16)
+    plan = rope.paged_plan(int32(cu), int32(held), cu[-1], Hq, Hkv)
+    for t in (table, table[:, :4], table[:, :1], table[:, :0]):
+        out, lse = rope.attn_paged(q, k, v, t, plan)
+        want, wlse, tol = ref.paged(q, k, v, t, cu, held, D ** -0.5)
+        ref.check(out, want, tol, f"out, {t.shape[1]} pages")
+        assert torch.equal(lse == float("-inf"), wlse == float("-inf"))
+
+
+def test_tokens_that_are_not_appended(rope):
+    """No page, behind the table, negative positions, rows of no sequence: the cache keeps its
+    bits there, q is rotated where it has a position and copied where it has none."""
+    Hq, Hkv, D, page = 4, 2, 64, 16
+    kc, vc = normal((6, page, Hkv, D), 1, BF16), normal((6, page, Hkv, D), 2, BF16)
+    table = int32([[0, -1, 2], [3, 6, 4]])
+    cu, lens, T = [2, 42, 60], [40, 50], 64     # rows 0, 1 and 60 .. 63 belong to nobody
+    q, k, v = normal((T, Hq, D), 3, BF16), normal((T, Hkv, D), 4, BF16), normal((T, Hkv, D), 5, BF16)
+    want_kc, want_vc, want_q, turned = kc.clone(), vc.clone(), q.clone(), k.clone()
+    pos = torch.full((T,), -1, dtype=torch.int32)
+    pos[2:42], pos[42:60] = torch.arange(40), torch.arange(32, 50)
+    rope.qk_apply_ex_(want_q, turned, 1e4, 1, position_ids=pos.to(DEV))
+    for t in range(T):
+        p, s = int(pos[t]), 0 if t < 42 else 1
+        if p >= 0 and p // page < 3 and 0 <= int(table[s, p // page]) < 6:
+            want_kc[int(table[s, p // page]), p % page] = turned[t]
+            want_vc[int(table[s, p // page]), p % page] = v[t]
+    got = rope.kv_append_(k, v, kc, vc, table, int32(cu), int32(lens), 1e4, q=q)
+    assert same(kc, want_kc) and same(vc, want_vc) and same(got, want_q)
+    # more new tokens than held ones: the first of them have no position
+
+    got = rope.kv_append_(k, v, kc, vc, table[:1], int32([0, 10]), int32([4]), 1e4, q=q)
+    assert same(got[:6], q[:6]) and same(got[10:], q[10:]) and not same(got[8:10], q[8:10])
+    assert same(kc[3:], want_kc[3:])
+    # no sequence at all
+    got = rope.kv_append_(k, v, kc, vc, table[:0], int32([0]), int32([]), 1e4, q=q)
+    assert same(got, q)
+
+
+def test_refusals(rope):
+    kc, vc = normal((4, 16, 2, 64), 1, BF16), normal((4, 16, 2, 64), 2, BF16)
+    q, k, v = normal((3, 4, 64), 3, BF16), normal((3, 2, 64), 4, BF16), normal((3, 2, 64), 5, BF16)
+    table, cu, lens = int32([[0, 1]]), int32([0, 3]), int32([9])
+
+    def append(**kw):
+        a = dict(k=k, v=v, k_cache=kc, v_cache=vc, block_table=table, cu_seqlens=cu, kv_lens=lens, theta=1e4)
+        a.update(kw)
+        return rope.kv_append_(**a)
+
+    for kw in (dict(k=k.half()), dict(v=v.cpu()), dict(k_cache=kc.half()), dict(kv_lens=lens.long()),
+               dict(q=q.half()), dict(block_table=table.long())):
+        with pytest.raises(TypeError):
+            append(**kw)
+    for kw in (dict(v=v[:2]), dict(k_cache=kc[:3]), dict(v_cache=vc.transpose(1, 2)), dict(kv_lens=int32([1, 2])),
+               dict(q=q[:2]), dict(q_out=q), dict(block_table=int32([[0], [1]])), dict(k=k[:, :1], v=v[:, :1]),
+               dict(q=q[:, :, ::2], q_out=None)):
+        with pytest.raises(ValueError):
+            append(**kw)
+    for kw in (dict(theta=0.1), dict(pos_scale=0.5)):
+        with pytest.raises(rope.RopeError):
+            append(**kw)
+    plan = rope.paged_plan(cu, lens, 3, 4, 2)
+    with pytest.raises(TypeError):
+        rope.attn_paged(q.float(), kc.float(), vc.float(), table, plan)
+    for a in ((q[:2], kc, vc, table, plan), (q[:, :2], kc, vc, table, plan), (q, kc, vc[:3], table, plan),
+              (q, kc[:, :, :1], vc[:, :, :1], table, plan), (q, kc, vc, int32([[0], [1]]), plan),
+              (q, kc[..., :60], vc[..., :60], table, plan)):
+        with pytest.raises(ValueError):
+            rope.attn_paged(*a)
+    with pytest.raises(ValueError):
+        rope.paged_plan(cu, lens, 3, 4, 3)
+    with pytest.raises(ValueError):
+        rope.paged_plan(cu, lens, 4, 4, 2, out=plan)
+
+
+def test_plan_of_another_batch_writes_nothing(rope):
+    kc = normal((4, 16, 2, 64), 1, BF16)
+    q = normal((3, 4, 64), 3, BF16)
+    other = rope.paged_plan(int32([0, 5]), int32([9]), 5, 4, 2)
+    fake = rope.PagedPlan(3, 1, 4, 2, other.buffer)
+    out, lse = torch.full_like(q, 3.0), torch.full((3, 4), 3.0, device=DEV)
+    rope.attn_paged(q, kc, kc, int32([[0, 1]]), fake, out=out, lse=lse)
+    assert bool((out == 3).all()) and bool((lse == 3).all())
+
+
+def test_rows_of_no_sequence(rope):
+    held = [30, 700]
+    k, v, table = pool(held, 16, 2, 64, BF16, 2)
+    q = normal((400, 4, 64), 3, BF16)
+    q[:3] = q[250:] = float("nan")
+    plan = rope.paged_plan(int32([3, 4, 250]), int32(held), 400, 4, 2)
+    out, lse = rope.attn_paged(q, k, v, table, plan)
+    want, wlse, tol = ref.paged(torch.nan_to_num(q), k, v, table, [3, 4, 250], held, 0.125)
+    ref.check(out, want, tol, "out")
+    keep = torch.full_like(q, 5.0), torch.full((400, 4), 5.0, device=DEV)
+    rope.attn_paged(q, k, v, table, plan, out=keep[0], lse=keep[1])
+    assert same(keep[0][3:250], out[3:250]) and bool((keep[0][250:] == 5).all()) and bool((keep[1][:3] == 5).all())
+
+
+@pytest.mark.parametrize("D,page,chunks", [(128, 16, [150, 1, 1, 64, 1, 33, 1]), (80, 7, [1, 1, 300, 2, 5]),
+                                           (64, 64, [257, 31, 1])])
+def test_serving_a_sequence(rope, D, page, chunks):
+    """A prompt in chunks and single tokens, through append and paged attention with one plan
+    buffer: every step's output against the packed attention's definition over the whole
+    sequence, rotated once by the packed rotation."""
+    print(f"[serving] D={D} page={page} {chunks}", flush=True)
+    Hq, Hkv, T = 8, 2, sum(chunks)
+    q, k, v = normal((T, Hq, D), 1, BF16), normal((T, Hkv, D), 2, BF16), normal((T, Hkv, D), 3, BF16)
+    rq, rk = q.clone(), k.clone()
+    rope.qk_fwd_(rq, rk, int32([0, T]), 1e5)
+    want, _, tol = ref.forward(rq, rk, v, [(0, T)], D ** -0.5)
+    pages = -(-T // page)
+    g = torch.Generator().manual_seed(1)
+    table = torch.randperm(pages + 4, generator=g)[:pages].int()[None].to(DEV)
+    kc = torch.full((pages + 4, page, Hkv, D), float("nan"), dtype=BF16, device=DEV)
+    vc = kc.clone()
+    at = 0
+    for n in chunks:
+        cu, lens = int32([0, n]), int32([at + n])
+        tq = rope.kv_append_(k[at:at + n], v[at:at + n], kc, vc, table, cu, lens, 1e5, q=q[at:at + n])
+        assert same(tq, rq[at:at + n])
+        out, _ = rope.attn_paged(tq, kc, vc, table, rope.paged_plan(cu, lens, n, Hq, Hkv))
+        ref.check(out, want[at:at + n], tol[at:at + n], f"tokens {at} .. {at + n}")
+        at += n
+
+
+def test_captured_decode_step(rope):
+    """Append, plan and attention of one step in a HIP graph, replayed with growing lengths."""
+    B, Hq, Hkv, D, page = 5, 8, 2, 128, 16
+    lens0 = [1, 15, 16, 700, 2047]
+    kc, vc, _ = pool([m + 8 for m in lens0], page, Hkv, D, BF16, 6)
+    _, _, table = pool([m + 8 for m in lens0], page, Hkv, D, BF16, 6)
+    q, k, v = normal((B, Hq, D), 1, BF16), normal((B, Hkv, D), 2, BF16), normal((B, Hkv, D), 3, BF16)
+    cu, lens = int32(list(range(B + 1))), int32(lens0)
+    plan = rope.paged_plan(cu, lens, B, Hq, Hkv)
+
+    def step(caches, plan):
+        tq = rope.kv_append_(k, v, *caches, table, cu, lens, 1e4, q=q)
+        rope.paged_plan(cu, lens, B, Hq, Hkv, out=plan)
+        return rope.attn_paged(tq, *caches, table, plan)
+
+    step((kc.clone(), vc.clone()), plan)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = step((kc, vc), plan)
+    for i in range(4):
+        lens.copy_(int32([m + i for m in lens0]))
+        q.copy_(normal((B, Hq, D), 50 + i, BF16))
+        k.copy_(normal((B, Hkv, D), 60 + i, BF16))
+        eager = kc.clone(), vc.clone()
+        graph.replay()
+        want = step(eager, rope.paged_plan(cu, lens, B, Hq, Hkv))
+        torch.cuda.synchronize()
+        assert same(out, want[0]) and same(lse, want[1]) and same(kc, eager[0]) and same(vc, eager[1])
+
+
+def test_repeatable_and_concurrent(rope):
+    """The same bits every time, with one plan in use on two streams at once."""
+    held, new = [3000, 40, 900, 1], [1, 40, 200, 1]
+    cu = [0, 1, 41, 241, 242]
+    k, v, table = pool(held, 32, 2, 64, BF16, 8)
+    q = normal((242, 8, 64), 1, BF16)
+    assert len(new) == 4
+    plan = rope.paged_plan(int32(cu), int32(held), 242, 8, 2)
+    want = rope.attn_paged(q, k, v, table, plan)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        got = []
+        for st in streams:
+            with torch.cuda.stream(st):
+                got += rope.attn_paged(q, k, v, table, plan)
+        # another plan of the same step has its items and slots in another order
+        got += rope.attn_paged(q, k, v, table, rope.paged_plan(int32(cu), int32(held), 242, 8, 2))
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(got, want * 3))
+
+
+def test_offsets_beyond_32_bits(rope):
+    """A cache of more than 2^31 elements: pages from its far end, written by the append and read
+    by the attention."""
+    print("[64-bit offsets]", flush=True)
+    pages, page, Hkv, D, Hq = 140000, 16, 8, 128, 32
+    kc = torch.zeros((pages, page, Hkv, D), dtype=BF16, device=DEV)
+    vc = torch.zeros_like(kc)
+    n = 50
+    table = int32([[pages - 1, 7, pages - 3, 131072], [pages - 2, 1, 131073, 2]])
+    q, k, v = normal((2 * n, Hq, D), 1, BF16), normal((2 * n, Hkv, D), 2, BF16), normal((2 * n, Hkv, D), 3, BF16)
+    cu, lens = int32([0, n, 2 * n]), int32([n, n])
+    tq = rope.kv_append_(k, v, kc, vc, table, cu, lens, 1e4, q=q)
+    rq, rk = q.clone(), k.clone()
+    rope.qk_fwd_(rq, rk, cu, 1e4)
+    assert same(tq, rq)
+    at = torch.arange(n, device=DEV)
+    for s in range(2):
+        where = table[s].long()[at // page], at % page
+        assert same(kc[where], rk[s * n:(s + 1) * n]) and same(vc[where], v[s * n:(s + 1) * n])
+    out, _ = rope.attn_paged(tq, kc, vc, table, rope.paged_plan(cu, lens, 2 * n, Hq, Hkv))
+    want, _, tol = ref.forward(rq, rk, v, [(0, n), (n, n)], D ** -0.5)
+    ref.check(out, want, tol, "out")
+    # decode, and a stride that a combined cache of keys and values has
+    both = torch.zeros((64, 2, page, Hkv, D), dtype=BF16, device=DEV)
+    t2 = int32([[63, 0, 30, 1]])
+    rope.kv_append_(k[:n], v[:n], both[:, 0], both[:, 1], t2, int32([0, n]), int32([n]), 1e4)
+    out1, _ = rope.attn_paged(rq[n - 1:n], both[:, 0], both[:, 1], t2,
+                              rope.paged_plan(int32([0, 1]), int32([n]), 1, Hq, Hkv))
+    ref.check(out1, want[n - 1:n], tol[n - 1:n], "one token")
