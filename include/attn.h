@@ -16,12 +16,12 @@
  * query does not see have no influence on its outputs, whatever they hold
  * (infinities and NaN among it), and queries that do not see a key none on its gradients.
  * Products are formed on the matrix cores from the storage type into fp32; the softmax and
- * its sums are fp32; the weights are rounded to the storage type before they meet V, and
- * outputs once at the end. Results do not depend on the order of execution: no atomics.
+ * its sums are fp32; the weights (and dS, backward) are rounded to the storage type before the
+ * second product, and outputs once at the end. In f16 a dS past 65504 overflows there. Results do not depend on the order of execution: no atomics.
  *
  * Layouts. Rows are [token][head][D], the heads of a token contiguous; every tensor has a
- * token stride in elements (0 = heads * D), so q, k and v may be views of one fused
- * projection. D is a multiple of 8, 8 .. 256 (backward: 8 .. 128). Data pointers are
+ * token stride in elements (0 = heads * D, else at least that: tokens do not overlap), so q, k
+ * and v may be views of one fused projection. D is a multiple of 8, 8 .. 256 (backward: 8 .. 128). Data pointers are
  * 16-byte aligned and strides multiples of 8 elements, below 2^24. dtype is ROPE_BF16 or
  * ROPE_F16 (the append takes ROPE_F32 too). lse is float [T][Hq].
  *
@@ -69,7 +69,7 @@ int32_t attn_plan(const int32_t* cu_seqlens, int32_t num_seqs, const int32_t* se
  *  q, k, v     device [T][Hq][D], [T][Hkv][D], [T][Hkv][D], read
  *  out, lse    device [T][Hq][D] and float [T][Hq], written
  *  plan        written by attn_plan for the same T, num_seqs, Hq and Hkv. Where it was made
- *              for others, memory stays safe and nothing is written.
+ *              for others, or by paged_plan, memory stays safe and nothing is written.
  *  scale       positive, and times log2 e within 1e-37 .. 3e38; usually D^-0.5
  *  fill        rows of no sequence: 0 leaves out and lse as they are, 1 writes out = 0 and
  *              lse = -inf */
@@ -114,6 +114,7 @@ int32_t attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
  *              they are.
  *  k, v        device [T][Hkv][D], read; tokens at no position, behind the table's last
  *              page or on no page are not written to the cache
+ *  T           0 .. 8388607 (a workgroup each); Hq 0 .. 4096, Hkv 1 .. 4096
  *  D           even, 2 .. 512; dtype any rope_dtype; any strides and alignment (the widest
  *              access that they allow is used)
  *  theta, pos_scale  as in rope_qk_apply_ex
@@ -142,7 +143,7 @@ int32_t paged_plan(const int32_t* cu_seqlens, int32_t num_seqs, const int32_t* k
  *  q, out, lse as in attn_fwd
  *  workspace   device float[paged_workspace_floats(...)], 16-byte aligned, scratch: calls
  *              that may run at the same time need one each
- *  plan        written by paged_plan for the same T, num_seqs, Hq and Hkv
+ *  plan        written by paged_plan for the same T, num_seqs, Hq and Hkv (as in attn_fwd)
  *  max_pages   entries of a sequence's row of block_table; keys behind them, and keys on no
  *              page, are seen by no query
  *  fill        as in attn_fwd

@@ -104,7 +104,11 @@ def _token_rows(t, name: str, dtypes) -> int:
     if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous "
                          "(stride(2) == 1 and stride(1) == D)")
-    return t.stride(0) if T > 1 else H * D
+    if T <= 1:
+        return H * D
+    if t.stride(0) < H * D:
+        raise ValueError(f"{name}: its tokens overlap (an expanded tensor needs a copy)")
+    return t.stride(0)
 
 
 def _heads_last(t, name: str, most: int = 256) -> int:
@@ -198,6 +202,8 @@ def attn_fwd(q, k, v, plan: AttnPlan, scale=None, out=None, lse=None, zero_rest=
     (out [T, Hq, D], lse float32 [T, Hq]), in the given ones or in new ones. zero_rest: whether
     rows of no sequence are written as 0 (-inf in lse) or left as they are; by default new
     outputs are written and given ones left."""
+    if not isinstance(plan, AttnPlan):
+        raise TypeError("plan: expected what attn_plan returns")
     plan._match(q, k, v)
     T, Hq, D = q.shape
     strides = _heads_last(q, "q"), _heads_last(k, "k"), _heads_last(v, "v")
@@ -223,6 +229,8 @@ def attn_bwd(dout, q, k, v, out, lse, plan: AttnPlan, scale=None, dq=None, dk=No
     outputs and the same scale; D up to 128. Deterministic (no atomics). Returns (dq, dk, dv), in
     the given ones (all three, e.g. parts of one fused gradient) or in new ones. zero_rest as in
     attn_fwd."""
+    if not isinstance(plan, AttnPlan):
+        raise TypeError("plan: expected what attn_plan returns")
     plan._match(q, k, v)
     T, Hq, D = q.shape
     Hkv = k.shape[1]
@@ -314,6 +322,12 @@ def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: 
     elif q_out is not None:
         raise ValueError("q_out without q")
     cache_strides = _caches(k_cache, v_cache, k)
+    if not k_cache.is_contiguous():
+        extent = D
+        for step, n in sorted(zip(cache_strides, k_cache.shape)):
+            if n > 1 and step < extent:
+                raise ValueError("rows of the cache overlap (an expanded tensor cannot be written)")
+            extent += (n - 1) * step
     if tuple(k_cache.shape[2:]) != (Hkv, D):
         raise ValueError("the cache must have k's heads and head size")
     cu = _index(cu_seqlens, "cu_seqlens", dev)
@@ -375,6 +389,8 @@ def attn_paged(q, k_cache, v_cache, block_table, plan: PagedPlan, scale=None, ou
     or on a page number that is no page are seen by no query. Returns (out [T, Hq, D], lse
     float32 [T, Hq]), in the given ones or in new ones; a query that sees no key gets 0 (-inf in
     lse). zero_rest, for rows of no sequence, as in attn_fwd."""
+    if not isinstance(plan, PagedPlan):
+        raise TypeError("plan: expected what paged_plan returns")
     q_stride = _heads_last(q, "q")
     T, Hq, D = q.shape
     if T != plan.T or Hq != plan.num_q_heads or q.device != plan.buffer.device:

@@ -68,7 +68,7 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   uint32_t kvh;
   const uint32_t index = div31(blockIdx.x, p.by_hkv);
   kvh = blockIdx.x - index * p.Hkv;
-  if (!plan_matches(p) || (int32_t)index >= p.plan[0]) return;
+  if (!plan_matches(p, kPackedPlan) || (int32_t)index >= p.plan[0]) return;
   const RowItem item = p.row_items[index];
   const int32_t start = item.start, n = item.n;
   if (start < 0 || n <= 0 || start > p.T - n) return;
@@ -315,7 +315,7 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
   __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage];
   __shared__ __attribute__((aligned(16))) uint8_t flags[16];
 
-  if (!plan_matches(p)) return;
+  if (!plan_matches(p, kPackedPlan)) return;
   const Place work = place_of(p, gridDim.x);
   // workgroup i runs on die i % 8: neighbouring shares, which read the same rows, on one die
   const int32_t share = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
@@ -338,299 +338,299 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
   const int64_t g_step = dt * p.dout_stride + (int64_t)dh * p.D, g_wrap = p.dout_stride - (int64_t)p.G * p.D;
 
   for (; left > 0; ++index) {
-  if (pos >= work.units) {
-    pos = 0;
-    index = 0;
-    ++kvh;
-  }
-  const KeyTile tile = p.key_tiles[index];
-  const int64_t tile_end = end_of_tile(p, work, index);
-  const int64_t from = pos - tile.first, to = min(tile_end - tile.first, from + left);
-  if (to <= from) return;  // no plan of this batch's
-  const bool whole = from == 0 && to == tile_end - tile.first;
-  left -= to - from;
-  pos += to - from;
-
-  const int32_t start = tile.start, n = tile.n, key0 = tile.key0;
-  if (start < 0 || n <= 0 || start > p.T - n) continue;
-  T* dk_out = static_cast<T*>(p.dk);
-  T* dv_out = static_cast<T*>(p.dv);
-  if (tile.gap != 0) {
-    if (p.fill) {
-      clear_rows(dk_out, start, n, p.dk_stride, kvh, 1, chunks);
-      clear_rows(dv_out, start, n, p.dv_stride, kvh, 1, chunks);
+    if (pos >= work.units) {
+      pos = 0;
+      index = 0;
+      ++kvh;
     }
-    continue;
-  }
-  if (key0 < 0 || key0 >= n) continue;
+    const KeyTile tile = p.key_tiles[index];
+    const int64_t tile_end = end_of_tile(p, work, index);
+    const int64_t from = pos - tile.first, to = min(tile_end - tile.first, from + left);
+    if (to <= from) return;  // no plan of this batch's
+    const bool whole = from == 0 && to == tile_end - tile.first;
+    left -= to - from;
+    pos += to - from;
 
-  const int32_t rows = n * p.G;
-  const int32_t wave_key0 = key0 + 32 * wave;
-  const int32_t key = wave_key0 + (lane & 31);
-  const bool on = key < n;
-  const int32_t at_key = on ? key : n - 1;
-  const int32_t first = at_key * p.G;  // the first row that sees this lane's key
-  const int32_t wave_all = wave_key0 < n ? min(wave_key0 + 31, n - 1) * p.G : rows;  // the wave's every key
-
-  x8<T> kf[KS], vf[KS];
-  load_row<T>(kf, static_cast<const T*>(p.k) + (int64_t)(start + at_key) * p.k_stride +
-                      (int64_t)kvh * p.D, half, chunks);
-  load_row<T>(vf, static_cast<const T*>(p.v) + (int64_t)(start + at_key) * p.v_stride +
-                      (int64_t)kvh * p.D, half, chunks);
-  f32x16 dk[DB], dv[DB];
-
-  // this piece's row blocks: the tile's first kTileUnits are what it costs beside them
-  const int32_t block0 = (int32_t)max(from - kTileUnits, (int64_t)0);
-  const int32_t blocks = min((int32_t)max(to - kTileUnits, (int64_t)0), blocks_of_tile(n, key0, p.G)) - block0;
-  const int32_t row_begin = key0 * p.G / BM * BM + block0 * BM;
-  auto first_row = [&](int32_t i) __attribute__((always_inline)) { return row_begin + i * BM; };
-
-  const T* q = static_cast<const T*>(p.q) + (int64_t)start * p.q_stride + (int64_t)kvh * p.G * p.D;
-  const T* g = static_cast<const T*>(p.dout) + (int64_t)start * p.dout_stride +
-               (int64_t)kvh * p.G * p.D;
-  const float* stats = (half ? p.delta : p.lse2) + ((int64_t)kvh * p.T + start) * p.G;
-  // the next block's rows of this thread: head of the group, and offsets
-  uint32_t heads[kLoads];
-  int64_t q_at[kLoads], g_at[kLoads];
-  auto seek = [&](int32_t row0) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint32_t at = min(row0 + (int32_t)row_of<CPR, 256>(i, tid), rows - 1);
-      const uint32_t t = div31(at, p.by_g);
-      heads[i] = at - t * p.G;
-      q_at[i] = t * p.q_stride + (heads[i] * p.D + 8 * chunk_of<CPR, 256>(i, tid));
-      g_at[i] = t * p.dout_stride + (heads[i] * p.D + 8 * chunk_of<CPR, 256>(i, tid));
-    }
-  };
-  auto advance = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      bool wrap = false;
-      if (dh != 0) {
-        heads[i] += dh;
-        wrap = heads[i] >= (uint32_t)p.G;
-        if (wrap) heads[i] -= p.G;
+    const int32_t start = tile.start, n = tile.n, key0 = tile.key0;
+    if (start < 0 || n <= 0 || start > p.T - n) continue;
+    T* dk_out = static_cast<T*>(p.dk);
+    T* dv_out = static_cast<T*>(p.dv);
+    if (tile.gap != 0) {
+      if (p.fill) {
+        clear_rows(dk_out, start, n, p.dk_stride, kvh, 1, chunks);
+        clear_rows(dv_out, start, n, p.dv_stride, kvh, 1, chunks);
       }
-      q_at[i] += q_step + (wrap ? q_wrap : 0);
-      g_at[i] += g_step + (wrap ? g_wrap : 0);
+      continue;
     }
-  };
-  // The x-th copy of block b; blocks are begun in order, each after a call of go_to. The first
-  // is of lse and D of the rows, 32 words each, by the first wave: it waits for one copy more
-  // than it would have to, the other waves for what they need.
-  constexpr int kPieces = 2 * kLoads, kPerStep = (kPieces + KS - 1) / KS;
-  auto go_to = [&](int32_t b) __attribute__((always_inline)) {
-    if (b == 0 || first_row(b) + BM > rows) seek(first_row(b));  // also where the rows end
-    else advance();
-  };
-  auto piece = [&](int32_t b, int x) __attribute__((always_inline)) {
-    const uint32_t qd = lds_address(lds) + b % kStages * kStage, gd = qd + kTileBytes;
-    const int i = x / 2;
-    const uint32_t dst = (i * 256 + wave * 64) * 16;
-    if (x == 0 && wave == 0)
-      copy_word_to_lds(stats + min(first_row(b) + (int32_t)(lane & 31), rows - 1), gd + kTileBytes);
-    if (x % 2 == 0) copy_chunk_to_lds(q + q_at[i], qd + dst, lanes[i]);
-    else copy_chunk_to_lds(g + g_at[i], gd + dst, lanes[i]);
-  };
+    if (key0 < 0 || key0 >= n) continue;
 
-  // Above 64 columns the accumulators leave room for one wave on a SIMD, and the loop is
-  // pipelined over two blocks: while the matrix unit forms S and dP of the next block, the
-  // vector unit turns this block's into P and dS, a slice of them per step; then dV and dK
-  // follow, and before their last step the block after the next is waited for. Up to 64
-  // columns two waves share a SIMD, and a block is finished before the next is begun.
-  f32x16 s, dp;         // of the block at hand, then of the next one
-  f32x4 lse2[4], delta[4];
-  x8<T> qr[KS], gr[KS];  // rows of the next block, the first two steps' from the round before
-  auto buffer = [&](int32_t b) __attribute__((always_inline)) { return lds + b % kStages * kStage; };
-  auto read_stats = [&](const uint8_t* qt) __attribute__((always_inline)) {
-    const float* stat = reinterpret_cast<const float*>(qt + 2 * kTileBytes);
+    const int32_t rows = n * p.G;
+    const int32_t wave_key0 = key0 + 32 * wave;
+    const int32_t key = wave_key0 + (lane & 31);
+    const bool on = key < n;
+    const int32_t at_key = on ? key : n - 1;
+    const int32_t first = at_key * p.G;  // the first row that sees this lane's key
+    const int32_t wave_all = wave_key0 < n ? min(wave_key0 + 31, n - 1) * p.G : rows;  // the wave's every key
+
+    x8<T> kf[KS], vf[KS];
+    load_row<T>(kf, static_cast<const T*>(p.k) + (int64_t)(start + at_key) * p.k_stride +
+                        (int64_t)kvh * p.D, half, chunks);
+    load_row<T>(vf, static_cast<const T*>(p.v) + (int64_t)(start + at_key) * p.v_stride +
+                        (int64_t)kvh * p.D, half, chunks);
+    f32x16 dk[DB], dv[DB];
+
+    // this piece's row blocks: the tile's first kTileUnits are what it costs beside them
+    const int32_t block0 = (int32_t)max(from - kTileUnits, (int64_t)0);
+    const int32_t blocks = min((int32_t)max(to - kTileUnits, (int64_t)0), blocks_of_tile(n, key0, p.G)) - block0;
+    const int32_t row_begin = key0 * p.G / BM * BM + block0 * BM;
+    auto first_row = [&](int32_t i) __attribute__((always_inline)) { return row_begin + i * BM; };
+
+    const T* q = static_cast<const T*>(p.q) + (int64_t)start * p.q_stride + (int64_t)kvh * p.G * p.D;
+    const T* g = static_cast<const T*>(p.dout) + (int64_t)start * p.dout_stride +
+                 (int64_t)kvh * p.G * p.D;
+    const float* stats = (half ? p.delta : p.lse2) + ((int64_t)kvh * p.T + start) * p.G;
+    // the next block's rows of this thread: head of the group, and offsets
+    uint32_t heads[kLoads];
+    int64_t q_at[kLoads], g_at[kLoads];
+    auto seek = [&](int32_t row0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      lse2[j] = *reinterpret_cast<const f32x4*>(stat + 8 * j + 4 * half);
-      delta[j] = *reinterpret_cast<const f32x4*>(stat + 32 + 8 * j + 4 * half);
-    }
-  };
-  auto read_row = [&](const uint8_t* qt, int t) __attribute__((always_inline)) {
-    qr[t] = read_rows<T, CPR>(qt, lane & 31, 2 * t + half);
-    gr[t] = read_rows<T, CPR>(qt + kTileBytes, lane & 31, 2 * t + half);
-  };
-  // S and dP of the block at `qt`, whose first two steps' rows have been read; `first(t)` and
-  // `second(t)` are called in step t of KS, one before each of its two products.
-  auto scores = [&](const uint8_t* qt, f32x16& s_out, f32x16& dp_out, auto first_half, auto second_half)
-                    __attribute__((always_inline)) {
-    f32x16 a, c;
+      for (int i = 0; i < kLoads; ++i) {
+        const uint32_t at = min(row0 + (int32_t)row_of<CPR, 256>(i, tid), rows - 1);
+        const uint32_t t = div31(at, p.by_g);
+        heads[i] = at - t * p.G;
+        q_at[i] = t * p.q_stride + (heads[i] * p.D + 8 * chunk_of<CPR, 256>(i, tid));
+        g_at[i] = t * p.dout_stride + (heads[i] * p.D + 8 * chunk_of<CPR, 256>(i, tid));
+      }
+    };
+    auto advance = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) a[i] = c[i] = 0.0f;
-#pragma unroll
-    for (int t = 0; t < KS; ++t) {
-      step();
-      if (t + 2 < KS) read_row(qt, t + 2);
-      a = mfma(qr[t], kf[t], a);
-      first_half(t);
-      step();
-      c = mfma(gr[t], vf[t], c);
-      second_half(t);
-    }
-    step();
-    s_out = a;
-    dp_out = c;
-  };
-  auto round = [&](auto mode, int32_t b) __attribute__((always_inline)) {
-    constexpr int MODE = decltype(mode)::value;
-    const uint8_t* qt = buffer(b);
-    const uint8_t* gt = qt + kTileBytes;
-    const int32_t row0 = first_row(b);
-    go_to(b + kStages - 1);
-    if constexpr (!kPipelined) {
-      wait_copies_and_sync<(kStages - 2) * kPieces>();  // block b; the buffer before it is free
-      read_stats(qt);
-      read_row(qt, 0);
-      read_row(qt, 1);
-    }
-    if (row0 + BM > rows) {  // copies of the last row behind it: no weight
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (row0 + 8 * (i / 4) + 4 * (int32_t)half + i % 4 >= rows) lse2[i / 4][i % 4] = __builtin_inff();
-    }
-    uint32_t w[8], ds[8];  // P and dS of row pairs, narrowed
-    auto pair = [&](int x) __attribute__((always_inline)) {
-      float wx[2], dx[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int i = 2 * x + c, j = i / 4, e = i % 4;
-        wx[c] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2[j][e]));
-        dx[c] = wx[c] * (dp[i] - delta[j][e]);
-        if constexpr (MODE != kWhole) {
-          const int32_t at = row0 + 8 * j + 4 * (int32_t)half + e;
-          if (at < first || (MODE == kCareful && at >= rows)) wx[c] = dx[c] = 0.0f;
+      for (int i = 0; i < kLoads; ++i) {
+        bool wrap = false;
+        if (dh != 0) {
+          heads[i] += dh;
+          wrap = heads[i] >= (uint32_t)p.G;
+          if (wrap) heads[i] -= p.G;
         }
+        q_at[i] += q_step + (wrap ? q_wrap : 0);
+        g_at[i] += g_step + (wrap ? g_wrap : 0);
       }
-      w[x] = narrow2<T>(wx[0], wx[1]);
-      ds[x] = narrow2<T>(dx[0], dx[1]);
     };
-    x8<T> gc[2 * DB], qc[2 * DB];  // by step: 16 rows x / DB, columns x % DB
-    auto read = [&](int x) __attribute__((always_inline)) {
-      gc[x] = read_columns<T, CPR>(gt, 16 * (x / DB), x % DB, lane);
-      qc[x] = read_columns<T, CPR>(qt, 16 * (x / DB), x % DB, lane);
+    // The x-th copy of block b; blocks are begun in order, each after a call of go_to. The first
+    // is of lse and D of the rows, 32 words each, by the first wave: it waits for one copy more
+    // than it would have to, the other waves for what they need.
+    constexpr int kPieces = 2 * kLoads, kPerStep = (kPieces + KS - 1) / KS;
+    auto go_to = [&](int32_t b) __attribute__((always_inline)) {
+      if (b == 0 || first_row(b) + BM > rows) seek(first_row(b));  // also where the rows end
+      else advance();
     };
-    auto begin_copies = [&](int t) __attribute__((always_inline)) {
-#pragma unroll
-      for (int x = t * kPerStep; x < (t + 1) * kPerStep && x < kPieces; ++x) piece(b + kStages - 1, x);
+    auto piece = [&](int32_t b, int x) __attribute__((always_inline)) {
+      const uint32_t qd = lds_address(lds) + b % kStages * kStage, gd = qd + kTileBytes;
+      const int i = x / 2;
+      const uint32_t dst = (i * 256 + wave * 64) * 16;
+      if (x == 0 && wave == 0)
+        copy_word_to_lds(stats + min(first_row(b) + (int32_t)(lane & 31), rows - 1), gd + kTileBytes);
+      if (x % 2 == 0) copy_chunk_to_lds(q + q_at[i], qd + dst, lanes[i]);
+      else copy_chunk_to_lds(g + g_at[i], gd + dst, lanes[i]);
     };
-    if constexpr (kPipelined) {
-      f32x16 s_next, dp_next;
-      // eight pairs of rows over 2 KS half steps, and the copies
-      scores(buffer(b + 1), s_next, dp_next,
-             [&](int t) __attribute__((always_inline)) {
-#pragma unroll
-               for (int x = 16 * t / (2 * KS); x < 8 * (2 * t + 1) / (2 * KS); ++x) pair(x);
-               begin_copies(t);
-             },
-             [&](int t) __attribute__((always_inline)) {
-#pragma unroll
-               for (int x = 8 * (2 * t + 1) / (2 * KS); x < 8 * (2 * t + 2) / (2 * KS); ++x) pair(x);
-               if (t == KS - 1) {
-                 read(0);
-                 read(1);
-               }
-             });
-      s = s_next;
-      dp = dp_next;
-      read_stats(buffer(b + 1));
-    } else {
-      scores(qt, s, dp, begin_copies, [](int) {});
-      read(0);
-      read(1);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) pair(x);
-    }
-    x8<T> wb, db;
-#pragma unroll
-    for (int x = 0; x < 2 * DB; ++x) {
-      step();
-      if (x + 2 < 2 * DB) read(x + 2);
-      if (kPipelined && x == 2 * DB - 1) {
-        // all of block b has been read: block b + 2 has arrived, and b's buffer is free
-        wait_copies_and_sync<kPieces>();
-        read_row(buffer(b + 2), 0);
-        read_row(buffer(b + 2), 1);
-      }
-      if (x % DB == 0) {
-        const int y = 4 * (x / DB);
-        wb = __builtin_bit_cast(x8<T>, (u32x4){w[y], w[y + 1], w[y + 2], w[y + 3]});
-        db = __builtin_bit_cast(x8<T>, (u32x4){ds[y], ds[y + 1], ds[y + 2], ds[y + 3]});
-      }
-      if constexpr (MODE == kCareful) {
-        gc[x] = cleaned<T>(gc[x]);
-        qc[x] = cleaned<T>(qc[x]);  // one that sees the key has made dS NaN or 0 already
-      }
-      dv[x % DB] = mfma(gc[x], wb, dv[x % DB]);
-      dk[x % DB] = mfma(qc[x], db, dk[x % DB]);
-      if constexpr (MODE == kCareful)
-        if (x == 2 * DB - 2)  // before the barrier
-          for (int32_t j = 0; j < BM; ++j)
-            add_nonfinite_row<T, DB, CPR>(dv, gt, j, row0 + j >= first && row0 + j < rows, half);
-    }
-    step();
-  };
 
-  const int32_t partly = min(max(blocks, 0), max(0, wave_all - row_begin + BM - 1) / BM);
-  auto walk = [&](auto mode) __attribute__((always_inline)) {
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.0f;
-    if (blocks <= 0) return;
-    // Blocks behind the last are begun and scored like the others, and not used.
-    for (int32_t i = 0; i < kStages - 1; ++i) {
-      go_to(i);
-#pragma unroll
-      for (int x = 0; x < kPieces; ++x) piece(i, x);
-    }
-    settle<T>(kf);
-    settle<T>(vf);
-    if constexpr (kPipelined) {
-      wait_copies_and_sync<kPieces>();  // blocks 0 and 1
-      read_row(buffer(0), 0);
-      read_row(buffer(0), 1);
-      scores(buffer(0), s, dp, [](int) {}, [](int) {});
-      read_stats(buffer(0));
-      read_row(buffer(1), 0);
-      read_row(buffer(1), 1);
-    }
-    // in careful mode every block is masked, for the rows behind the last
-    const int32_t masked = decltype(mode)::value == kCareful ? blocks : partly;
-    int32_t b = 0;
-    for (; b < masked; ++b) round(mode, b);
-    for (; b < blocks; ++b) round(Constant<kWhole>(), b);
-    wait_copies<0>();
-  };
-  walk(Constant<kMasked>());
-  if (any_wave(any_nonfinite(dk) || any_nonfinite(dv), flags)) walk(Constant<kCareful>());
-
-  if (!whole) {
-    float* part = p.part + (2 * (int64_t)share + (from == 0)) * 2 * kKeyTile * p.D +
-                  (32 * wave + (lane & 31)) * p.D;
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
+    // Above 64 columns the accumulators leave room for one wave on a SIMD, and the loop is
+    // pipelined over two blocks: while the matrix unit forms S and dP of the next block, the
+    // vector unit turns this block's into P and dS, a slice of them per step; then dV and dK
+    // follow, and before their last step the block after the next is waited for. Up to 64
+    // columns two waves share a SIMD, and a block is finished before the next is begun.
+    f32x16 s, dp;         // of the block at hand, then of the next one
+    f32x4 lse2[4], delta[4];
+    x8<T> qr[KS], gr[KS];  // rows of the next block, the first two steps' from the round before
+    auto buffer = [&](int32_t b) __attribute__((always_inline)) { return lds + b % kStages * kStage; };
+    auto read_stats = [&](const uint8_t* qt) __attribute__((always_inline)) {
+      const float* stat = reinterpret_cast<const float*>(qt + 2 * kTileBytes);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t e = 32 * d + 8 * j + 4 * half;
-        if (!on || e >= (uint32_t)p.D) continue;
-        *reinterpret_cast<f32x4*>(part + e) =
-            (f32x4){dk[d][4 * j], dk[d][4 * j + 1], dk[d][4 * j + 2], dk[d][4 * j + 3]};
-        *reinterpret_cast<f32x4*>(part + kKeyTile * p.D + e) =
-            (f32x4){dv[d][4 * j], dv[d][4 * j + 1], dv[d][4 * j + 2], dv[d][4 * j + 3]};
+        lse2[j] = *reinterpret_cast<const f32x4*>(stat + 8 * j + 4 * half);
+        delta[j] = *reinterpret_cast<const f32x4*>(stat + 32 + 8 * j + 4 * half);
       }
-    continue;
-  }
+    };
+    auto read_row = [&](const uint8_t* qt, int t) __attribute__((always_inline)) {
+      qr[t] = read_rows<T, CPR>(qt, lane & 31, 2 * t + half);
+      gr[t] = read_rows<T, CPR>(qt + kTileBytes, lane & 31, 2 * t + half);
+    };
+    // S and dP of the block at `qt`, whose first two steps' rows have been read; `first(t)` and
+    // `second(t)` are called in step t of KS, one before each of its two products.
+    auto scores = [&](const uint8_t* qt, f32x16& s_out, f32x16& dp_out, auto first_half, auto second_half)
+                      __attribute__((always_inline)) {
+      f32x16 a, c;
 #pragma unroll
-  for (int d = 0; d < DB; ++d)
+      for (int i = 0; i < 16; ++i) a[i] = c[i] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dk[d][i] *= p.scale;
-  const int64_t at_row = (int64_t)(start + at_key);
-  store_row<T, DB>(dk, dk_out + at_row * p.dk_stride + (int64_t)kvh * p.D, half, chunks, on);
-  store_row<T, DB>(dv, dv_out + at_row * p.dv_stride + (int64_t)kvh * p.D, half, chunks, on);
+      for (int t = 0; t < KS; ++t) {
+        step();
+        if (t + 2 < KS) read_row(qt, t + 2);
+        a = mfma(qr[t], kf[t], a);
+        first_half(t);
+        step();
+        c = mfma(gr[t], vf[t], c);
+        second_half(t);
+      }
+      step();
+      s_out = a;
+      dp_out = c;
+    };
+    auto round = [&](auto mode, int32_t b) __attribute__((always_inline)) {
+      constexpr int MODE = decltype(mode)::value;
+      const uint8_t* qt = buffer(b);
+      const uint8_t* gt = qt + kTileBytes;
+      const int32_t row0 = first_row(b);
+      go_to(b + kStages - 1);
+      if constexpr (!kPipelined) {
+        wait_copies_and_sync<(kStages - 2) * kPieces>();  // block b; the buffer before it is free
+        read_stats(qt);
+        read_row(qt, 0);
+        read_row(qt, 1);
+      }
+      if (row0 + BM > rows) {  // copies of the last row behind it: no weight
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (row0 + 8 * (i / 4) + 4 * (int32_t)half + i % 4 >= rows) lse2[i / 4][i % 4] = __builtin_inff();
+      }
+      uint32_t w[8], ds[8];  // P and dS of row pairs, narrowed
+      auto pair = [&](int x) __attribute__((always_inline)) {
+        float wx[2], dx[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int i = 2 * x + c, j = i / 4, e = i % 4;
+          wx[c] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2[j][e]));
+          dx[c] = wx[c] * (dp[i] - delta[j][e]);
+          if constexpr (MODE != kWhole) {
+            const int32_t at = row0 + 8 * j + 4 * (int32_t)half + e;
+            if (at < first || (MODE == kCareful && at >= rows)) wx[c] = dx[c] = 0.0f;
+          }
+        }
+        w[x] = narrow2<T>(wx[0], wx[1]);
+        ds[x] = narrow2<T>(dx[0], dx[1]);
+      };
+      x8<T> gc[2 * DB], qc[2 * DB];  // by step: 16 rows x / DB, columns x % DB
+      auto read = [&](int x) __attribute__((always_inline)) {
+        gc[x] = read_columns<T, CPR>(gt, 16 * (x / DB), x % DB, lane);
+        qc[x] = read_columns<T, CPR>(qt, 16 * (x / DB), x % DB, lane);
+      };
+      auto begin_copies = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+        for (int x = t * kPerStep; x < (t + 1) * kPerStep && x < kPieces; ++x) piece(b + kStages - 1, x);
+      };
+      if constexpr (kPipelined) {
+        f32x16 s_next, dp_next;
+        // eight pairs of rows over 2 KS half steps, and the copies
+        scores(buffer(b + 1), s_next, dp_next,
+               [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+                 for (int x = 16 * t / (2 * KS); x < 8 * (2 * t + 1) / (2 * KS); ++x) pair(x);
+                 begin_copies(t);
+               },
+               [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+                 for (int x = 8 * (2 * t + 1) / (2 * KS); x < 8 * (2 * t + 2) / (2 * KS); ++x) pair(x);
+                 if (t == KS - 1) {
+                   read(0);
+                   read(1);
+                 }
+               });
+        s = s_next;
+        dp = dp_next;
+        read_stats(buffer(b + 1));
+      } else {
+        scores(qt, s, dp, begin_copies, [](int) {});
+        read(0);
+        read(1);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) pair(x);
+      }
+      x8<T> wb, db;
+#pragma unroll
+      for (int x = 0; x < 2 * DB; ++x) {
+        step();
+        if (x + 2 < 2 * DB) read(x + 2);
+        if (kPipelined && x == 2 * DB - 1) {
+          // all of block b has been read: block b + 2 has arrived, and b's buffer is free
+          wait_copies_and_sync<kPieces>();
+          read_row(buffer(b + 2), 0);
+          read_row(buffer(b + 2), 1);
+        }
+        if (x % DB == 0) {
+          const int y = 4 * (x / DB);
+          wb = __builtin_bit_cast(x8<T>, (u32x4){w[y], w[y + 1], w[y + 2], w[y + 3]});
+          db = __builtin_bit_cast(x8<T>, (u32x4){ds[y], ds[y + 1], ds[y + 2], ds[y + 3]});
+        }
+        if constexpr (MODE == kCareful) {
+          gc[x] = cleaned<T>(gc[x]);
+          qc[x] = cleaned<T>(qc[x]);  // one that sees the key has made dS NaN or 0 already
+        }
+        dv[x % DB] = mfma(gc[x], wb, dv[x % DB]);
+        dk[x % DB] = mfma(qc[x], db, dk[x % DB]);
+        if constexpr (MODE == kCareful)
+          if (x == 2 * DB - 2)  // before the barrier
+            for (int32_t j = 0; j < BM; ++j)
+              add_nonfinite_row<T, DB, CPR>(dv, gt, j, row0 + j >= first && row0 + j < rows, half);
+      }
+      step();
+    };
+
+    const int32_t partly = min(max(blocks, 0), max(0, wave_all - row_begin + BM - 1) / BM);
+    auto walk = [&](auto mode) __attribute__((always_inline)) {
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.0f;
+      if (blocks <= 0) return;
+      // Blocks behind the last are begun and scored like the others, and not used.
+      for (int32_t i = 0; i < kStages - 1; ++i) {
+        go_to(i);
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x) piece(i, x);
+      }
+      settle<T>(kf);
+      settle<T>(vf);
+      if constexpr (kPipelined) {
+        wait_copies_and_sync<kPieces>();  // blocks 0 and 1
+        read_row(buffer(0), 0);
+        read_row(buffer(0), 1);
+        scores(buffer(0), s, dp, [](int) {}, [](int) {});
+        read_stats(buffer(0));
+        read_row(buffer(1), 0);
+        read_row(buffer(1), 1);
+      }
+      // in careful mode every block is masked, for the rows behind the last
+      const int32_t masked = decltype(mode)::value == kCareful ? blocks : partly;
+      int32_t b = 0;
+      for (; b < masked; ++b) round(mode, b);
+      for (; b < blocks; ++b) round(Constant<kWhole>(), b);
+      wait_copies<0>();
+    };
+    walk(Constant<kMasked>());
+    if (any_wave(any_nonfinite(dk) || any_nonfinite(dv), flags)) walk(Constant<kCareful>());
+
+    if (!whole) {
+      float* part = p.part + (2 * (int64_t)share + (from == 0)) * 2 * kKeyTile * p.D +
+                    (32 * wave + (lane & 31)) * p.D;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t e = 32 * d + 8 * j + 4 * half;
+          if (!on || e >= (uint32_t)p.D) continue;
+          *reinterpret_cast<f32x4*>(part + e) =
+              (f32x4){dk[d][4 * j], dk[d][4 * j + 1], dk[d][4 * j + 2], dk[d][4 * j + 3]};
+          *reinterpret_cast<f32x4*>(part + kKeyTile * p.D + e) =
+              (f32x4){dv[d][4 * j], dv[d][4 * j + 1], dv[d][4 * j + 2], dv[d][4 * j + 3]};
+        }
+      continue;
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dk[d][i] *= p.scale;
+    const int64_t at_row = (int64_t)(start + at_key);
+    store_row<T, DB>(dk, dk_out + at_row * p.dk_stride + (int64_t)kvh * p.D, half, chunks, on);
+    store_row<T, DB>(dv, dv_out + at_row * p.dv_stride + (int64_t)kvh * p.D, half, chunks, on);
   }
 }
 
@@ -638,7 +638,7 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
 // takes the tile there if that is the first cut in it; y takes 32 of its keys.
 template <typename T>
 __global__ __launch_bounds__(256) void attn_bwd_join_kernel(const BwdParams p) {
-  if (!plan_matches(p)) return;
+  if (!plan_matches(p, kPackedPlan)) return;
   const Place work = place_of(p, gridDim.x);
   const int64_t share = blockIdx.x, cut = (share + 1) * work.share;
   if (cut >= work.total || work.tiles <= 0) return;

@@ -128,14 +128,14 @@ constexpr int chunks_per_row(int db) { return db <= 2 ? 8 : db <= 4 ? 16 : 32; }
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-typedef const __attribute__((address_space(1))) void gvoid;
 
 // One 16-byte chunk (4-byte word) per lane from global memory into LDS, no registers
 // between: lane l's lands at dst + 16 l (4 l), dst the same for the whole wave; lanes that are
 // not set in `lanes` write nothing. For whole waves in uniform flow: all lanes are active, and
 // are again behind it. In assembly because the compiler otherwise waits for every copy in
 // flight before each transposed read of LDS, also of a buffer that no copy writes, and breaks
-// the loop up where lanes are left out. m0 holds the LDS address and needs one wait state.
+// the loop up where lanes are left out. m0 holds the LDS address and needs one wait state (the
+// compiler keeps no value of its own there).
 // Whoever reads the data waits first (wait_copies).
 __device__ inline uint32_t lds_address(const uint8_t* p) {
   return (uint32_t)(uintptr_t)(lds_void*)p;
@@ -166,19 +166,6 @@ __device__ inline void wait_copies() {
 template <int LEFT>
 __device__ inline void wait_copies_and_sync() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(LEFT) : "memory");
-}
-
-// A ring of STAGES buffers that a workgroup fills block by block, COPIES copies a wave and
-// block: waits for a block while up to STAGES - 2 younger ones stay in flight. `younger`:
-// how many were begun. Behind it the buffer of the block before is free in every wave.
-template <int STAGES, int COPIES>
-__device__ inline void wait_ring(int32_t younger) {
-  static_assert(STAGES >= 2 && STAGES <= 6 && (STAGES - 2) * COPIES < 64, "vmcnt holds 6 bits");
-  if (STAGES >= 6 && younger >= 4) wait_copies_and_sync<STAGES >= 6 ? 4 * COPIES : 0>();
-  else if (STAGES >= 5 && younger >= 3) wait_copies_and_sync<STAGES >= 5 ? 3 * COPIES : 0>();
-  else if (STAGES >= 4 && younger >= 2) wait_copies_and_sync<STAGES >= 4 ? 2 * COPIES : 0>();
-  else if (STAGES >= 3 && younger >= 1) wait_copies_and_sync<STAGES >= 3 ? COPIES : 0>();
-  else wait_copies_and_sync<0>();
 }
 
 // The chunks of a tile, 256 (one workgroup) or 64 (one wave) at a time in the order of LDS:
@@ -291,10 +278,13 @@ inline bool valid_scale(double s) {  // positive and normal once it is single pr
 }
 inline int32_t launched() { return hipGetLastError() == hipSuccess ? ROPE_OK : ROPE_ELAUNCH; }
 
-// Whether a plan was made for this call's sizes (its header says for which).
+// Whether a plan is of this call's kind and sizes, as its header says: words 0 and 1 count its
+// two lists, 2 to 5 are T, G, num_seqs and Hkv, 8 is the kind (6 and 7: attn_plan.hip).
+enum PlanKind : int32_t { kPackedPlan = 0x7061636b, kPagedPlan = 0x70616765 };
 template <typename P>
-__device__ inline bool plan_matches(const P& p) {
-  return p.plan[2] == p.T && p.plan[3] == p.G && p.plan[4] == p.num_seqs && p.plan[5] == p.Hkv;
+__device__ inline bool plan_matches(const P& p, PlanKind kind) {
+  return p.plan[2] == p.T && p.plan[3] == p.G && p.plan[4] == p.num_seqs && p.plan[5] == p.Hkv &&
+         p.plan[8] == kind;
 }
 
 // Bounds of the tiles of a batch, rows of no sequence among them (128 of those a tile).

@@ -34,7 +34,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
 
   const uint32_t index = div31(blockIdx.x, p.by_hkv);
   const uint32_t kvh = blockIdx.x - index * p.Hkv;
-  if (!plan_matches(p)) return;
+  if (!plan_matches(p, kPackedPlan)) return;
   if ((int32_t)index >= p.plan[0]) return;
   const RowItem item = p.items[index];
   const int32_t start = item.start, n = item.n;

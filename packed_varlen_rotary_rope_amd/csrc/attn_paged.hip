@@ -166,6 +166,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(const PlanPara
     p.header[3] = p.G;
     p.header[4] = p.num_seqs;
     p.header[5] = p.Hkv;
+    p.header[8] = kPagedPlan;
   }
 }
 
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
 
   const uint32_t index = div31(blockIdx.x, p.by_hkv);
   const uint32_t kvh = blockIdx.x - index * p.Hkv;
-  if (!plan_matches(p) || (int32_t)index >= p.plan[0]) return;
+  if (!plan_matches(p, kPagedPlan) || (int32_t)index >= p.plan[0]) return;
   const Item item = p.items[index];
   const uint32_t tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -531,7 +532,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void paged_join_kernel(const PagedParams p) {
   const uint32_t index = div31(blockIdx.x, p.by_hkv);
   const uint32_t kvh = blockIdx.x - index * p.Hkv, part = blockIdx.y;
-  if (!plan_matches(p) || (int32_t)index >= p.plan[1]) return;
+  if (!plan_matches(p, kPagedPlan) || (int32_t)index >= p.plan[1]) return;
   const Join j = p.joins[index];
   if (j.q0 < 0 || j.row0 < 0 || j.rows <= 0 || j.rows > kRowTile || j.units < (j.rows + 31) / 32 ||
       j.splits < 0 || j.slot < 0 || j.slot + (int64_t)j.splits * j.units > p.units ||

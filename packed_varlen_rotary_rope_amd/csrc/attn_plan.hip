@@ -3,7 +3,7 @@
 // reach the host.
 //
 // Layout: a header of kHeader words {row items, key tiles, T, G, num_seqs, Hkv, work (64
-// bits)}, then the row items and the key tiles (attn_packed.h). Row items are ordered by
+// bits), kind}, then the row items and the key tiles (attn_packed.h). Row items are ordered by
 // falling work, so that the last workgroups of a launch are short ones: the hardware starts
 // workgroups in order. The order of items of like work depends on the execution; no result
 // depends on it. Key tiles are in the order of the rows, each with the work before it, so that
@@ -111,6 +111,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(const PlanParam
     p.header[3] = p.G;
     p.header[4] = p.num_seqs;
     p.header[5] = p.Hkv;
+    p.header[8] = kPackedPlan;
     *reinterpret_cast<int64_t*>(p.header + 6) = work_before;
   }
 }

@@ -235,6 +235,7 @@ class _Attn(torch.autograd.Function):
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, _ = ctx.saved_tensors
         dq, dk, dv = attn_bwd(_rows_for_kernel(dout), q, k, v, out, lse, ctx.plan, ctx.scale)
@@ -275,6 +276,7 @@ class _AttnQKV(torch.autograd.Function):
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         qkv, out, lse, _ = ctx.saved_tensors
         q, k, v = _qkv_heads(qkv, *ctx.heads)

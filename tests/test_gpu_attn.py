@@ -471,3 +471,68 @@ def test_many_sequences(rope):
             tol = 1.02 * ref.half_step(BF16) * (p @ vh.abs() + o.abs()) + 1e-4 * (p @ vh.abs())
             ref.check(out[at][:, :, h], o, tol, f"length {n}")
     assert bool((out[cu[-1]:] == 0).all()) and bool((dk[cu[-1]:] == 0).all())
+
+
+def test_tokens_that_overlap_are_refused(rope):
+    """An expanded tensor has token stride 0, which the C ABI reads as dense rows."""
+    q, k, v = batch(64, 4, 2, 64, BF16)
+    plan = rope.attn_plan(int32([0, 64]), 64, 4, 2)
+    out, lse = rope.attn_fwd(q, k, v, plan)
+    inputs = [q, q, k, v, out]
+    for i in range(5):
+        a = list(inputs)
+        a[i] = a[i][:1].expand_as(a[i])
+        with pytest.raises(ValueError, match="overlap"):
+            rope.attn_bwd(*a, lse, plan)
+        if 0 < i < 4:
+            with pytest.raises(ValueError, match="overlap"):
+                rope.attn_fwd(*a[1:4], plan)
+    half = torch.as_strided(q, (64, 4, 64), (128, 64, 1))
+    for kw in (dict(out=half, lse=lse), dict(out=q[:1].expand_as(q), lse=lse)):
+        with pytest.raises(ValueError, match="overlap"):
+            rope.attn_fwd(q, k, v, plan, **kw)
+    one = rope.attn_plan(int32([0, 1]), 1, 4, 2)  # one token: its stride says nothing
+    a = [torch.as_strided(x, (1, *x.shape[1:]), (0, 64, 1)) for x in (q, k, v)]
+    got, ref1 = rope.attn_fwd(*a, one), rope.attn_fwd(q[:1], k[:1], v[:1], one)
+    assert same(got[0], ref1[0]) and same(got[1], ref1[1])
+
+
+def test_plan_of_another_kind_is_refused(rope):
+    q, k, v = batch(64, 4, 2, 64, BF16)
+    cu = int32([0, 64])
+    packed, paged = rope.attn_plan(cu, 64, 4, 2), rope.paged_plan(cu, int32([64]), 64, 4, 2)
+    cache, table = k.reshape(4, 16, 2, 64), int32([[0, 1, 2, 3]])
+    with pytest.raises(TypeError, match="attn_plan"):
+        rope.attn_fwd(q, k, v, paged)
+    with pytest.raises(TypeError, match="paged_plan"):
+        rope.attn_paged(q, cache, cache, table, packed)
+    out, lse = torch.full_like(q, 3.0), torch.full((64, 4), 3.0, device=DEV)
+    grads = [torch.full_like(x, 3.0) for x in (q, k, v)]
+    fake = rope.AttnPlan(64, 1, 4, 2, paged.buffer)  # the kernels look, too
+    rope.attn_fwd(q, k, v, fake, out=out, lse=lse)
+    rope.attn_bwd(q, q, k, v, out, lse, fake, None, *grads)
+    rope.attn_paged(q, cache, cache, table, rope.PagedPlan(64, 1, 4, 2, packed.buffer), out=out, lse=lse)
+    assert all(bool((x == 3).all()) for x in (out, lse, *grads))
+
+
+def test_no_tokens_and_no_sequences(rope):
+    from packed_varlen_rotary_rope_amd import functional as F
+    q, k, v = batch(0, 4, 2, 64, BF16)
+    for cu in ([0], [0, 0, 0]):
+        plan = rope.attn_plan(int32(cu), 0, 4, 2)
+        out, lse = rope.attn_fwd(q, k, v, plan)
+        assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+        assert [g.shape for g in rope.attn_bwd(q, q, k, v, out, lse, plan)] == [q.shape, k.shape, v.shape]
+    q, k, v = (x.requires_grad_() for x in batch(130, 4, 2, 64, BF16))
+    out = F.attn(q, k, v, cu_seqlens=int32([0]))
+    out.sum().backward()
+    assert all(bool((x == 0).all()) for x in (out, q.grad, k.grad, v.grad))
+
+
+def test_no_second_derivative(rope):
+    from packed_varlen_rotary_rope_amd import functional as F
+    q, k, v = (x.requires_grad_() for x in batch(40, 2, 1, 64, BF16))
+    (g,) = torch.autograd.grad(F.attn(q, k, v, cu_seqlens=int32([0, 40])).float().square().sum(), q,
+                               create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.float().sum().backward()

@@ -365,3 +365,60 @@ def test_offsets_beyond_32_bits(rope):
     out1, _ = rope.attn_paged(rq[n - 1:n], both[:, 0], both[:, 1], t2,
                               rope.paged_plan(int32([0, 1]), int32([n]), 1, Hq, Hkv))
     ref.check(out1, want[n - 1:n], tol[n - 1:n], "one token")
+
+
+def test_tokens_that_overlap_are_refused(rope):
+    """An expanded tensor has token stride 0, which the C ABI reads as dense rows."""
+    kc, vc = normal((4, 16, 2, 64), 1, BF16), normal((4, 16, 2, 64), 2, BF16)
+    q, k, v = normal((3, 4, 64), 3, BF16), normal((3, 2, 64), 4, BF16), normal((3, 2, 64), 5, BF16)
+    table, cu, lens = int32([[0, 1]]), int32([0, 3]), int32([9])
+    wide = [x[:1].expand_as(x) for x in (q, k, v)]
+    for a in ((wide[0], k, v), (q, wide[1], v), (q, k, wide[2])):
+        with pytest.raises(ValueError, match="overlap"):
+            rope.kv_append_(a[1], a[2], kc, vc, table, cu, lens, 1e4, q=a[0])
+    with pytest.raises(ValueError, match="overlap"):
+        rope.kv_append_(k, v, kc, vc, table, cu, lens, 1e4, q=q, q_out=wide[0])
+    for of in (lambda c: c[:1].expand_as(c), lambda c: c[:, :1].expand_as(c), lambda c: c[:, :, :1].expand_as(c),
+               lambda c: torch.as_strided(c, (4, 16, 2, 64), (1024, 128, 64, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            rope.kv_append_(k, v, of(kc), of(vc), table, cu, lens, 1e4)
+    with pytest.raises(ValueError, match="overlap"):
+        rope.attn_paged(wide[0], kc, vc, table, rope.paged_plan(cu, lens, 3, 4, 2))
+
+
+def test_no_tokens_and_no_sequences(rope):
+    kc, vc = normal((4, 16, 2, 64), 1, BF16), normal((4, 16, 2, 64), 2, BF16)
+    old = kc.clone()
+    for B, T in ((0, 0), (2, 0), (0, 130)):
+        q, k, v = normal((T, 4, 64), 3, BF16), normal((T, 2, 64), 4, BF16), normal((T, 2, 64), 5, BF16)
+        cu, lens, table = int32([0] * (B + 1)), int32([7] * B), torch.zeros((B, 3), dtype=torch.int32, device=DEV)
+        assert same(rope.kv_append_(k, v, kc, vc, table, cu, lens, 1e4, q=q), q)
+        out, lse = rope.attn_paged(q, kc, vc, table, rope.paged_plan(cu, lens, T, 4, 2))
+        assert out.shape == q.shape and bool((out == 0).all()) and bool((lse == float("-inf")).all())
+    none = torch.zeros((1, 0), dtype=torch.int32, device=DEV)  # a table without pages
+    q, k, v = normal((3, 4, 64), 3, BF16), normal((3, 2, 64), 4, BF16), normal((3, 2, 64), 5, BF16)
+    rope.kv_append_(k, v, kc, vc, none, int32([0, 3]), int32([3]), 1e4)
+    out, lse = rope.attn_paged(q, kc, vc, none, rope.paged_plan(int32([0, 3]), int32([3]), 3, 4, 2))
+    assert bool((out == 0).all()) and bool((lse == float("-inf")).all()) and same(kc, old)
+
+
+@pytest.mark.parametrize("D,Hq,new", [(64, 4, 8), (128, 8, 100), (80, 2, 40), (192, 4, 90), (256, 2, 12)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_hidden_new_tokens_have_no_influence(rope, D, Hq, new, value):
+    """A new token whose key or value is not finite changes no query before it and no other
+    sequence."""
+    print(f"[hidden] D={D} Hq={Hq} new={new} {value}", flush=True)
+    held, page, cu = [new + 333, 77], 16, [0, new, new + 1]
+    k, v, table = pool(held, page, 2, D, BF16, D)
+    q = normal((new + 1, Hq, D), 3, BF16)
+    plan = rope.paged_plan(int32(cu), int32(held), new + 1, Hq, 2)
+    out0, lse0 = rope.attn_paged(q, k, v, table, plan)
+    bad = new // 2
+    pos = held[0] - new + bad
+    for c in (k, v):
+        c[table[0, pos // page].item(), pos % page, 1, 5] = value
+    out, lse = rope.attn_paged(q, k, v, table, plan)
+    keep = [i for i in range(new + 1) if i < bad or i == new]
+    assert same(out[keep], out0[keep]) and same(lse[keep], lse0[keep])
+    assert same(out[:, :Hq // 2], out0[:, :Hq // 2])
+    assert bool(out0[:new].isfinite().all())
