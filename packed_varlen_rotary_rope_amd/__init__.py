@@ -1,12 +1,14 @@
-"""Fused, in-place, packed variable-length QK rotary position embedding (RoPE),
-and the SwiGLU / GeGLU MLP activations, for AMD Instinct MI355X (gfx950).
+"""Fused, in-place, packed variable-length QK rotary position embedding (RoPE), the
+SwiGLU / GeGLU MLP activations, and the attention beside them (packed, and over a
+paged cache), for AMD Instinct MI355X (gfx950).
 
 Thin Python binding over the C ABI of ``include/rope_qk.h`` and ``include/glu.h``
 (librope_qk.so, built from ``csrc/rope_qk.hip`` and ``csrc/glu.hip``). This module
 only checks tensor metadata and marshals pointers, sizes and the current HIP
 stream; every step of the computation runs in the library's HIP kernels. There is
-no CPU fallback: if the library is missing, importing this package raises.
-Differentiable wrappers live in ``packed_varlen_rotary_rope_amd.functional``.
+no CPU fallback: if the library is missing, importing this package raises. The
+attention is a library of its own (libattn.so, ``attention.py``): its names raise
+if that one is missing. Differentiable wrappers live in ``packed_varlen_rotary_rope_amd.functional``.
 
 The operations follow the Unsloth page "Entrainement des LLM 3 fois plus rapide
 avec les noyaux Unsloth + le packing" (section "Kernel Triton QK RoPE fusionne
@@ -26,8 +28,7 @@ __all__ = [
     "RopeError", "qk_fwd_", "qk_bwd_", "qk_apply_", "qk_apply_ex_", "qk_apply_table_",
     "qk_apply_padded_", "valid_prefix", "qk_fwd_pos_", "qk_bwd_pos_",
     "positions", "cos_sin", "cos_sin_table", "inv_freq", "abi_version", "LIB_PATH", "INDEX_AUTO", "INDEX_32",
-    "INDEX_64", "glu_fwd", "glu_bwd", "GLU_KINDS", "AttnPlan", "attn_plan", "attn_fwd",
-    "attn_bwd", "PagedPlan", "paged_plan", "attn_paged", "kv_append_",
+    "INDEX_64", "glu_fwd", "glu_bwd", "GLU_KINDS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librope_qk.so")
@@ -433,6 +434,17 @@ def glu_bwd(kind: str, dh, e, g, de=None, dg=None, index_mode: int = INDEX_AUTO)
 
 # ---------------------------------------------------------------- attention
 
-from .attention import (  # noqa: E402
-    AttnPlan, PagedPlan, attn_bwd, attn_fwd, attn_paged, attn_plan, kv_append_, paged_plan,
-)
+_ATTENTION = ("AttnPlan", "attn_plan", "attn_fwd", "attn_bwd", "PagedPlan", "paged_plan",
+              "attn_paged", "kv_append_")
+
+if os.path.exists(os.path.join(os.path.dirname(LIB_PATH), "libattn.so")):
+    from .attention import (  # noqa: E402
+        AttnPlan, PagedPlan, attn_bwd, attn_fwd, attn_paged, attn_plan, kv_append_, paged_plan,
+    )
+    __all__ += _ATTENTION
+else:  # the rest of the package does without that library; its own names do not
+    def __getattr__(name):
+        if name in _ATTENTION:
+            from . import attention
+            return getattr(attention, name)
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -35,10 +35,13 @@ place would change the other consumer's gradient.
 """
 from __future__ import annotations
 
+import sys
+
 import torch
 
-from . import (attn_bwd, attn_fwd, attn_plan, glu_bwd, glu_fwd, qk_apply_ex_, qk_apply_padded_,
-               qk_apply_table_)
+from . import glu_bwd, glu_fwd, qk_apply_ex_, qk_apply_padded_, qk_apply_table_
+
+_rope = sys.modules[__package__]  # the attention's names, which need their library
 
 
 def _rotate(q, k, theta, direction, cu, su, pid, so, pos_scale, cv, valid):
@@ -219,7 +222,7 @@ def _plan_of(plan, cu_seqlens, seqused, T, Hq, Hkv):
     if plan is None:
         if cu_seqlens is None:
             raise ValueError("give a plan or cu_seqlens")
-        return attn_plan(cu_seqlens, T, Hq, Hkv, seqused=seqused)
+        return _rope.attn_plan(cu_seqlens, T, Hq, Hkv, seqused=seqused)
     if cu_seqlens is not None or seqused is not None:
         raise ValueError("a plan holds the sequences: give it or cu_seqlens (and seqused), not both")
     return plan
@@ -228,7 +231,7 @@ def _plan_of(plan, cu_seqlens, seqused, T, Hq, Hkv):
 class _Attn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, plan, scale):
-        out, lse = attn_fwd(q, k, v, plan, scale)
+        out, lse = _rope.attn_fwd(q, k, v, plan, scale)
         # the plan's buffer too: autograd notices where it has been written over since
         ctx.save_for_backward(q, k, v, out, lse, plan.buffer)
         ctx.plan, ctx.scale = plan, scale
@@ -238,7 +241,7 @@ class _Attn(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, _ = ctx.saved_tensors
-        dq, dk, dv = attn_bwd(_rows_for_kernel(dout), q, k, v, out, lse, ctx.plan, ctx.scale)
+        dq, dk, dv = _rope.attn_bwd(_rows_for_kernel(dout), q, k, v, out, lse, ctx.plan, ctx.scale)
         return dq, dk, dv, None, None
 
 
@@ -270,7 +273,7 @@ class _AttnQKV(torch.autograd.Function):
     @staticmethod
     def forward(ctx, qkv, Hq, Hkv, plan, scale):
         q, k, v = _qkv_heads(qkv, Hq, Hkv)
-        out, lse = attn_fwd(q, k, v, plan, scale)
+        out, lse = _rope.attn_fwd(q, k, v, plan, scale)
         ctx.save_for_backward(qkv, out, lse, plan.buffer)
         ctx.heads, ctx.plan, ctx.scale = (Hq, Hkv), plan, scale
         return out
@@ -282,7 +285,7 @@ class _AttnQKV(torch.autograd.Function):
         q, k, v = _qkv_heads(qkv, *ctx.heads)
         grad = torch.empty_like(qkv, memory_format=torch.contiguous_format)
         dq, dk, dv = _qkv_heads(grad, *ctx.heads)
-        attn_bwd(_rows_for_kernel(dout), q, k, v, out, lse, ctx.plan, ctx.scale, dq, dk, dv,
+        _rope.attn_bwd(_rows_for_kernel(dout), q, k, v, out, lse, ctx.plan, ctx.scale, dq, dk, dv,
                  zero_rest=True)
         return grad, None, None, None, None
 

@@ -3,9 +3,12 @@ host-side validation rejects bad arguments before any HIP call (no kernel is lau
 package refuses tensors that are not on a GPU, and the reference the GPU tests compare with
 agrees with plain autograd in 64 bits and notices planted mistakes."""
 import ctypes
+import glob
 import os
 import re
+import shutil
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -179,3 +182,26 @@ def test_reference_pages():
     s = (q[:, 0].double() @ k[2, :, 0].double().T)
     assert torch.allclose(lse[:, 0], torch.logsumexp(s, -1))
     assert torch.allclose(out[:, 0], torch.softmax(s, -1) @ v[2, :, 0].double())
+
+
+def test_package_without_the_attention_library(tmp_path):
+    """The rotary and GLU entry points import without libattn.so; the attention's names say what
+    is missing."""
+    pkg = os.path.join(ROOT, "packed_varlen_rotary_rope_amd")
+    there = tmp_path / "packed_varlen_rotary_rope_amd"
+    there.mkdir()
+    for path in [*glob.glob(os.path.join(pkg, "*.py")), os.path.join(pkg, "librope_qk.so")]:
+        shutil.copy(path, there)
+    code = ("import packed_varlen_rotary_rope_amd as m\n"
+            "from packed_varlen_rotary_rope_amd import functional as F\n"
+            "from packed_varlen_rotary_rope_amd import *\n"
+            "assert F.rope_qk and m.qk_fwd_ is qk_fwd_ and not hasattr(m, 'nothing')\n"
+            "for name in ('attn_fwd', 'kv_append_', 'AttnPlan'):\n"
+            "    try:\n"
+            "        getattr(m, name)\n"
+            "    except ImportError as e:\n"
+            "        assert 'build_attn.py' in str(e)\n"
+            "    else:\n"
+            "        raise SystemExit(name)\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=tmp_path, timeout=300,
+                   env={**os.environ, "PYTHONPATH": str(tmp_path)})
