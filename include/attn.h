@@ -17,13 +17,14 @@
  * (infinities and NaN among it), and queries that do not see a key none on its gradients.
  * Products are formed on the matrix cores from the storage type into fp32; the softmax and
  * its sums are fp32; the weights (and dS, backward) are rounded to the storage type before the
- * second product, and outputs once at the end. In f16 a dS past 65504 overflows there. Results do not depend on the order of execution: no atomics.
+ * second product, and outputs once at the end. In f16 a dS past 65504 overflows there. Results
+ * do not depend on the order of execution: no atomics on them.
  *
  * Layouts. Rows are [token][head][D], the heads of a token contiguous; every tensor has a
  * token stride in elements (0 = heads * D, else at least that: tokens do not overlap), so q, k
- * and v may be views of one fused projection. D is a multiple of 8, 8 .. 256 (backward: 8 .. 128). Data pointers are
- * 16-byte aligned and strides multiples of 8 elements, below 2^24. dtype is ROPE_BF16 or
- * ROPE_F16 (the append takes ROPE_F32 too). lse is float [T][Hq].
+ * and v may be views of one fused projection. D is a multiple of 8, 8 .. 256 (backward: 8 ..
+ * 128). Data pointers are 16-byte aligned and strides multiples of 8 elements, below 2^24.
+ * dtype is ROPE_BF16 or ROPE_F16 (the append takes ROPE_F32 too). lse is float [T][Hq].
  *
  * Ownership, threading and errors are those of rope_qk.h: the caller owns every buffer, the
  * library allocates nothing, keeps no state, never synchronizes, and only enqueues work on

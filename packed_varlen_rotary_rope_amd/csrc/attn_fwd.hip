@@ -4,6 +4,16 @@
 // (token-major, the group's heads minor), so that the heads of a group share every key and
 // value read and a tile spans few tokens, which wastes little above the diagonal and in
 // short sequences.
+//
+// What bounds it: matrix and vector unit together (with 128-wide heads both are busy for more
+// than half of the cycles, with 64-wide ones the exponentials for two thirds), and in long
+// launches the power limit, which takes the clock from 2.1 to 1.55 GHz. Two workgroups of four
+// waves share a CU (64 KB of LDS each), so that one wave's softmax runs beside another's products.
+// Measured, bf16: a prompt of 16384 tokens, 32 + 8 heads of 128, 2.0 to 2.3 ms, about 1.05
+// PFLOP/s (a large library product reaches 1.35); eight samples of 256 to 2048 tokens of the
+// same heads 148 us, 0.79; 8192 tokens of 16 + 2 heads of 64, 181 us, 0.76. Pipelined within a
+// wave over blocks of 32 keys (scores of the next beside this one's exponentials) it was 5 %
+// slower: twice the barriers and address arithmetic per key.
 #include "attn_packed.h"
 #include "attn_tile.h"
 

