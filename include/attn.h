@@ -17,8 +17,10 @@
  * (infinities and NaN among it), and queries that do not see a key none on its gradients.
  * Products are formed on the matrix cores from the storage type into fp32; the softmax and
  * its sums are fp32; the weights (and dS, backward) are rounded to the storage type before the
- * second product, and outputs once at the end. In f16 a dS past 65504 overflows there. Results
- * do not depend on the order of execution: no atomics on them.
+ * second product, and outputs once at the end. In f16 a dS past 65504 overflows there. Scores
+ * of any finite size are weighed forward; the backward forms the weights again from lse, with a
+ * relative error of |lse| 2^-22. Results do not depend on the order of execution: no atomics on
+ * them.
  *
  * Layouts. Rows are [token][head][D], the heads of a token contiguous; every tensor has a
  * token stride in elements (0 = heads * D, else at least that: tokens do not overlap), so q, k

@@ -30,10 +30,10 @@ struct Constant {
   static constexpr int value = N;
 };
 
-// Whether x holds in any lane of the workgroup's four waves. lds: 16 bytes
+// Bits 0 and 1 of x, of all lanes of the workgroup's four waves together. lds: 16 bytes
 // that may be overwritten once every wave has come here.
-__device__ inline bool any_wave(bool x, uint8_t* lds) {
-  const uint32_t mine = __any(x);
+__device__ inline uint32_t any_wave(uint32_t x, uint8_t* lds) {
+  const uint32_t mine = (__any(x & 1) ? 1 : 0) | (__any(x & 2) ? 2 : 0);
   uint32_t* flags = reinterpret_cast<uint32_t*>(lds);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) flags[threadIdx.x >> 6] = mine;
@@ -41,7 +41,7 @@ __device__ inline bool any_wave(bool x, uint8_t* lds) {
   const uint32_t found =
       __builtin_amdgcn_readfirstlane(flags[0] | flags[1] | flags[2] | flags[3]);
   if (found) __syncthreads();  // read by all before it is overwritten
-  return found != 0;
+  return found;
 }
 
 // How a block of keys (rows) is treated: every pair is seen; some are hidden; some are hidden

@@ -124,7 +124,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
     };
     // Two loops, so that neither body's registers are moved for the other's sake. Waves may be
     // in different ones: each passes one barrier per block in either.
-    for (; b < all; ++b) {
+    for (; b < (decltype(mode)::value == kCareful && t.exact ? 0 : all); ++b) {
       wait_copies_and_sync<0>();  // block b has arrived, and the other buffers are free
       const uint8_t* kt = lds + (b & 1) * 2 * Tile::kTileBytes;
       t.template block<kWhole>(kt, kt + Tile::kTileBytes, b * BN, seen, 0, p.scale, lane, next);
@@ -142,7 +142,12 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
     wait_copies<0>();
   };
   walk(Constant<kMasked>());
-  if (any_wave(any_nonfinite(t.o), lds)) walk(Constant<kCareful>());
+  const uint32_t anew = any_wave(any_nonfinite(t.o) | (uint32_t)t.large() << 1, lds);
+  if (anew) {
+    t.exact = anew & 2;
+    walk(Constant<kCareful>());
+    t.scale_maximum(p.scale);
+  }
 
   const float lse = t.finish();
   store_row<T, DB>(t.o, out + (int64_t)(start + token) * p.out_stride + (int64_t)head * p.D, half,

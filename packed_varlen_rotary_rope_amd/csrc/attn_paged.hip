@@ -353,7 +353,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
 #pragma unroll
         for (int x = s * kPerStep; x < (s + 1) * kPerStep && x < kPieces; ++x) piece(b + 1, x);
       };
-      for (; b < all && hidden_next == 0; ++b) {
+      for (; b < (decltype(mode)::value == kCareful && t.exact ? 0 : all) && hidden_next == 0; ++b) {
         const uint8_t* kt = arrive();
         t.template block<kWhole>(kt, kt + kTileBytes, item.key0 + b * BN, seen, 0, p.scale, lane, next);
       }
@@ -370,7 +370,12 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
       wait_copies<0>();
     };
     walk(Constant<kMasked>());
-    if (any_wave(any_nonfinite(t.o), lds)) walk(Constant<kCareful>());
+    const uint32_t anew = any_wave(any_nonfinite(t.o) | (uint32_t)t.large() << 1, lds);
+    if (anew) {
+      t.exact = anew & 2;
+      walk(Constant<kCareful>());
+      t.scale_maximum(p.scale);
+    }
     if (item.slot < 0) {
       const float lse = t.finish();
       store_row<T, DB>(t.o, out + row_at(p.out_stride, p.D, true), half, chunks, on);
@@ -459,11 +464,15 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
       stage(kb, kt, 0);
       if (!kOneBuffer) stage(vb, vt, 0);
       int32_t b = 0;
-      for (; b < all && hidden_next == 0; ++b) round(Constant<kWhole>(), b);
+      for (; b < (decltype(mode)::value == kCareful && t.exact ? 0 : all) && hidden_next == 0; ++b) round(Constant<kWhole>(), b);
       for (; b < blocks; ++b) round(mode, b);
     };
     walk(Constant<kMasked>());
-    if (__any(any_nonfinite(t.o))) walk(Constant<kCareful>());  // this wave alone
+    t.exact = __any(t.large());  // this wave alone
+    if (t.exact || __any(any_nonfinite(t.o))) {
+      walk(Constant<kCareful>());
+      t.scale_maximum(p.scale);
+    }
   }
 
   // Join the waves: O scaled to the common maximum goes to LDS four blocks of columns at a

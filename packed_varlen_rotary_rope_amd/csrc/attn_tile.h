@@ -23,6 +23,7 @@ __device__ inline float log_sum_exp(float m, float l) {  // from base 2
 }
 
 constexpr float kRescale = 8.0f;  // log2 of how far a maximum may rise before O is scaled
+constexpr float kLargeScore = 67108864.0f;  // 2^26, whose half steps are 4: weights up to 2^12
 
 // One row as B operand, a column of the product: chunks past the head size are zeros.
 template <typename T, int KS>
@@ -94,7 +95,15 @@ struct FwdTile {
 
   x8<T> q[KS];
   f32x16 o[DB];
-  float m, l;
+  float m, l;  // m in base 2; while `exact` is set, a score as it is
+  bool exact;  // read in kCareful mode only: m is subtracted before the scale, without rounding
+
+  // Whether scores are so large that scale * s - m, with m rounded, may be far from 0 for the
+  // largest of them, and its weight beyond the type's range: the walk is done again in kCareful
+  // mode with `exact` set, every block of it.
+  __device__ bool large() const {
+    return __builtin_fabsf(m) > kLargeScore && __builtin_fabsf(m) < __builtin_inff();
+  }
 
   __device__ void clear() {
 #pragma unroll
@@ -153,11 +162,12 @@ struct FwdTile {
     for (int b = 0; b < KB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[b][i]);
-    top = half_max(top) * scale;
-    const bool rises = !(top - m <= kRescale);
+    const bool as_is = MODE == kCareful && exact;
+    top = as_is ? half_max(top) : half_max(top) * scale;
+    const bool rises = !((as_is ? (top - m) * scale : top - m) <= kRescale);
     if (__any(rises)) {  // for the rows that need it: a row's bits do not depend on others
       const float m_new = rises ? __builtin_fmaxf(m, top) : m;
-      const float a = m == m_new ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
+      const float a = m == m_new ? 1.0f : __builtin_amdgcn_exp2f(as_is ? (m - m_new) * scale : m - m_new);
       m = m_new;
       l *= a;
 #pragma unroll
@@ -171,7 +181,8 @@ struct FwdTile {
     for (int b = 0; b < KB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], scale, -base));
+        s[b][i] = __builtin_amdgcn_exp2f(as_is ? (s[b][i] - base) * scale
+                                               : __builtin_fmaf(s[b][i], scale, -base));
         sum += s[b][i];
       }
     l += sum;
@@ -219,6 +230,11 @@ struct FwdTile {
     scores(s, kt, lane, piece);
     weights<MODE>(s, p, key0, seen, hidden, scale, lane);
     accumulate<MODE>(p, vt, key0, seen, hidden, lane);
+  }
+
+  // Ends a walk with `exact` set.
+  __device__ void scale_maximum(float scale) {
+    if (exact) m *= scale;
   }
 
   // Normalizes O and returns the row's log-sum-exp.

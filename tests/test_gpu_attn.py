@@ -536,3 +536,28 @@ def test_no_second_derivative(rope):
                                create_graph=True)
     with pytest.raises(RuntimeError):
         g.float().sum().backward()
+
+
+LARGE = [(BF16, 20, 12), (BF16, 8, 8), (BF16, 40, 40), (F16, 10, 4), (F16, 5, 5), (F16, 15, 7)]
+
+
+@pytest.mark.parametrize("D", [64, 128, 192])
+@pytest.mark.parametrize("dtype,a,b", LARGE)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_very_large_scores(rope, D, dtype, a, b, sign):
+    """Scores sign * n 2^(a+b) D^0.5 with distinct integers n, exact in fp32: each row's softmax is
+    one key's. That weight is 1, or 2^e rounded with its sum 2^e unrounded, |e| <= 4: out is off by
+    its half step and the output's. lse is the score, scaled twice and multiplied by ln 2."""
+    print(f"[large] D={D} {dtype} {a} {b} {sign}", flush=True)
+    T, cu = 256, [0, 100, 256]
+    n = (torch.randperm(T, generator=torch.Generator().manual_seed(D + a)) + 1).to(DEV)
+    q = torch.full((T, 4, D), 2.0 ** a, device=DEV).to(dtype)
+    k = (sign * n[:, None, None] * 2.0 ** b).expand(T, 2, D).to(dtype).contiguous()
+    v = normal((T, 2, D), 5, dtype)
+    out, lse = rope.attn_fwd(q, k, v, rope.attn_plan(int32(cu), T, 4, 2))
+    for s, e in zip(cu, cu[1:]):
+        m = torch.cummax(sign * n[s:e], 0)
+        want = v[s:e][m.indices].repeat_interleave(2, 1).double()
+        ref.check(out[s:e], want, want.abs() * 2.1 * ref.half_step(dtype), "out")
+        score = (m.values.double() * 2.0 ** (a + b) * D ** 0.5)[:, None].expand(-1, 4)
+        ref.check(lse[s:e], score, score.abs() * 2.0 ** -21, "lse")

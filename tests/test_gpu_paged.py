@@ -422,3 +422,25 @@ def test_hidden_new_tokens_have_no_influence(rope, D, Hq, new, value):
     assert same(out[keep], out0[keep]) and same(lse[keep], lse0[keep])
     assert same(out[:, :Hq // 2], out0[:, :Hq // 2])
     assert bool(out0[:new].isfinite().all())
+
+
+@pytest.mark.parametrize("D,new", [(64, 1), (128, 1), (128, 100), (192, 9), (256, 90)])
+@pytest.mark.parametrize("dtype,a,b", [(BF16, 20, 12), (BF16, 40, 40), (F16, 10, 4), (F16, 15, 7)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_very_large_scores(rope, D, new, dtype, a, b, sign):
+    """As test_gpu_attn's: every score is sign * n 2^(a+b) D^0.5, n distinct, one key takes all;
+    of 6 splits or waves each but one has weight 0."""
+    print(f"[large] D={D} new={new} {dtype} {a} {b} {sign}", flush=True)
+    held, page = 256, 16
+    n = (torch.randperm(held, generator=torch.Generator().manual_seed(D + a)) + 1).to(DEV)
+    k = (sign * n[:, None, None] * 2.0 ** b).expand(held, 2, D).to(dtype).contiguous()
+    v = normal((held, 2, D), 5, dtype)
+    q = torch.full((new, 4, D), 2.0 ** a, device=DEV).to(dtype)
+    table = torch.arange(16, dtype=torch.int32, device=DEV)[None]
+    plan = rope.paged_plan(int32([0, new]), int32([held]), new, 4, 2)
+    out, lse = rope.attn_paged(q, k.view(16, page, 2, D), v.view(16, page, 2, D), table, plan)
+    m = torch.cummax(sign * n, 0)
+    want = v[m.indices[held - new:]].repeat_interleave(2, 1).double()
+    ref.check(out, want, want.abs() * 2.1 * ref.half_step(dtype), "out")
+    score = (m.values[held - new:].double() * 2.0 ** (a + b) * D ** 0.5)[:, None].expand(-1, 4)
+    ref.check(lse, score, score.abs() * 2.0 ** -21, "lse")
