@@ -15,11 +15,11 @@
 // columns. S and dP are formed twice, 14 flops per pair and element of D instead of 10;
 // the price of having no fp32 sums of dQ in memory.
 //
-// What bounds them: of the cycles the matrix unit is busy for 39 % (dQ) and 34 % (dK, dV), the
+// What bounds them: of the cycles the matrix unit is busy for 39 % (dQ) and 37 % (dK, dV), the
 // vector unit for as many; the rest is waiting, for LDS and at the barrier of each block, with
 // one or two waves on a SIMD to hide it (the accumulators leave no room for more). Measured,
-// bf16: eight samples of 256 to 2048 tokens, 32 + 8 heads of 128: dQ 220 us, dK and dV 338, their
-// join 20, which is 0.8 and 0.7 PFLOP/s of the 6 and 8 flops that each of them does; 8192 tokens
+// bf16: eight samples of 256 to 2048 tokens, 32 + 8 heads of 128: dQ 220 us, dK and dV 318, their
+// join 20, which is 0.79 and 0.73 PFLOP/s of the 6 and 8 flops that each of them does; 8192 tokens
 // of 16 + 2 heads of 64: 240, 340 and 20 us, 0.86 and 0.81 PFLOP/s. Rounding: P and dS go to
 // the storage type before their second product, as the matrix unit takes it; a dS past 65504
 // overflows in f16, as a stored dP would.
@@ -315,6 +315,9 @@ __device__ inline int64_t end_of_tile(const BwdParams& p, const Place& w, int32_
   return tile + 1 < w.tiles ? p.key_tiles[tile + 1].first : w.units;
 }
 
+// lse and D of a row that is none: no weight.
+__device__ const float kNoRow[2] = {__builtin_inff(), 0.0f};
+
 template <typename T, int DB>
 __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(const BwdParams p) {
   constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BM = kRowBlock;
@@ -436,27 +439,50 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
       const uint32_t qd = lds_address(lds) + b % kStages * kStage, gd = qd + kTileBytes;
       const int i = x / 2;
       const uint32_t dst = (i * 256 + wave * 64) * 16;
-      if (x == 0 && wave == 0)
-        copy_word_to_lds(stats + min(first_row(b) + (int32_t)(lane & 31), rows - 1), gd + kTileBytes);
+      if (x == 0 && wave == 0) {
+        const int32_t row = first_row(b) + (int32_t)(lane & 31);
+        copy_word_to_lds(row < rows ? stats + row : kNoRow + half, gd + kTileBytes);
+      }
       if (x % 2 == 0) copy_chunk_to_lds(q + q_at[i], qd + dst, lanes[i]);
       else copy_chunk_to_lds(g + g_at[i], gd + dst, lanes[i]);
     };
 
     // Above 64 columns the accumulators leave room for one wave on a SIMD, and the loop is
-    // pipelined over two blocks: while the matrix unit forms S and dP of the next block, the
-    // vector unit turns this block's into P and dS, a slice of them per step; then dV and dK
-    // follow, and before their last step the block after the next is waited for. Up to 64
-    // columns two waves share a SIMD, and a block is finished before the next is begun.
-    f32x16 s, dp;         // of the block at hand, then of the next one
-    f32x4 lse2[4], delta[4];
+    // pipelined over two blocks so that every product has vector work beside it: while the matrix
+    // unit forms S and dP of the next block, the vector unit turns the middle half of this one's
+    // into P and dS, an operation or two per product; then dV and dK follow, beside the last
+    // quarter of this block and the first one of the next. Before their last step the block after
+    // the next is waited for. (With all of P and dS beside the first half of the products the
+    // pass of a packed batch took 339 us, and 318 so.) Up to 64 columns two waves share a SIMD, and a
+    // block is finished before the next is begun.
+    f32x16 s, dp;             // of the block at hand, then of the next one
+    f32x4 lse2[4], delta[4];  // of rows 8 j + 4 half .. + 3
+    float wx[2], dx[2];
+    uint32_t w[8], ds[8];  // P and dS of row pairs, narrowed
     x8<T> qr[KS], gr[KS];  // rows of the next block, the first two steps' from the round before
     auto buffer = [&](int32_t b) __attribute__((always_inline)) { return lds + b % kStages * kStage; };
-    auto read_stats = [&](const uint8_t* qt) __attribute__((always_inline)) {
+    auto read_stats = [&](const uint8_t* qt, int j) __attribute__((always_inline)) {
       const float* stat = reinterpret_cast<const float*>(qt + 2 * kTileBytes);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        lse2[j] = *reinterpret_cast<const f32x4*>(stat + 8 * j + 4 * half);
-        delta[j] = *reinterpret_cast<const f32x4*>(stat + 32 + 8 * j + 4 * half);
+      lse2[j] = *reinterpret_cast<const f32x4*>(stat + 8 * j + 4 * half);
+      delta[j] = *reinterpret_cast<const f32x4*>(stat + 32 + 8 * j + 4 * half);
+    };
+    // The u-th of 32 operations from S and dP to P (even) and dS (odd), in order.
+    auto weigh = [&](auto mode, int u, const f32x16& sv, const f32x16& dpv, int32_t row0)
+                     __attribute__((always_inline)) {
+      constexpr int MODE = decltype(mode)::value;
+      const int i = u / 2, j = i / 4, e = i % 4, c = i % 2;
+      const int32_t at = row0 + 8 * j + 4 * (int32_t)half + e;
+      const bool gone = MODE != kWhole && (at < first || (MODE == kCareful && at >= rows));
+      if (u % 2 == 0) {
+        wx[c] = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[i], p.scale2, -lse2[j][e]));
+        if (gone) wx[c] = 0.0f;
+      } else {
+        dx[c] = wx[c] * (dpv[i] - delta[j][e]);
+        if (gone) dx[c] = 0.0f;
+        if (c == 1) {
+          w[i / 2] = narrow2<T>(wx[0], wx[1]);
+          ds[i / 2] = narrow2<T>(dx[0], dx[1]);
+        }
       }
     };
     auto read_row = [&](const uint8_t* qt, int t) __attribute__((always_inline)) {
@@ -492,31 +518,11 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
       go_to(b + kStages - 1);
       if constexpr (!kPipelined) {
         wait_copies_and_sync<(kStages - 2) * kPieces>();  // block b; the buffer before it is free
-        read_stats(qt);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) read_stats(qt, j);
         read_row(qt, 0);
         read_row(qt, 1);
       }
-      if (row0 + BM > rows) {  // copies of the last row behind it: no weight
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (row0 + 8 * (i / 4) + 4 * (int32_t)half + i % 4 >= rows) lse2[i / 4][i % 4] = __builtin_inff();
-      }
-      uint32_t w[8], ds[8];  // P and dS of row pairs, narrowed
-      auto pair = [&](int x) __attribute__((always_inline)) {
-        float wx[2], dx[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int i = 2 * x + c, j = i / 4, e = i % 4;
-          wx[c] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2[j][e]));
-          dx[c] = wx[c] * (dp[i] - delta[j][e]);
-          if constexpr (MODE != kWhole) {
-            const int32_t at = row0 + 8 * j + 4 * (int32_t)half + e;
-            if (at < first || (MODE == kCareful && at >= rows)) wx[c] = dx[c] = 0.0f;
-          }
-        }
-        w[x] = narrow2<T>(wx[0], wx[1]);
-        ds[x] = narrow2<T>(dx[0], dx[1]);
-      };
       x8<T> gc[2 * DB], qc[2 * DB];  // by step: 16 rows x / DB, columns x % DB
       auto read = [&](int x) __attribute__((always_inline)) {
         gc[x] = read_columns<T, CPR>(gt, 16 * (x / DB), x % DB, lane);
@@ -526,32 +532,42 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
 #pragma unroll
         for (int x = t * kPerStep; x < (t + 1) * kPerStep && x < kPieces; ++x) piece(b + kStages - 1, x);
       };
+      f32x16 s_next, dp_next;
+      // operations 8 .. 23 beside the 2 KS products of the first half
+      auto middle = [&](int x) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 8 + 16 * x / (2 * KS); u < 8 + 16 * (x + 1) / (2 * KS); ++u) weigh(mode, u, s, dp, row0);
+      };
+      // of 4 DB in the second half: operations 24 .. 31, and 0 .. 7 of the next block
+      auto rest = [&](int x) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 16 * x / (4 * DB); u < 16 * (x + 1) / (4 * DB); ++u) {
+          if (u < 8) weigh(mode, 24 + u, s, dp, row0);
+          else weigh(mode, u - 8, s_next, dp_next, first_row(b + 1));
+        }
+      };
       if constexpr (kPipelined) {
-        f32x16 s_next, dp_next;
-        // eight pairs of rows over 2 KS half steps, and the copies
         scores(buffer(b + 1), s_next, dp_next,
                [&](int t) __attribute__((always_inline)) {
-#pragma unroll
-                 for (int x = 16 * t / (2 * KS); x < 8 * (2 * t + 1) / (2 * KS); ++x) pair(x);
+                 if (t == 0) read_stats(qt, 2);
+                 if (t == KS / 2) read_stats(qt, 3);
+                 middle(2 * t);
                  begin_copies(t);
                },
                [&](int t) __attribute__((always_inline)) {
-#pragma unroll
-                 for (int x = 8 * (2 * t + 1) / (2 * KS); x < 8 * (2 * t + 2) / (2 * KS); ++x) pair(x);
+                 middle(2 * t + 1);
                  if (t == KS - 1) {
                    read(0);
                    read(1);
+                   read_stats(buffer(b + 1), 0);
                  }
                });
-        s = s_next;
-        dp = dp_next;
-        read_stats(buffer(b + 1));
       } else {
         scores(qt, s, dp, begin_copies, [](int) {});
         read(0);
         read(1);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) pair(x);
+        for (int u = 0; u < 32; ++u) weigh(mode, u, s, dp, row0);
       }
       x8<T> wb, db;
 #pragma unroll
@@ -563,6 +579,7 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
           wait_copies_and_sync<kPieces>();
           read_row(buffer(b + 2), 0);
           read_row(buffer(b + 2), 1);
+          read_stats(buffer(b + 1), 1);
         }
         if (x % DB == 0) {
           const int y = 4 * (x / DB);
@@ -574,13 +591,22 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
           qc[x] = cleaned<T>(qc[x]);  // one that sees the key has made dS NaN or 0 already
         }
         dv[x % DB] = mfma(gc[x], wb, dv[x % DB]);
+        if constexpr (kPipelined) {
+          rest(2 * x);
+          step();
+        }
         dk[x % DB] = mfma(qc[x], db, dk[x % DB]);
+        if constexpr (kPipelined) rest(2 * x + 1);
         if constexpr (MODE == kCareful)
           if (x == 2 * DB - 2)  // before the barrier
             for (int32_t j = 0; j < BM; ++j)
               add_nonfinite_row<T, DB, CPR>(dv, gt, j, row0 + j >= first && row0 + j < rows, half);
       }
       step();
+      if constexpr (kPipelined) {
+        s = s_next;
+        dp = dp_next;
+      }
     };
 
     const int32_t partly = min(max(blocks, 0), max(0, wave_all - row_begin + BM - 1) / BM);
@@ -603,7 +629,10 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
         read_row(buffer(0), 0);
         read_row(buffer(0), 1);
         scores(buffer(0), s, dp, [](int) {}, [](int) {});
-        read_stats(buffer(0));
+        read_stats(buffer(0), 0);
+        read_stats(buffer(0), 1);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) weigh(mode, u, s, dp, first_row(0));
         read_row(buffer(1), 0);
         read_row(buffer(1), 1);
       }
