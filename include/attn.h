@@ -27,6 +27,8 @@
  * and v may be views of one fused projection. D is a multiple of 8, 8 .. 256 (backward: 8 ..
  * 128). Data pointers are 16-byte aligned and strides multiples of 8 elements, below 2^24.
  * dtype is ROPE_BF16 or ROPE_F16 (the append takes ROPE_F32 too). lse is float [T][Hq].
+ * A launch has at most 8388607 workgroups: attention refuses (ROPE_EINVAL) what needs more,
+ * T * Hq / 128 + (2 num_seqs + 3) Hkv of them.
  *
  * Ownership, threading and errors are those of rope_qk.h: the caller owns every buffer, the
  * library allocates nothing, keeps no state, never synchronizes, and only enqueues work on

@@ -93,6 +93,10 @@ def _gpu(device: torch.device) -> None:
 
 def _token_rows(t, name: str, dtypes) -> int:
     """Token stride of a [T, H, D] tensor whose tokens hold their heads contiguously."""
+    shape, stride = t.shape, t.stride()
+    if (len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2] and
+            stride[0] >= shape[1] * shape[2] and t.is_cuda and t.dtype in dtypes):
+        return stride[0]
     _gpu(t.device)
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected " + " or ".join(str(d)[6:] for d in dtypes))
@@ -260,21 +264,21 @@ def attn_bwd(dout, q, k, v, out, lse, plan: AttnPlan, scale=None, dq=None, dk=No
 
 # ---------------------------------------------------------------- paged cache
 
-def _caches(k_cache, v_cache, ref):
-    """Checked caches [num_pages, page_size, Hkv, D] of one layout; their strides."""
-    stride = k_cache.stride()
-    if k_cache.dtype != ref.dtype or v_cache.dtype != ref.dtype or k_cache.device != ref.device or \
-            v_cache.device != ref.device:
+def _caches(k_cache, v_cache, dtype, device):
+    """Checked caches [num_pages, page_size, Hkv, D] of one layout; their shape and strides."""
+    shape, stride = k_cache.shape, k_cache.stride()
+    if k_cache.dtype != dtype or v_cache.dtype != dtype or k_cache.device != device or \
+            v_cache.device != device:
         raise TypeError("k_cache or v_cache: dtype or device differs from the new tokens'")
     if len(stride) != 4:
         raise ValueError("k_cache: expected [num_pages, page_size, Hkv, D]")
-    if k_cache.shape != v_cache.shape or stride != v_cache.stride():
+    if shape != v_cache.shape or stride != v_cache.stride():
         raise ValueError("k_cache and v_cache must have one shape and layout")
-    if k_cache.shape[0] < 1 or k_cache.shape[1] < 1:
+    if shape[0] < 1 or shape[1] < 1:
         raise ValueError("the cache needs at least one page of at least one slot")
-    if k_cache.shape[3] > 1 and stride[3] != 1:
+    if shape[3] > 1 and stride[3] != 1:
         raise ValueError("the D elements of a cache row must be contiguous")
-    return stride[:3]
+    return shape, stride
 
 
 def _table(block_table, num_seqs, device):
@@ -283,9 +287,10 @@ def _table(block_table, num_seqs, device):
     B, per = block_table.shape
     if B != num_seqs:
         raise ValueError("block_table must have one row per sequence")
-    if per > 1 and block_table.stride(1) != 1:
+    row, step = block_table.stride()
+    if per > 1 and step != 1:
         raise ValueError("block_table: a sequence's pages must be contiguous")
-    return per, block_table.stride(0) if B > 1 else per
+    return per, row if B > 1 else per
 
 
 def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: float, q=None,
@@ -300,18 +305,18 @@ def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: 
     Tokens at a negative position, of no sequence, behind the table or on a page number that
     is no page are not appended. Returns the rotated q, in q_out (a new tensor if None; may be
     q itself), or None without q."""
-    if k.dim() != 3 or k.shape != v.shape:
+    shape, dtype, dev = k.shape, k.dtype, k.device
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError("expected k and v [T, Hkv, D]")
-    if v.dtype != k.dtype or v.device != k.device:
+    if v.dtype != dtype or v.device != dev:
         raise TypeError("k and v must share one dtype and device")
-    dev = k.device
     k_stride, v_stride = _token_rows(k, "k", _ANY), _token_rows(v, "v", _ANY)
-    T, Hkv, D = k.shape
+    T, Hkv, D = shape
     Hq, q_stride, out_stride = 0, 0, 0
     if q is not None:
-        if q.dtype != k.dtype or q.device != dev:
+        if q.dtype != dtype or q.device != dev:
             raise TypeError("q: dtype or device differs from k")
-        if q.dim() != 3 or (q.shape[0], q.shape[2]) != (T, D):
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D:
             raise ValueError("expected q [T, Hq, D] with k's T and D")
         Hq = q.shape[1]
         if q_out is None:
@@ -321,15 +326,15 @@ def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: 
         q_stride = _token_rows(q, "q", _ANY)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    cache_strides = _caches(k_cache, v_cache, k)
+    cache, steps = _caches(k_cache, v_cache, dtype, dev)
+    if cache[2] != Hkv or cache[3] != D:
+        raise ValueError("the cache must have k's heads and head size")
     if not k_cache.is_contiguous():
         extent = D
-        for step, n in sorted(zip(cache_strides, k_cache.shape)):
+        for step, n in sorted(zip(steps[:3], cache)):
             if n > 1 and step < extent:
                 raise ValueError("rows of the cache overlap (an expanded tensor cannot be written)")
             extent += (n - 1) * step
-    if tuple(k_cache.shape[2:]) != (Hkv, D):
-        raise ValueError("the cache must have k's heads and head size")
     cu = _index(cu_seqlens, "cu_seqlens", dev)
     num_seqs = cu.numel() - 1
     if num_seqs < 0:
@@ -338,9 +343,9 @@ def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: 
     per, table_stride = _table(block_table, num_seqs, dev)
     _call(dev, _lib.kv_append, "kv_append", _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), T, Hq, Hkv, D, q_stride, out_stride, k_stride,
-          v_stride, k_cache.shape[0], k_cache.shape[1], *cache_strides, block_table.data_ptr(), per,
+          v_stride, cache[0], cache[1], steps[0], steps[1], steps[2], block_table.data_ptr(), per,
           table_stride, cu.data_ptr(), num_seqs, lens.data_ptr(), float(theta), float(pos_scale),
-          _DTYPE_CODE[k.dtype])
+          _DTYPE_CODE[dtype])
     return q_out
 
 
@@ -395,8 +400,8 @@ def attn_paged(q, k_cache, v_cache, block_table, plan: PagedPlan, scale=None, ou
     T, Hq, D = q.shape
     if T != plan.T or Hq != plan.num_q_heads or q.device != plan.buffer.device:
         raise ValueError("the plan was made for other new tokens, query heads or another device")
-    page_stride, slot_stride, head_stride = _caches(k_cache, v_cache, q)
-    num_pages, page_size, Hkv, cache_d = k_cache.shape
+    cache, (page_stride, slot_stride, head_stride, _) = _caches(k_cache, v_cache, q.dtype, q.device)
+    num_pages, page_size, Hkv, cache_d = cache
     if Hkv != plan.num_kv_heads or cache_d != D:
         raise ValueError("the cache must have the plan's key/value heads and q's head size")
     if (page_stride | slot_stride | head_stride) % 8 or k_cache.data_ptr() % 16 or v_cache.data_ptr() % 16:

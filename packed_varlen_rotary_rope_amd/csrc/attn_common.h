@@ -125,7 +125,6 @@ __device__ inline uint32_t swizzle(uint32_t r) {
 constexpr int keys_per_block(int db) { return db <= 4 ? 64 : 32; }
 constexpr int chunks_per_row(int db) { return db <= 2 ? 8 : db <= 4 ? 16 : 32; }
 
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
