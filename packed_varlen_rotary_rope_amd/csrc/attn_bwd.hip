@@ -644,7 +644,12 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
       wait_copies<0>();
     };
     walk(Constant<kMasked>());
-    if (any_wave(any_nonfinite(dk) || any_nonfinite(dv), flags)) walk(Constant<kCareful>());
+    if (any_wave(any_nonfinite(dk) || any_nonfinite(dv), flags)) {
+      walk(Constant<kCareful>());
+      // The next tile's first copies go into buffers that the last block was read from (behind the
+      // walk above, any_wave has waited for all waves).
+      wait_copies_and_sync<0>();
+    }
 
     if (!whole) {
       float* part = p.part + (2 * (int64_t)share + (from == 0)) * 2 * kKeyTile * p.D +

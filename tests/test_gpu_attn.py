@@ -561,3 +561,37 @@ def test_very_large_scores(rope, D, dtype, a, b, sign):
         ref.check(out[s:e], want, want.abs() * 2.1 * ref.half_step(dtype), "out")
         score = (m.values.double() * 2.0 ** (a + b) * D ** 0.5)[:, None].expand(-1, 4)
         ref.check(lse[s:e], score, score.abs() * 2.0 ** -21, "lse")
+
+
+@pytest.mark.parametrize("D,G,dtype", [(32, 2, F16), (40, 1, BF16), (64, 1, BF16), (64, 3, F16), (80, 3, BF16), (128, 4, F16)])
+def test_rows_that_are_not_finite_among_short_sequences(rope, D, G, dtype):
+    """1200 sequences of 11 to 60 tokens, so that a workgroup of the dK/dV pass walks several key
+    tiles one behind the other, and in every third sequence one row of dout with an infinity: every
+    other column of dv keeps its bits, also in the keys that the row sees, and so does all that the
+    row does not reach. Several times: waves must not run into each other's tiles."""
+    print(f"[short, not finite] D={D} G={G} {dtype}", flush=True)
+    cu = [0]
+    for i in range(1200):
+        cu.append(cu[-1] + 11 + (7 * i) % 50)
+    T, Hkv = cu[-1], 2
+    q, k, v = batch(T, Hkv * G, Hkv, D, dtype, seed=D + G)
+    do = normal((T, Hkv * G, D), 5, dtype)
+    plan = rope.attn_plan(int32(cu), T, Hkv * G, Hkv)
+    out, lse = rope.attn_fwd(q, k, v, plan)
+    dq0, dk0, dv0 = rope.attn_bwd(do, q, k, v, out, lse, plan)
+    reached = torch.zeros(T, dtype=torch.bool)
+    rows = torch.zeros(T, dtype=torch.bool)
+    for s in range(0, 1200, 3):
+        at = cu[s] + (5 * s) % (cu[s + 1] - cu[s])
+        rows[at] = True
+        reached[cu[s]:at + 1] = True
+    rows, reached = rows.to(DEV), reached.to(DEV)
+    do[rows, G, 2] = float("inf")  # of the second key/value head's first query head
+    rest = torch.arange(D, device=DEV) != 2
+    for _ in range(4):
+        dq, dk, dv = rope.attn_bwd(do, q, k, v, out, lse, plan)
+        assert same(dv[:, :, rest], dv0[:, :, rest])
+        assert same(dv[~reached], dv0[~reached]) and same(dk[~reached], dk0[~reached])
+        assert same(dv[:, 0], dv0[:, 0]) and same(dk[:, 0], dk0[:, 0])
+        assert same(dq[~rows], dq0[~rows])
+        assert not bool(dv[reached][:, 1, 2].isfinite().any())
