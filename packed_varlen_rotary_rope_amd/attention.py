@@ -189,13 +189,15 @@ def attn_plan(cu_seqlens, T: int, num_q_heads: int, num_kv_heads: int, seqused=N
                          "key/value heads (the query heads must be a multiple)")
     if out is None:
         out = AttnPlan(T, num_seqs, Hq, Hkv, torch.empty(words, dtype=torch.int32, device=dev))
+    elif not isinstance(out, AttnPlan):
+        raise TypeError("out: expected what attn_plan returns")
     elif (out.T, out.num_seqs, out.num_q_heads, out.num_kv_heads, out.buffer.device) != \
             (T, num_seqs, Hq, Hkv, dev):
         raise ValueError("out: a plan of other sizes or of another device")
     else:
         torch.autograd.graph.increment_version(out.buffer)  # a backward that saved it shall know
     _call(dev, _lib.attn_plan, "attn_plan", _ptr(cu), num_seqs, _ptr(su), T, Hq, Hkv,
-          _ptr(out.buffer), words)
+          _ptr(out.buffer), out.buffer.numel())
     return out
 
 
@@ -378,11 +380,13 @@ def paged_plan(cu_seqlens, kv_lens, T: int, num_q_heads: int, num_kv_heads: int,
                          "key/value heads (the query heads must be a multiple)")
     if out is None:
         out = PagedPlan(T, num_seqs, Hq, Hkv, torch.empty(words, dtype=torch.int32, device=dev))
+    elif not isinstance(out, PagedPlan):
+        raise TypeError("out: expected what paged_plan returns")
     elif (out.T, out.num_seqs, out.num_q_heads, out.num_kv_heads, out.buffer.device) != \
             (T, num_seqs, Hq, Hkv, dev):
         raise ValueError("out: a plan of other sizes or of another device")
     _call(dev, _lib.paged_plan, "paged_plan", _ptr(cu), num_seqs, _ptr(lens), T, Hq, Hkv,
-          _ptr(out.buffer), words)
+          _ptr(out.buffer), out.buffer.numel())
     return out
 
 

@@ -205,3 +205,31 @@ def test_package_without_the_attention_library(tmp_path):
             "        raise SystemExit(name)\n")
     subprocess.run([sys.executable, "-c", code], check=True, cwd=tmp_path, timeout=300,
                    env={**os.environ, "PYTHONPATH": str(tmp_path)})
+
+
+def test_plans_are_not_written_over_by_the_other_kind(monkeypatch):
+    """The two kinds of plan are of different lengths, each longer for some batches: a plan given as
+    `out` is of the function's own kind, and its real length reaches the library. No GPU: the
+    launch is replaced."""
+    launched = []
+    monkeypatch.setattr(A, "_gpu", lambda device: None)
+    monkeypatch.setattr(A, "_call", lambda device, fn, what, *args: launched.append((what, args[-1])))
+    for T, Hq, Hkv in ((64, 4, 2), (2 ** 20, 1, 1)):
+        cu, lens = torch.tensor([0, T], dtype=torch.int32), torch.tensor([T], dtype=torch.int32)
+        words = A._lib.attn_plan_ints(T, 1, Hq, Hkv), A._lib.paged_plan_ints(T, 1, Hq, Hkv)
+        packed = rope.AttnPlan(T, 1, Hq, Hkv, torch.empty(words[0], dtype=torch.int32))
+        paged = rope.PagedPlan(T, 1, Hq, Hkv, torch.empty(words[1], dtype=torch.int32))
+        for wrong in (paged, packed.buffer, object()):
+            with pytest.raises(TypeError, match="attn_plan"):
+                rope.attn_plan(cu, T, Hq, Hkv, out=wrong)
+        for wrong in (packed, paged.buffer, object()):
+            with pytest.raises(TypeError, match="paged_plan"):
+                rope.paged_plan(cu, lens, T, Hq, Hkv, out=wrong)
+        assert launched == []
+        assert rope.attn_plan(cu, T, Hq, Hkv, out=packed) is packed
+        assert rope.paged_plan(cu, lens, T, Hq, Hkv, out=paged) is paged
+        short = rope.AttnPlan(T, 1, Hq, Hkv, torch.empty(40, dtype=torch.int32))
+        rope.attn_plan(cu, T, Hq, Hkv, out=short)  # the library refuses its length
+        assert launched == [("attn_plan", words[0]), ("paged_plan", words[1]), ("attn_plan", 40)]
+        launched.clear()
+        assert A._lib.attn_plan(FAKE, 1, None, T, Hq, Hkv, FAKE, 40, None) == EINVAL
