@@ -98,12 +98,16 @@ struct FwdTile {
   float m, l;  // m in base 2; while `exact` is set, a score as it is
   bool exact;  // read in kCareful mode only: m is subtracted before the scale, without rounding
 
-  // Whether scores are so large that scale * s - m, with m rounded, may be far from 0 for the
-  // largest of them, and its weight beyond the type's range: the walk is done again in kCareful
-  // mode with `exact` set, every block of it.
-  __device__ bool large() const {
+  bool was_large;  // of the wave: some row's m was large, and has risen since
+
+  static __device__ bool is_large(float m) {
     return __builtin_fabsf(m) > kLargeScore && __builtin_fabsf(m) < __builtin_inff();
   }
+  // Whether scores are so large that scale * s - m, with m rounded, may be far from 0 for the
+  // largest of them, and its weight beyond the type's range: the walk is done again in kCareful
+  // mode with `exact` set, every block of it. Any m counts that the row had: the sums of an earlier
+  // one may be infinite, which no later factor takes back.
+  __device__ bool large() const { return was_large || is_large(m); }
 
   __device__ void clear() {
 #pragma unroll
@@ -112,6 +116,7 @@ struct FwdTile {
       for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
     m = -__builtin_inff();
     l = 0.0f;
+    was_large = false;
   }
 
   // S^T of a block of keys, in KS steps; `piece(t)` is called in step t.
@@ -166,6 +171,7 @@ struct FwdTile {
     top = as_is ? half_max(top) : half_max(top) * scale;
     const bool rises = !((as_is ? (top - m) * scale : top - m) <= kRescale);
     if (__any(rises)) {  // for the rows that need it: a row's bits do not depend on others
+      was_large |= __any(rises && is_large(m));
       const float m_new = rises ? __builtin_fmaxf(m, top) : m;
       const float a = m == m_new ? 1.0f : __builtin_amdgcn_exp2f(as_is ? (m - m_new) * scale : m - m_new);
       m = m_new;

@@ -595,3 +595,34 @@ def test_rows_that_are_not_finite_among_short_sequences(rope, D, G, dtype):
         assert same(dv[:, 0], dv0[:, 0]) and same(dk[:, 0], dk0[:, 0])
         assert same(dq[~rows], dq0[~rows])
         assert not bool(dv[reached][:, 1, 2].isfinite().any())
+
+
+def first_large_then_ordinary(T, D, dtype, H, seed):
+    """Keys of which the first 64 have scores below -2^28 (f16) or -2^31 (bf16) once scaled and the
+    others scores of exactly 0, so that a query of the later ones weighs those alike."""
+    a = 5736.0 if dtype == F16 else 17536.0
+    q = torch.full((T, 2, D), a, dtype=dtype, device=DEV)
+    k = torch.zeros((T, H, D), dtype=dtype, device=DEV)
+    k[:64] = -a
+    return q, k, normal((T, H, D), seed, dtype)
+
+
+@pytest.mark.parametrize("D", [64, 128, 192])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("H", [1, 2])
+def test_very_large_scores_before_ordinary_ones(rope, D, dtype, H):
+    """A maximum that was large and is small in the end. n keys of score 0 have the weight 1 / n
+    each, exactly formed; their fp32 sum of n products errs by n 2^-23 of its spread, and out is
+    rounded once. The rows before see equal scores too, however large."""
+    print(f"[large first] D={D} {dtype} H={H}", flush=True)
+    T = 400
+    q, k, v = first_large_then_ordinary(T, D, dtype, H, 6)
+    out, lse = rope.attn_fwd(q, k, v, rope.attn_plan(int32([0, T]), T, 2, H))
+    v64 = v.repeat_interleave(2 // H, 1).double()
+    for a, b in ((0, 64), (64, T)):
+        n = torch.arange(1, b - a + 1, device=DEV, dtype=torch.float64)[:, None, None]
+        mean, spread = v64[a:b].cumsum(0) / n, v64[a:b].abs().cumsum(0) / n
+        ref.check(out[a:b], mean, 1.01 * (ref.half_step(dtype) * mean.abs() + T * 2.0 ** -23 * spread) +
+                  ref.tiny(dtype), f"out from {a}")
+    n = torch.arange(1, T - 63, device=DEV, dtype=torch.float64)[:, None].expand(-1, 2)
+    ref.check(lse[64:], n.log(), (n.log() + 1) * 2.0 ** -21, "lse")

@@ -444,3 +444,28 @@ def test_very_large_scores(rope, D, new, dtype, a, b, sign):
     ref.check(out, want, want.abs() * 2.1 * ref.half_step(dtype), "out")
     score = (m.values[held - new:].double() * 2.0 ** (a + b) * D ** 0.5)[:, None].expand(-1, 4)
     ref.check(lse, score, score.abs() * 2.0 ** -21, "lse")
+
+
+@pytest.mark.parametrize("D,new", [(64, 1), (128, 1), (128, 8), (128, 100), (192, 9), (256, 90)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("held", [400, 4000])
+def test_very_large_scores_before_ordinary_ones(rope, D, new, dtype, held):
+    """As test_gpu_attn's: the first 64 keys' scores are below -2^28, the others 0; the new tokens
+    weigh the others alike."""
+    print(f"[large first] D={D} new={new} {dtype} {held}", flush=True)
+    a = 5736.0 if dtype == F16 else 17536.0
+    page = 16
+    q = torch.full((new, 4, D), a, dtype=dtype, device=DEV)
+    k = torch.zeros((held, 2, D), dtype=dtype, device=DEV)
+    k[:64] = -a
+    v = normal((held, 2, D), 6, dtype)
+    table = torch.arange(held // page, dtype=torch.int32, device=DEV)[None]
+    plan = rope.paged_plan(int32([0, new]), int32([held]), new, 4, 2)
+    out, lse = rope.attn_paged(q, k.view(-1, page, 2, D), v.view(-1, page, 2, D), table, plan)
+    v64 = v.repeat_interleave(2, 1).double()[64:]
+    n = torch.arange(1, held - 63, device=DEV, dtype=torch.float64)[:, None, None]
+    mean, spread = (v64.cumsum(0) / n)[-new:], (v64.abs().cumsum(0) / n)[-new:]
+    ref.check(out, mean, 1.01 * (ref.half_step(dtype) * mean.abs() + held * 2.0 ** -23 * spread) + ref.tiny(dtype),
+              "out")
+    want = n[-new:, :, 0].log().expand(-1, 4)
+    ref.check(lse, want, (want + 1) * 2.0 ** -21, "lse")
