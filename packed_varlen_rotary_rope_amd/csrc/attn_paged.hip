@@ -11,7 +11,7 @@
 //  * up to 32 rows (decode): the four waves have the same rows and take key blocks in turn,
 //    each with its own LDS, so that none waits for another and K and V stream all the time
 //    (bound by memory); their results are joined in LDS at the end.
-// Splits leave (m, l, O) in fp32, and a second, small kernel joins them in a fixed order.
+// Splits leave (m, its rounding, l, O) in fp32, and a second, small kernel joins them in a fixed order.
 //
 // Keys are found through the block table: a block's page numbers arrive in LDS by an
 // asynchronous copy two blocks ahead, a lane turns one key's page into its row's offset, and
@@ -189,7 +189,7 @@ struct PagedParams {
   void* out;
   float* lse;
   float* part_o;   // [unit][Hkv][32][D], not normalized
-  float* part_ml;  // [unit][Hkv][32][2]
+  float* part_ml;  // [unit][Hkv][32][4]: m in base 2, what its rounding left, l
   const int32_t* plan;
   const Item* items;
   const Join* joins;
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * kTileBytes];
   __shared__ __attribute__((aligned(16))) uint8_t pages[4][512];
   __shared__ __attribute__((aligned(16))) uint8_t offsets[4][2 * 64 * 8];
-  __shared__ float joined[4][2][32];
+  __shared__ float joined[4][3][32];
 
   const uint32_t index = div31(blockIdx.x, p.by_hkv);
   const uint32_t kvh = blockIdx.x - index * p.Hkv;
@@ -371,10 +371,11 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
     };
     walk(Constant<kMasked>());
     const uint32_t anew = any_wave(any_nonfinite(t.o) | (uint32_t)t.large() << 1, lds);
+    float low = 0.0f;
     if (anew) {
       t.exact = anew & 2;
       walk(Constant<kCareful>());
-      t.scale_maximum(p.scale);
+      low = t.scale_maximum(p.scale);
     }
     if (item.slot < 0) {
       const float lse = t.finish();
@@ -385,10 +386,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
     const int64_t unit = ((int64_t)(item.slot + wave) * p.Hkv + kvh) * 32 + (lane & 31);
     const float l = half_sum(t.l);
     if (!on) return;
-    if (half == 0) {
-      p.part_ml[2 * unit] = t.m;
-      p.part_ml[2 * unit + 1] = l;
-    }
+    if (half == 0) *reinterpret_cast<f32x4*>(p.part_ml + 4 * unit) = (f32x4){t.m, low, l, 0.0f};
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -407,6 +405,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   constexpr bool kOneBuffer = DB > 4;
   constexpr int kLoads = 32 * CPR / 64;
   FwdTile<T, DB, 32> t;
+  float low = 0.0f;
   load_row<T>(t.q, q_row, half, chunks);
   {
     const PagedKeys<32, CPR> src{table, pages[wave], offsets[wave], key_end};
@@ -471,7 +470,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
     t.exact = __any(t.large());  // this wave alone
     if (t.exact || __any(any_nonfinite(t.o))) {
       walk(Constant<kCareful>());
-      t.scale_maximum(p.scale);
+      low = t.scale_maximum(p.scale);
     }
   }
 
@@ -480,14 +479,25 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   const float l = half_sum(t.l);
   if (half == 0) {
     joined[wave][0][lane] = t.m;
-    joined[wave][1][lane] = l;
+    joined[wave][1][lane] = low;
+    joined[wave][2][lane] = l;
   }
   __syncthreads();
   const uint32_t r = lane & 31;
-  float top = joined[0][0][r];
+  auto find_top = [&](uint32_t y, float& m, float& m_low) __attribute__((always_inline)) {
+    m = joined[0][0][y];
+    m_low = joined[0][1][y];
 #pragma unroll
-  for (int w = 1; w < 4; ++w) top = __builtin_fmaxf(top, joined[w][0][r]);
-  const float factor = t.m == top ? 1.0f : __builtin_amdgcn_exp2f(t.m - top);
+    for (int w = 1; w < 4; ++w) {
+      const float mw = joined[w][0][y], lw = joined[w][1][y];
+      const bool higher = above(mw, lw, m, m_low);
+      m = higher ? mw : m;
+      m_low = higher ? lw : m_low;
+    }
+  };
+  float top, top_low;
+  find_top(r, top, top_low);
+  const float factor = join_factor(t.m, low, top, top_low);
   constexpr int kColumns = DB < 4 ? DB : 4;  // blocks of 32 columns a time
   constexpr int kGroups = kColumns * 8;      // 16-byte groups of a row
   const int32_t n_rows = row_end - item.row0;
@@ -512,26 +522,21 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
       const uint32_t y = i / kGroups, group = i % kGroups;
       const uint32_t e = 32 * d0 + 4 * group;
       f32x4 x = {0, 0, 0, 0};
-      float m = joined[0][0][y], sum = 0.0f;
-#pragma unroll
-      for (int w = 1; w < 4; ++w) m = __builtin_fmaxf(m, joined[w][0][y]);
+      float m, m_low, sum = 0.0f;
+      find_top(y, m, m_low);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const f32x4 part = *reinterpret_cast<const f32x4*>(
             lds + w * kTileBytes + (y * kGroups + (group ^ (y & 7))) * 16);
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[c] += part[c];
-        const float mw = joined[w][0][y];
-        sum += joined[w][1][y] * (mw == m ? 1.0f : __builtin_amdgcn_exp2f(mw - m));
+        sum += joined[w][2][y] * join_factor(joined[w][0][y], joined[w][1][y], m, m_low);
       }
       if (e >= (uint32_t)p.D) continue;
       if (item.slot >= 0) {
         const int64_t unit = ((int64_t)item.slot * p.Hkv + kvh) * 32 + y;
         *reinterpret_cast<f32x4*>(p.part_o + unit * p.D + e) = x;
-        if (e == 0) {
-          p.part_ml[2 * unit] = m;
-          p.part_ml[2 * unit + 1] = sum;
-        }
+        if (e == 0) *reinterpret_cast<f32x4*>(p.part_ml + 4 * unit) = (f32x4){m, m_low, sum, 0.0f};
       } else {
         const int32_t packed = item.row0 + y, tok = div31(packed, p.by_g);
         const int32_t h = kvh * p.G + (packed - tok * p.G);
@@ -546,7 +551,8 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   }
 }
 
-// Joins the splits of a tile: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.
+// Joins the splits of a tile: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, each m_i with what
+// its rounding left.
 template <typename T>
 __global__ __launch_bounds__(256) void paged_join_kernel(const PagedParams p) {
   const uint32_t index = div31(blockIdx.x, p.by_hkv);
@@ -563,32 +569,37 @@ __global__ __launch_bounds__(256) void paged_join_kernel(const PagedParams p) {
   const int64_t unit0 = ((int64_t)(j.slot + part) * p.Hkv + kvh) * 32;
   for (int32_t i = threadIdx.x; i < rows * (int32_t)groups; i += 256) {
     const uint32_t y = i / groups, e = 4 * (i - y * groups);
-    const float* ml = p.part_ml + 2 * (unit0 + y);
+    const float* ml = p.part_ml + 4 * (unit0 + y);
     const float* o = p.part_o + (unit0 + y) * p.D + e;
-    float m = -__builtin_inff(), l = 0.0f;
+    float m = -__builtin_inff(), low = 0.0f, l = 0.0f;
     f32x4 x = {0, 0, 0, 0};
     for (int32_t s0 = 0; s0 < j.splits; s0 += 8) {  // eight splits' loads at a time
-      f32x2 w[8];
+      f32x4 w[8];
       f32x4 v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int64_t s = min(s0 + u, j.splits - 1);
-        w[u] = *reinterpret_cast<const f32x2*>(ml + 2 * s * step);
+        w[u] = *reinterpret_cast<const f32x4*>(ml + 4 * s * step);
         v[u] = *reinterpret_cast<const f32x4*>(o + s * step * p.D);
       }
-      float top = m;
+      float top = m, top_low = low;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) top = __builtin_fmaxf(top, w[u][0]);
-      const float f0 = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+      for (int u = 0; u < 8; ++u) {
+        const bool higher = above(w[u][0], w[u][1], top, top_low);
+        top = higher ? w[u][0] : top;
+        top_low = higher ? w[u][1] : top_low;
+      }
+      const float f0 = join_factor(m, low, top, top_low);
       m = top;
+      low = top_low;
       l *= f0;
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[c] *= f0;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         if (s0 + u >= j.splits) break;
-        const float f = w[u][0] == m ? 1.0f : __builtin_amdgcn_exp2f(w[u][0] - m);
-        l = __builtin_fmaf(w[u][1], f, l);
+        const float f = join_factor(w[u][0], w[u][1], m, low);
+        l = __builtin_fmaf(w[u][2], f, l);
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[c] = __builtin_fmaf(v[u][c], f, x[c]);
       }
@@ -644,7 +655,7 @@ int64_t paged_plan_ints(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv) {
 
 int64_t paged_workspace_floats(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D) {
   if (attn_plan_ints(T, num_seqs, Hq, Hkv) < 0 || !valid_head_size(D)) return -1;
-  return paged_sizes(T, num_seqs, Hq, Hkv).units * Hkv * 32 * (D + 2);
+  return paged_sizes(T, num_seqs, Hq, Hkv).units * Hkv * 32 * (D + 4);
 }
 
 int32_t paged_plan(const int32_t* cu_seqlens, int32_t num_seqs, const int32_t* kv_lens, int64_t T,

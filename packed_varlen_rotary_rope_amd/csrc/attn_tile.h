@@ -238,9 +238,12 @@ struct FwdTile {
     accumulate<MODE>(p, vt, key0, seen, hidden, lane);
   }
 
-  // Ends a walk with `exact` set.
-  __device__ void scale_maximum(float scale) {
-    if (exact) m *= scale;
+  // Ends a walk with `exact` set: m in base 2. Returns what its rounding leaves, without which the
+  // sums of two walks cannot be joined: half a step of a large m may be any number of powers of 2.
+  __device__ float scale_maximum(float scale) {
+    const float s = m;
+    if (exact) m = s * scale;
+    return exact && __builtin_fabsf(m) < __builtin_inff() ? __builtin_fmaf(s, scale, -m) : 0.0f;
   }
 
   // Normalizes O and returns the row's log-sum-exp.
@@ -254,6 +257,15 @@ struct FwdTile {
     return log_sum_exp(m, l);
   }
 };
+
+// The maxima of walks that are joined, each m + low. What the sums at (m, low) are multiplied by
+// to stand at (top, top_low); with both infinite, or none seen in either, that is 1.
+__device__ inline bool above(float m, float low, float m2, float low2) {
+  return m > m2 || (m == m2 && low > low2);
+}
+__device__ inline float join_factor(float m, float low, float top, float top_low) {
+  return m == top && low == top_low ? 1.0f : __builtin_amdgcn_exp2f((m - top) + (low - top_low));
+}
 
 // The chunks of a tile's rows that no load fills (head sizes below CPR chunks) are zeroed
 // once: products of them with q's zeros must not be NaN.

@@ -469,3 +469,36 @@ def test_very_large_scores_before_ordinary_ones(rope, D, new, dtype, held):
               "out")
     want = n[-new:, :, 0].log().expand(-1, 4)
     ref.check(lse, want, (want + 1) * 2.0 ** -21, "lse")
+
+
+@pytest.mark.parametrize("D,new", [(64, 1), (128, 8), (256, 3), (64, 300), (256, 200)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("c", [83, 101, 127])
+def test_very_large_scores_close_together(rope, D, new, dtype, c):
+    """One key's score is one step of fp32 above all the others', which are about 2^29: they weigh
+    exp(-8) each (D 128: exp(-5.7)), whichever waves and splits they fall in, though scale * s is
+    known to half a step of 8 to 16 there. Scores are exact; a weight errs by its rounding and
+    2^-18 (an exponent of about 12 in fp32, twice), sums of n terms by n 2^-23 of their spread."""
+    print(f"[close] D={D} new={new} {dtype} {c}", flush=True)
+    held, page, high = 4000, 16, 1234
+    parts = 2 if D == 256 else 1  # the score is c 2^23 for each of these columns
+    step = 64.0 * parts
+    q, k = torch.zeros((new, 4, D), device=DEV), torch.zeros((held, 2, D), device=DEV)
+    q[..., :parts], k[..., :parts] = c * 2.0 ** 8, 2.0 ** 15
+    q[..., 40], k[high, :, 40] = 1.0, step
+    q, k, v = q.to(dtype), k.to(dtype), normal((held, 2, D), 6, dtype)
+    table = torch.arange(held // page, dtype=torch.int32, device=DEV)[None]
+    plan = rope.paged_plan(int32([0, new]), int32([held]), new, 4, 2)
+    out, lse = rope.attn_paged(q, k.view(-1, page, 2, D), v.view(-1, page, 2, D), table, plan)
+    t = torch.arange(held, device=DEV)
+    p = torch.full((new, held), -step * D ** -0.5, dtype=torch.float64, device=DEV).exp()
+    p[:, high] = 1.0
+    p = p.masked_fill(t[None] > held - new + torch.arange(new, device=DEV)[:, None], 0.0)
+    p = p / p.sum(-1, keepdim=True)
+    u = ref.half_step(dtype)
+    for h in range(4):
+        want, spread = p @ v[:, h // 2].double(), p @ v[:, h // 2].double().abs()
+        ref.check(out[:, h], want, 1.01 * (u * (want.abs() + spread) + (held * 2.0 ** -23 + 2.0 ** -18) * spread) +
+                  ref.tiny(dtype), f"out of head {h}")
+    score = torch.full((new, 4), c * 2.0 ** 23 * parts * D ** -0.5, dtype=torch.float64, device=DEV)
+    ref.check(lse, score, score * 2.0 ** -21, "lse")
