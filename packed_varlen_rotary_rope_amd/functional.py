@@ -210,12 +210,13 @@ def rope_qk_table(q: torch.Tensor, k: torch.Tensor, cos_tab: torch.Tensor, sin_t
 
 def _rows_for_kernel(t: torch.Tensor) -> torch.Tensor:
     """t itself where the attention kernels take its layout, else a contiguous copy (upstream
-    gradients come in any layout, expanded ones among them)."""
+    gradients come in any layout and at any address, expanded ones among them)."""
     T, H, D = t.shape
-    if t.stride(2) == 1 and t.stride(1) == D and t.stride(0) % 8 == 0 and t.stride(0) >= H * D and \
-            t.data_ptr() % 16 == 0:
+    if t.stride(2) == 1 and t.stride(1) == D and t.stride(0) % 8 == 0 and \
+            H * D <= t.stride(0) < 1 << 24 and t.data_ptr() % 16 == 0:
         return t
-    return t.contiguous()
+    # a copy also of what is contiguous, and begins at an odd address
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 def _plan_of(plan, cu_seqlens, seqused, T, Hq, Hkv):

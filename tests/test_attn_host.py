@@ -233,3 +233,22 @@ def test_plans_are_not_written_over_by_the_other_kind(monkeypatch):
         assert launched == [("attn_plan", words[0]), ("paged_plan", words[1]), ("attn_plan", 40)]
         launched.clear()
         assert A._lib.attn_plan(FAKE, 1, None, T, Hq, Hkv, FAKE, 40, None) == EINVAL
+
+
+def test_upstream_gradients_of_any_layout_are_laid_out_for_the_kernels():
+    """Contiguous rows at an odd address, as behind another tensor of one concatenated buffer, and
+    tokens further apart than the kernels take, are copied; what they take is passed on as it is."""
+    T, H, D = 5, 2, 16
+    flat = torch.arange(T * H * D + 64, dtype=torch.float32).bfloat16()
+    flat = flat[(-flat.data_ptr() // 2) % 8:]
+    for first in (1, 3, 4):
+        t = flat[first:first + T * H * D].view(T, H, D)
+        got = F._rows_for_kernel(t)
+        assert torch.equal(got, t) and got.data_ptr() % 16 == 0 and got.is_contiguous()
+    for t in (flat[:T * H * D].view(T, H, D), flat[8:8 + T * H * D].view(T, H, D), flat[:T * 40].view(T, 40)[:, 8:40].view(T, H, D)):
+        assert F._rows_for_kernel(t) is t
+    for t in (flat[:1].expand(T, H, D), flat[:T * H * D].view(H, T, D).transpose(0, 1)):
+        assert F._rows_for_kernel(t).is_contiguous()
+    far = torch.empty((1,), dtype=torch.bfloat16).expand(2, H, D).as_strided((2, H, D), (0, 0, 0))
+    wide = torch.empty((2, 1 << 24), dtype=torch.bfloat16)[:, :H * D].view(2, H, D)
+    assert F._rows_for_kernel(far).stride(0) == F._rows_for_kernel(wide).stride(0) == H * D

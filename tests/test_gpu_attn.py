@@ -626,3 +626,22 @@ def test_very_large_scores_before_ordinary_ones(rope, D, dtype, H):
                   ref.tiny(dtype), f"out from {a}")
     n = torch.arange(1, T - 63, device=DEV, dtype=torch.float64)[:, None].expand(-1, 2)
     ref.check(lse[64:], n.log(), (n.log() + 1) * 2.0 ** -21, "lse")
+
+
+def test_gradient_at_an_odd_address(rope):
+    """Outputs that go into one flat buffer behind something else: their gradient is contiguous and
+    not aligned."""
+    import packed_varlen_rotary_rope_amd.functional as F
+    cu = int32([0, 20, 50])
+    leaves = [x.requires_grad_() for x in batch(50, 4, 2, 64, BF16)]
+    plan = rope.attn_plan(cu, 50, 4, 2)
+    weights = normal((3 + 50 * 4 * 64,), 8, BF16)
+    (torch.cat([torch.zeros(3, dtype=BF16, device=DEV), F.attn(*leaves, plan).flatten()]) * weights).sum().backward()
+    q, k, v = (x.detach() for x in leaves)
+    out, lse = rope.attn_fwd(q, k, v, plan)
+    do = weights[3:].view(50, 4, 64).clone()
+    for x, g in zip(leaves, rope.attn_bwd(do, q, k, v, out, lse, plan)):
+        assert same(x.grad, g)
+    fused = torch.cat([x.flatten(1) for x in (q, k, v)], 1).requires_grad_()
+    (torch.cat([torch.zeros(3, dtype=BF16, device=DEV), F.attn_qkv(fused, 4, 2, plan).flatten()]) * weights).sum().backward()
+    assert same(fused.grad, torch.cat([x.grad.flatten(1) for x in leaves], 1))
