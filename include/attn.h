@@ -110,7 +110,9 @@ int32_t attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
  * p of sequence s lies in page block_table[s * table_stride + p / page_size], slot p %
  * page_size. kv_lens[s] counts the tokens that sequence s holds, the new ones included; the
  * new tokens are rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 of q, k and v, so token i of them
- * is at position kv_lens[s] - n + i. A page number outside 0 .. num_pages - 1 is no page. */
+ * is at position kv_lens[s] - n + i. Entries of cu_seqlens count as clamped to [0, T], and are
+ * non-decreasing (where they are not, memory stays safe, but append and plan may differ in whose
+ * token it is). A page number outside 0 .. num_pages - 1 is no page. */
 
 /* Writes the new tokens' keys and values into the cache, the keys rotated as rope_qk_fwd
  * rotates them at their position, and the new queries, rotated, to q_out. One launch.

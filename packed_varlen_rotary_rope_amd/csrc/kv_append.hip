@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(const AppendParams 
   int64_t pos = -1;
   int64_t row = -1;  // the token's row of the cache, in elements from its base
   if (s >= 0) {
-    pos = (int64_t)p.kv_lens[s] - p.cu[s + 1] + t;
+    pos = (int64_t)p.kv_lens[s] - min(p.cu[s + 1], p.T) + t;  // as paged_plan reads it
     if (pos >= 0 && pos < INT32_MAX) {
       const uint32_t block = div31((uint32_t)pos, p.by_page);
       if (block < (uint32_t)p.max_pages) {

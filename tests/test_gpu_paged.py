@@ -502,3 +502,21 @@ def test_very_large_scores_close_together(rope, D, new, dtype, c):
                   ref.tiny(dtype), f"out of head {h}")
     score = torch.full((new, 4), c * 2.0 ** 23 * parts * D ** -0.5, dtype=torch.float64, device=DEV)
     ref.check(lse, score, score * 2.0 ** -21, "lse")
+
+
+def test_sequences_that_leave_the_rows(rope):
+    """cu_seqlens with entries outside of the T rows: append and plan both count the rows that are
+    there as the last of the held tokens."""
+    Hq, Hkv, D, page, T = 4, 2, 64, 16, 8
+    q, k, v = normal((T, Hq, D), 3, BF16), normal((T, Hkv, D), 4, BF16), normal((T, Hkv, D), 5, BF16)
+    table, lens = int32([[0, 1], [2, 3], [4, 5]]), int32([20, 9, 30])
+    got = []
+    for cu in ([0, 5, 12, 40], [0, 5, T, T], [-3, 5, 2 ** 31 - 1, 2 ** 31 - 1]):
+        print(f"[cu_seqlens] {cu}", flush=True)
+        kc, vc = normal((6, page, Hkv, D), 1, BF16), normal((6, page, Hkv, D), 2, BF16)
+        tq = rope.kv_append_(k, v, kc, vc, table, int32(cu), lens, 1e4, q=q)
+        out, lse = rope.attn_paged(tq, kc, vc, table, rope.paged_plan(int32(cu), lens, T, Hq, Hkv))
+        got.append((kc, vc, tq, out, lse))
+    assert same(got[0][0][2, 6:9], got[1][0][2, 6:9])  # the second sequence's rows at positions 6 .. 8
+    for other in (got[0], got[2]):
+        assert all(same(a, b) for a, b in zip(other, got[1]))
