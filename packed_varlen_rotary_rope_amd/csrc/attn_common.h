@@ -133,9 +133,11 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // not set in `lanes` write nothing. For whole waves in uniform flow: all lanes are active, and
 // are again behind it. In assembly because the compiler otherwise waits for every copy in
 // flight before each transposed read of LDS, also of a buffer that no copy writes, and breaks
-// the loop up where lanes are left out. m0 holds the LDS address and needs one wait state (the
-// compiler keeps no value of its own there).
+// the loop up where lanes are left out. m0 holds the LDS address and needs one wait state; it is
+// declared, which the compiler heeds and warns of. exec holds what it held before.
 // Whoever reads the data waits first (wait_copies).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ inline uint32_t lds_address(const uint8_t* p) {
   return (uint32_t)(uintptr_t)(lds_void*)p;
 }
@@ -145,14 +147,15 @@ __device__ inline void copy_chunk_to_lds(const void* src, uint32_t dst, uint64_t
       "s_mov_b64 exec, -1"
       :
       : "v"(src), "s"(__builtin_amdgcn_readfirstlane(dst)), "s"(lanes)
-      : "memory");
+      : "memory", "m0");
 }
 __device__ inline void copy_word_to_lds(const void* src, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
                :
                : "v"(src), "s"(__builtin_amdgcn_readfirstlane(dst))
-               : "memory");
+               : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Waits until at most LEFT of this wave's copies (and loads) are in flight, the newest.
 template <int LEFT>
