@@ -57,6 +57,7 @@ _lib = _load()
 
 _HALF = (torch.bfloat16, torch.float16)
 _ANY = (torch.float32, torch.bfloat16, torch.float16)
+_INT32_MAX = 2 ** 31 - 1
 
 
 def _call(device: torch.device, fn, what: str, *args) -> None:
@@ -278,6 +279,8 @@ def _caches(k_cache, v_cache, dtype, device):
         raise ValueError("k_cache and v_cache must have one shape and layout")
     if shape[0] < 1 or shape[1] < 1:
         raise ValueError("the cache needs at least one page of at least one slot")
+    if shape[0] > _INT32_MAX or shape[1] > _INT32_MAX:
+        raise ValueError("the cache has more pages or slots than int32 numbers name")
     if shape[3] > 1 and stride[3] != 1:
         raise ValueError("the D elements of a cache row must be contiguous")
     return shape, stride

@@ -252,3 +252,15 @@ def test_upstream_gradients_of_any_layout_are_laid_out_for_the_kernels():
     far = torch.empty((1,), dtype=torch.bfloat16).expand(2, H, D).as_strided((2, H, D), (0, 0, 0))
     wide = torch.empty((2, 1 << 24), dtype=torch.bfloat16)[:, :H * D].view(2, H, D)
     assert F._rows_for_kernel(far).stride(0) == F._rows_for_kernel(wide).stride(0) == H * D
+
+
+def test_more_pages_than_a_table_can_name_are_refused():
+    """Page numbers are int32; a larger count would reach the library cut to its low bits. The
+    cache here is one element seen many times, only its shape is read."""
+    one = torch.zeros(8, dtype=torch.bfloat16)
+    for shape in ((2 ** 32 + 5, 1, 1, 8), (1, 2 ** 31, 1, 8)):
+        cache = one.as_strided(shape, (0, 0, 0, 1))
+        with pytest.raises(ValueError, match="int32"):
+            A._caches(cache, cache, torch.bfloat16, cache.device)
+    assert A._caches(one.as_strided((5, 2, 1, 8), (0, 0, 0, 1)), one.as_strided((5, 2, 1, 8), (0, 0, 0, 1)),
+                     torch.bfloat16, one.device)[0] == (5, 2, 1, 8)
