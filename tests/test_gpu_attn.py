@@ -645,3 +645,22 @@ def test_gradient_at_an_odd_address(rope):
     fused = torch.cat([x.flatten(1) for x in (q, k, v)], 1).requires_grad_()
     (torch.cat([torch.zeros(3, dtype=BF16, device=DEV), F.attn_qkv(fused, 4, 2, plan).flatten()]) * weights).sum().backward()
     assert same(fused.grad, torch.cat([x.grad.flatten(1) for x in leaves], 1))
+
+
+def test_many_sequences_gradients(rope):
+    """The gradients of 3001 sequences of up to 4 tokens, several of them in each tile of a
+    workgroup's share, each against the formula in 64 bits (on the CPU: they are many and small)."""
+    lengths = [(7 * i) % 5 for i in range(3001)]
+    cu = [0]
+    for n in lengths:
+        cu.append(cu[-1] + n)
+    T = cu[-1] + 9
+    q, k, v = batch(T, 4, 2, 64, BF16, seed=15)
+    do = normal((T, 4, 64), 16, BF16)
+    plan = rope.attn_plan(int32(cu), T, 4, 2)
+    out, lse = rope.attn_fwd(q, k, v, plan)
+    got = rope.attn_bwd(do, q, k, v, out, lse, plan)
+    want, tols = ref.backward(*(x.cpu() for x in (do, q, k, v)), ref.sequences(cu, T), 0.125, BF16)
+    for name, g, w, tol in zip(("dq", "dk", "dv"), got, want, tols):
+        assert bool((g[cu[-1]:] == 0).all())
+        ref.check(g.cpu(), w, tol, name)
