@@ -664,3 +664,64 @@ def test_many_sequences_gradients(rope):
     for name, g, w, tol in zip(("dq", "dk", "dv"), got, want, tols):
         assert bool((g[cu[-1]:] == 0).all())
         ref.check(g.cpu(), w, tol, name)
+
+
+def mixed_scores(n, m, heads, D, dtype, seed):
+    """q [n, heads[0], D] and k [m, heads[1], D] of powers of 2 and zeros, each token at a magnitude
+    of its own, so that every product of two rows is exact in fp32 and scores run from 1 to 2^60
+    (f16: 2^27) side by side."""
+    g = torch.Generator().manual_seed(seed)
+    tops = torch.tensor([0, 0, 1, 4, 9, 17, 27] if dtype == BF16 else [0, 0, 1, 4, 7, 9, 12])
+
+    def rows(count, h):
+        sign = torch.randint(-1, 2, (count, h, D), generator=g).float()
+        size = tops[torch.randint(0, len(tops), (count, h), generator=g)].float()
+        return (sign * 2.0 ** size[..., None]).to(dtype).to(DEV)
+
+    return rows(n, heads[0]), rows(m, heads[1])
+
+
+def head_of_any_scores(q, k, v, scale, before, gone=None):
+    """One head in 64 bits as attn_reference.head_forward, with the maximum taken off before the
+    logarithm: past 2^50 a log-sum-exp of 64 bits no longer holds the logarithm."""
+    n, m = q.shape[0], k.shape[0]
+    hidden = torch.arange(m, device=DEV)[None] > before + torch.arange(n, device=DEV)[:, None]
+    if gone is not None:
+        hidden = hidden | gone[None]
+        k = k.masked_fill(gone[:, None], 0.0)
+    s = (q.double() @ k.double().T * scale).masked_fill(hidden, float("-inf"))
+    top = s.amax(-1, keepdim=True)
+    e = torch.exp(s - top.masked_fill(top == float("-inf"), 0.0))
+    total = e.sum(-1, keepdim=True)
+    p = e / total.masked_fill(total == 0.0, 1.0)
+    return p @ v, (top + total.log())[:, 0], p
+
+
+def exact_scores_bound(o, p, v, dtype, n):
+    """Bound of out where scores are exact: a weight 2^-x is formed from an exponent that errs by
+    2^-22 x (scale, product and join, in fp32), which moves it by 2^-22 x 2^-x < 2^-22 of the
+    largest, and is rounded once (subnormal f16 weights by 2^-25 of the largest); sums of n terms
+    err by n 2^-23."""
+    u = ref.half_step(dtype)
+    spread = p @ v.abs()
+    largest = p.amax(-1, keepdim=True) * v.abs().sum(0)
+    return 1.01 * (u * (o.abs() + spread) + (n + 32) * 2.0 ** -23 * spread + 2.0 ** -21 * largest) + ref.tiny(dtype)
+
+
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("D,Hq,Hkv", [(32, 4, 1), (64, 4, 2), (128, 2, 2), (192, 3, 1)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_scores_of_all_sizes(rope, seed, D, Hq, Hkv, dtype):
+    """Ordinary, large and very large scores in one batch, in any order and with ties."""
+    print(f"[all sizes] {seed} D={D} {Hq}+{Hkv} {dtype}", flush=True)
+    cu, T = [0, 5, 150, 151, 480], 480
+    q, k = mixed_scores(T, T, (Hq, Hkv), D, dtype, seed)
+    v = normal((T, Hkv, D), seed, dtype)
+    out, lse = rope.attn_fwd(q, k, v, rope.attn_plan(int32(cu), T, Hq, Hkv))
+    for a, n in ref.sequences(cu, T):
+        rows = slice(a, a + n)
+        for h in range(Hq):
+            v64 = v[rows, h // (Hq // Hkv)].double()
+            o, l, p = head_of_any_scores(q[rows, h], k[rows, h // (Hq // Hkv)], v64, D ** -0.5, 0)
+            ref.check(out[rows, h], o, exact_scores_bound(o, p, v64, dtype, n), "out")
+            ref.check(lse[rows, h], l, (l.abs() + 8) * 2.0 ** -21, "lse")

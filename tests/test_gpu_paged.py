@@ -520,3 +520,36 @@ def test_sequences_that_leave_the_rows(rope):
     assert same(got[0][0][2, 6:9], got[1][0][2, 6:9])  # the second sequence's rows at positions 6 .. 8
     for other in (got[0], got[2]):
         assert all(same(a, b) for a, b in zip(other, got[1]))
+
+
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("D,Hq,Hkv", [(32, 4, 1), (64, 4, 2), (128, 2, 2), (192, 3, 1), (256, 2, 2)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("new,held", [([1, 1, 3], [700, 33, 2500]), ([60, 1, 200], [300, 9, 1111])])
+def test_scores_of_all_sizes(rope, seed, D, Hq, Hkv, dtype, new, held):
+    """As test_gpu_attn's, over a cache with NaN behind the sequences and a page that is none: parts
+    of a row with ordinary and with very large maxima are joined."""
+    from test_gpu_attn import exact_scores_bound, head_of_any_scores, mixed_scores
+    print(f"[all sizes] {seed} D={D} {Hq}+{Hkv} {dtype} {new}", flush=True)
+    page, cu = 16, [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    k, v, table = pool(held, page, Hkv, D, dtype, 40 + seed)
+    q, _ = mixed_scores(cu[-1], 1, (Hq, Hkv), D, dtype, 2 * seed)
+    for s, m in enumerate(held):
+        at = torch.arange(m, device=DEV)
+        k[table[s].long()[at // page], at % page] = mixed_scores(1, m, (Hq, Hkv), D, dtype, 100 * seed + s)[1]
+    table[2, 5] = -1
+    plan = rope.paged_plan(int32(cu), int32(held), cu[-1], Hq, Hkv)
+    out, lse = rope.attn_paged(q, k, v, table, plan)
+    for s, (n, m) in enumerate(zip(new, held)):
+        rows, at = slice(cu[s], cu[s + 1]), torch.arange(m, device=DEV)
+        number = table[s].long()[at // page]
+        gone = number < 0
+        where = number.clamp_min(0), at % page
+        for h in range(Hq):
+            kh, vh = k[where][:, h // (Hq // Hkv)], v[where][:, h // (Hq // Hkv)].double()
+            vh = vh.masked_fill(gone[:, None], 0.0)
+            o, l, p = head_of_any_scores(q[rows, h], kh, vh, D ** -0.5, m - n, gone)
+            ref.check(out[rows, h], o, exact_scores_bound(o, p, vh, dtype, m), "out")
+            ref.check(lse[rows, h], l, (l.abs() + 8) * 2.0 ** -21, "lse")
