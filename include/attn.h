@@ -18,9 +18,9 @@
  * Products are formed on the matrix cores from the storage type into fp32; the softmax and
  * its sums are fp32; the weights (and dS, backward) are rounded to the storage type before the
  * second product, and outputs once at the end. In f16 a dS past 65504 overflows there. Scores
- * of any finite size are weighed forward; the backward forms the weights again from lse, with a
- * relative error of |lse| 2^-22. Results do not depend on the order of execution: no atomics on
- * them.
+ * of any size, in any mixture, are weighed forward as their fp32 values differ, as long as fp32
+ * holds s_ij log2 e; the backward forms the weights again from lse, with a relative error of
+ * |lse| 2^-22. Results do not depend on the order of execution: no atomics on them.
  *
  * Layouts. Rows are [token][head][D], the heads of a token contiguous; every tensor has a
  * token stride in elements (0 = heads * D, else at least that: tokens do not overlap), so q, k
@@ -33,7 +33,7 @@
  * Ownership, threading and errors are those of rope_qk.h: the caller owns every buffer, the
  * library allocates nothing, keeps no state, never synchronizes, and only enqueues work on
  * `stream`; arguments are checked on the host before any HIP call (rope_status codes).
- * Inputs and outputs must not overlap, except where stated.
+ * An output must not overlap an input or another output, except where stated.
  */
 #ifndef ATTN_H
 #define ATTN_H
@@ -83,7 +83,9 @@ int32_t attn_fwd(const void* q, const void* k, const void* v, void* out, float* 
                  int64_t v_stride, int64_t out_stride, const int32_t* plan, int32_t num_seqs,
                  double scale, int32_t dtype, int32_t fill, void* stream);
 
-/* Floats of attn_bwd's scratch, or -1 for bad arguments. */
+/* Floats of attn_bwd's scratch, or -1 for bad arguments: 0.5 MB of partial sums for each of D
+ * columns, twice that for D up to 64 (67 MB at D = 64 and 128), whatever T is, and 8 bytes a row
+ * and query head. */
 int64_t attn_bwd_scratch_floats(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D);
 
 /* Its gradients, from dout and what attn_fwd read and wrote:
@@ -125,7 +127,7 @@ int32_t attn_bwd(const void* dout, const void* q, const void* k, const void* v, 
  *  D           even, 2 .. 512; dtype any rope_dtype; any strides and alignment (the widest
  *              access that they allow is used)
  *  theta, pos_scale  as in rope_qk_apply_ex
- * Two tokens of one call that share a cache row leave one of them there. */
+ * Two tokens of one call must not share a cache row: it would hold parts of either, in no order. */
 int32_t kv_append(const void* q, void* q_out, const void* k, const void* v, void* k_cache,
                   void* v_cache, int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int64_t q_stride,
                   int64_t q_out_stride, int64_t k_stride, int64_t v_stride, int32_t num_pages,
@@ -134,7 +136,10 @@ int32_t kv_append(const void* q, void* q_out, const void* k, const void* v, void
                   const int32_t* cu_seqlens, int32_t num_seqs, const int32_t* kv_lens, double theta,
                   double pos_scale, int32_t dtype, void* stream);
 
-/* int32 words of a paged plan and floats of attn_paged's workspace, or -1. */
+/* int32 words of a paged plan and floats of attn_paged's workspace, or -1. The workspace has room
+ * for the splits of any batch of these sizes: about 2048 of them over all key/value heads, of 32
+ * rows of D + 4 floats where T * Hq / Hkv is at most 32, else of 128 rows (D = 128, 8 heads: 35
+ * and 139 MB). */
 int64_t paged_plan_ints(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv);
 int64_t paged_workspace_floats(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D);
 

@@ -308,8 +308,8 @@ def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: 
     block_table[s, position // page_size] (int32 [B, max_pages]) of the caches [num_pages,
     page_size, Hkv, D]. Keys and queries are rotated as qk_apply_ex_ does at that position.
     Tokens at a negative position, of no sequence, behind the table or on a page number that
-    is no page are not appended. Returns the rotated q, in q_out (a new tensor if None; may be
-    q itself), or None without q."""
+    is no page are not appended. No two tokens of a call may share a cache row. Returns the
+    rotated q, in q_out (a new tensor if None; may be q itself), or None without q."""
     shape, dtype, dev = k.shape, k.dtype, k.device
     if len(shape) != 3 or v.shape != shape:
         raise ValueError("expected k and v [T, Hkv, D]")

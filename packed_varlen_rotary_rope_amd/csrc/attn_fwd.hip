@@ -7,7 +7,9 @@
 //
 // What bounds it: matrix and vector unit together (with 128-wide heads both are busy for more
 // than half of the cycles, with 64-wide ones the exponentials for two thirds), and in long
-// launches the power limit, which takes the clock from 1.9 to 1.6 GHz. Two workgroups of four
+// launches the power limit, which takes the clock from 1.9 to 1.6 GHz; with short samples also the
+// start and end of workgroups (22 samples of 32 to 4096 tokens: 11 blocks of keys a workgroup, and
+// 155 us where the blocks alone would take 124). Two workgroups of four
 // waves share a CU (64 KB of LDS each), so that one wave's softmax runs beside another's products.
 // Measured, bf16: a prompt of 16384 tokens, 32 + 8 heads of 128, 2.0 to 2.3 ms, about 1.05
 // PFLOP/s (a large library product reaches 1.35); eight samples of 256 to 2048 tokens of the

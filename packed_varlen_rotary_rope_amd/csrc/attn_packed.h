@@ -24,7 +24,9 @@ static_assert(sizeof(RowItem) == 16 && sizeof(KeyTile) == 32, "words");
 
 constexpr int32_t kRowBlock = 32;   // packed rows of a step of the dK/dV pass
 constexpr int32_t kTileUnits = 8;   // what a tile costs beside its blocks, in blocks
-constexpr int32_t kMinUnits = 12;   // of a workgroup's share
+// Of a workgroup's share, at least. Not swept: where most samples are short a tile is about as much
+// work, and most tiles are cut (61 samples of 1 to 301 tokens, 6 + 2 heads: 118 of 138).
+constexpr int32_t kMinUnits = 12;
 
 // Row blocks that see a key of the tile at key0 of a sequence of n tokens.
 __host__ __device__ inline int32_t blocks_of_tile(int32_t n, int32_t key0, int32_t G) {

@@ -20,8 +20,9 @@
 //
 // Measured, bf16, 32 + 8 heads of 128: 64 sequences of 512 to 16384 tokens, one new token each,
 // 204 us, 5.6 TB/s (a large copy moves 5.0; reading alone goes faster); one sequence of 4099
-// tokens 8 us, latency; four chunks of 1024 tokens over 8000 to 24000 keys 1.15 to 1.3 ms, 1.0
-// PFLOP/s. The join takes 4 to 8 us, the plan 20.
+// tokens 8.5 us, latency; four chunks of 1024 tokens over 8000 to 24000 keys 1.15 to 1.3 ms, 1.0
+// PFLOP/s. The join takes 4 to 8 us, also where no tile is split, the plan 20 to 25. Head sizes
+// above 128 (one workgroup on a CU, blocks of 32 keys) are tested, not measured.
 #include "attn_packed.h"
 #include "attn_plan.h"
 #include "attn_tile.h"

@@ -10,8 +10,8 @@
 // token: its first D/2 lanes evaluate the token's cos/sin once for all heads, into LDS,
 // while the loads of its first chunk pairs are in flight. Rows are moved as pairs of chunks
 // (VEC elements of either half row), V's without a rotation. Measured, bf16, 32 + 8 heads of
-// 128: 4001 tokens of each of four prompts 72 us, 5.5 TB/s, a large copy's rate; one token of each
-// of 64 sequences 5 us, latency.
+// 128: 4001 tokens of each of four prompts 72 us at best and 76 in the middle of many launches, 5.5
+// and 5.2 TB/s (a large copy moves 5.0); one token of each of 64 sequences 5 us, latency.
 #include "attn_common.h"
 #include "cr_sincos.h"
 
