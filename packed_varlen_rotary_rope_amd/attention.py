@@ -2,7 +2,7 @@
 and backward), the append of new keys and values to a paged cache (rotated on the way), and
 attention over that cache.
 
-Thin binding over the C ABI of ``include/attn.h`` (libattn.so, built by build_attn.py from
+Thin binding over the C ABI of ``include/attn.h`` and ``include/attn_ex.h`` (libattn.so, built by build_attn.py from
 ``csrc/attn_*.hip`` and ``csrc/kv_append.hip``), as the package's other entry points are: it checks
 tensor metadata and marshals pointers, sizes and the current HIP stream. There is no
 fallback: if the library is missing, importing this module raises. The public names are
@@ -47,7 +47,16 @@ def _load() -> ctypes.CDLL:
     lib.paged_plan.argtypes = [vp, i32, vp, i64, i32, i32, vp, i64, vp]
     lib.attn_paged.argtypes = ([vp] * 6 + [i64, i32, i32, i32, i64, i64, i32, i32] + [i64] * 3 +
                                [vp, i32, i64, vp, i32, dbl, i32, i32, vp])
-    for name in ("attn_plan", "attn_fwd", "attn_bwd", "kv_append", "paged_plan", "attn_paged"):
+    # attn_ex.h: prefixes behind the lengths, cap and slopes behind the scale
+    lib.attn_plan_ex.argtypes = [vp, i32, vp, vp, i64, i32, i32, vp, i64, vp]
+    lib.attn_fwd_ex.argtypes = lib.attn_fwd.argtypes[:16] + [dbl, vp] + lib.attn_fwd.argtypes[16:]
+    lib.attn_bwd_ex.argtypes = lib.attn_bwd.argtypes[:25] + [dbl, vp] + lib.attn_bwd.argtypes[25:]
+    lib.attn_bwd_ex_scratch_floats.argtypes = [i64, i32, i32, i32, i32, i32]
+    lib.attn_bwd_ex_scratch_floats.restype = i64
+    lib.paged_plan_ex.argtypes = [vp, i32, vp, vp, i64, i32, i32, vp, i64, vp]
+    lib.attn_paged_ex.argtypes = lib.attn_paged.argtypes[:23] + [dbl, vp] + lib.attn_paged.argtypes[23:]
+    for name in ("attn_plan", "attn_fwd", "attn_bwd", "kv_append", "paged_plan", "attn_paged",
+                 "attn_plan_ex", "attn_fwd_ex", "attn_bwd_ex", "paged_plan_ex", "attn_paged_ex"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -146,6 +155,21 @@ def _like(t, ref, shape, name: str):
     return t
 
 
+def _scores(softcap, slopes, Hq: int, device):
+    """The arguments that change the scores: the cap (0 for none) and a pointer to the slopes."""
+    cap = 0.0
+    if softcap is not None:
+        cap = float(softcap)
+        if not 0.0 < cap < float("inf"):
+            raise ValueError("softcap: expected a positive number, or None")
+    if slopes is not None:
+        if slopes.dtype != torch.float32 or slopes.device != device or not slopes.is_contiguous():
+            raise TypeError(f"slopes must be a contiguous float32 tensor on {device}")
+        if tuple(slopes.shape) != (Hq,):
+            raise ValueError("slopes must have one entry per query head")
+    return cap, _ptr(slopes)
+
+
 class AttnPlan:
     """The work items of a packed batch (see attn_plan): one per batch, for every layer."""
 
@@ -170,11 +194,13 @@ class AttnPlan:
             raise TypeError("q, k, v and the plan must be on one device")
 
 
-def attn_plan(cu_seqlens, T: int, num_q_heads: int, num_kv_heads: int, seqused=None, out=None) -> AttnPlan:
+def attn_plan(cu_seqlens, T: int, num_q_heads: int, num_kv_heads: int, seqused=None, out=None,
+              prefix_lens=None) -> AttnPlan:
     """The plan of a packed batch of T rows whose sequence s is the rows cu_seqlens[s] ..
     cu_seqlens[s+1] - 1 (int32[B+1] on the GPU; with `seqused`, int32[B], only the first
     seqused[s] of them): one small launch, no host synchronization. It serves every layer
-    of the batch, forward and backward.
+    of the batch, forward and backward. prefix_lens (int32[B]): every token of sequence s sees its
+    first prefix_lens[s] tokens, those behind itself among them.
     `out`: a plan of the same sizes to be written over (for a captured graph's replays)."""
     dev = cu_seqlens.device
     _gpu(dev)
@@ -183,6 +209,7 @@ def attn_plan(cu_seqlens, T: int, num_q_heads: int, num_kv_heads: int, seqused=N
     if num_seqs < 0:
         raise ValueError("cu_seqlens needs at least one entry")
     su = None if seqused is None else _index(seqused, "seqused", dev, num_seqs)
+    pre = None if prefix_lens is None else _index(prefix_lens, "prefix_lens", dev, num_seqs)
     T, Hq, Hkv = int(T), int(num_q_heads), int(num_kv_heads)
     words = _lib.attn_plan_ints(T, num_seqs, Hq, Hkv)
     if words < 0:
@@ -197,18 +224,20 @@ def attn_plan(cu_seqlens, T: int, num_q_heads: int, num_kv_heads: int, seqused=N
         raise ValueError("out: a plan of other sizes or of another device")
     else:
         torch.autograd.graph.increment_version(out.buffer)  # a backward that saved it shall know
-    _call(dev, _lib.attn_plan, "attn_plan", _ptr(cu), num_seqs, _ptr(su), T, Hq, Hkv,
+    _call(dev, _lib.attn_plan_ex, "attn_plan", _ptr(cu), num_seqs, _ptr(su), _ptr(pre), T, Hq, Hkv,
           _ptr(out.buffer), out.buffer.numel())
     return out
 
 
-def attn_fwd(q, k, v, plan: AttnPlan, scale=None, out=None, lse=None, zero_rest=None):
+def attn_fwd(q, k, v, plan: AttnPlan, scale=None, out=None, lse=None, zero_rest=None, softcap=None,
+             slopes=None):
     """Causal attention of the packed batch: q [T, Hq, D], k and v [T, Hkv, D] (bf16 or f16;
     views whose tokens hold their heads contiguously, e.g. parts of a fused projection), D a
     multiple of 8 up to 256, Hq a multiple of Hkv. scale: D ** -0.5 unless given. Returns
     (out [T, Hq, D], lse float32 [T, Hq]), in the given ones or in new ones. zero_rest: whether
     rows of no sequence are written as 0 (-inf in lse) or left as they are; by default new
-    outputs are written and given ones left."""
+    outputs are written and given ones left. softcap c: scores s become c * tanh(s / c); slopes
+    (float32[Hq]): slopes[h] * the distance of query and key is taken off them, behind the cap."""
     if not isinstance(plan, AttnPlan):
         raise TypeError("plan: expected what attn_plan returns")
     plan._match(q, k, v)
@@ -224,16 +253,18 @@ def attn_fwd(q, k, v, plan: AttnPlan, scale=None, out=None, lse=None, zero_rest=
     else:
         out_stride = _heads_last(_like(out, q, (T, Hq, D), "out"), "out")
         _statistic(lse, q, T, Hq)
-    _call(q.device, _lib.attn_fwd, "attn_fwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-          lse.data_ptr(), T, Hq, k.shape[1], D, *strides, out_stride, plan.buffer.data_ptr(),
-          plan.num_seqs, D ** -0.5 if scale is None else float(scale), _DTYPE_CODE[q.dtype], int(fill))
+    more = () if softcap is None and slopes is None else _scores(softcap, slopes, Hq, q.device)
+    _call(q.device, _lib.attn_fwd_ex if more else _lib.attn_fwd, "attn_fwd", q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), out.data_ptr(), lse.data_ptr(), T, Hq, k.shape[1], D, *strides, out_stride,
+          plan.buffer.data_ptr(), plan.num_seqs, D ** -0.5 if scale is None else float(scale), *more,
+          _DTYPE_CODE[q.dtype], int(fill))
     return out, lse
 
 
 def attn_bwd(dout, q, k, v, out, lse, plan: AttnPlan, scale=None, dq=None, dk=None, dv=None,
-             zero_rest=None):
+             zero_rest=None, softcap=None, slopes=None):
     """Gradients of attn_fwd for the upstream gradient dout [T, Hq, D], from its inputs and
-    outputs and the same scale; D up to 128. Deterministic (no atomics). Returns (dq, dk, dv), in
+    outputs and the same scale, softcap and slopes (which get none); D up to 128. Deterministic (no atomics). Returns (dq, dk, dv), in
     the given ones (all three, e.g. parts of one fused gradient) or in new ones. zero_rest as in
     attn_fwd."""
     if not isinstance(plan, AttnPlan):
@@ -256,12 +287,13 @@ def attn_bwd(dout, q, k, v, out, lse, plan: AttnPlan, scale=None, dq=None, dk=No
     else:
         strides += [_heads_last(_like(t, q, (T, h, D), name), name, 128)
                     for t, h, name in ((dq, Hq, "dq"), (dk, Hkv, "dk"), (dv, Hkv, "dv"))]
-    scratch = q.new_empty(_lib.attn_bwd_scratch_floats(T, plan.num_seqs, Hq, Hkv, D),
+    more = () if softcap is None and slopes is None else _scores(softcap, slopes, Hq, q.device)
+    scratch = q.new_empty(_lib.attn_bwd_ex_scratch_floats(T, plan.num_seqs, Hq, Hkv, D, slopes is not None),
                           dtype=torch.float32)
-    _call(q.device, _lib.attn_bwd, "attn_bwd", dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _call(q.device, _lib.attn_bwd_ex if more else _lib.attn_bwd, "attn_bwd", dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
           out.data_ptr(), lse.data_ptr(), scratch.data_ptr(), dq.data_ptr(), dk.data_ptr(),
           dv.data_ptr(), T, Hq, Hkv, D, *strides, plan.buffer.data_ptr(), plan.num_seqs,
-          D ** -0.5 if scale is None else float(scale), _DTYPE_CODE[q.dtype], int(fill))
+          D ** -0.5 if scale is None else float(scale), *more, _DTYPE_CODE[q.dtype], int(fill))
     return dq, dk, dv
 
 
@@ -363,12 +395,14 @@ class PagedPlan:
         self.buffer = buffer  # int32, on the GPU
 
 
-def paged_plan(cu_seqlens, kv_lens, T: int, num_q_heads: int, num_kv_heads: int, out=None) -> PagedPlan:
+def paged_plan(cu_seqlens, kv_lens, T: int, num_q_heads: int, num_kv_heads: int, out=None,
+               prefix_lens=None) -> PagedPlan:
     """The plan of one step over a paged cache: T new tokens, rows cu_seqlens[s] ..
     cu_seqlens[s+1] - 1 of sequence s (int32[B+1] on the GPU), which holds kv_lens[s] tokens
     with them (int32[B], read now). One small launch, no host synchronization; it serves every
-    layer of the step. `out`: a plan of the same sizes to be written over (for the next step,
-    or in a captured graph)."""
+    layer of the step. prefix_lens (int32[B]): every new token of sequence s sees the first
+    prefix_lens[s] of the tokens that it holds, those behind itself among them. `out`: a plan of the
+    same sizes to be written over (for the next step, or in a captured graph)."""
     dev = cu_seqlens.device
     _gpu(dev)
     cu = _index(cu_seqlens, "cu_seqlens", dev)
@@ -376,6 +410,7 @@ def paged_plan(cu_seqlens, kv_lens, T: int, num_q_heads: int, num_kv_heads: int,
     if num_seqs < 0:
         raise ValueError("cu_seqlens needs at least one entry")
     lens = _index(kv_lens, "kv_lens", dev, num_seqs)
+    pre = None if prefix_lens is None else _index(prefix_lens, "prefix_lens", dev, num_seqs)
     T, Hq, Hkv = int(T), int(num_q_heads), int(num_kv_heads)
     words = _lib.paged_plan_ints(T, num_seqs, Hq, Hkv)
     if words < 0:
@@ -388,19 +423,19 @@ def paged_plan(cu_seqlens, kv_lens, T: int, num_q_heads: int, num_kv_heads: int,
     elif (out.T, out.num_seqs, out.num_q_heads, out.num_kv_heads, out.buffer.device) != \
             (T, num_seqs, Hq, Hkv, dev):
         raise ValueError("out: a plan of other sizes or of another device")
-    _call(dev, _lib.paged_plan, "paged_plan", _ptr(cu), num_seqs, _ptr(lens), T, Hq, Hkv,
+    _call(dev, _lib.paged_plan_ex, "paged_plan", _ptr(cu), num_seqs, _ptr(lens), _ptr(pre), T, Hq, Hkv,
           _ptr(out.buffer), out.buffer.numel())
     return out
 
 
 def attn_paged(q, k_cache, v_cache, block_table, plan: PagedPlan, scale=None, out=None, lse=None,
-               zero_rest=None):
+               zero_rest=None, softcap=None, slopes=None):
     """Attention of the new tokens q [T, Hq, D] (bf16 or f16, D a multiple of 8 up to 256) over
     the paged caches [num_pages, page_size, Hkv, D] that hold their sequences (kv_append_),
     causal among themselves; block_table as there, plan from paged_plan. Keys behind the table
     or on a page number that is no page are seen by no query. Returns (out [T, Hq, D], lse
     float32 [T, Hq]), in the given ones or in new ones; a query that sees no key gets 0 (-inf in
-    lse). zero_rest, for rows of no sequence, as in attn_fwd."""
+    lse). zero_rest, for rows of no sequence, softcap and slopes as in attn_fwd."""
     if not isinstance(plan, PagedPlan):
         raise TypeError("plan: expected what paged_plan returns")
     q_stride = _heads_last(q, "q")
@@ -425,9 +460,10 @@ def attn_paged(q, k_cache, v_cache, block_table, plan: PagedPlan, scale=None, ou
         out_stride = _heads_last(_like(out, q, (T, Hq, D), "out"), "out")
         _statistic(lse, q, T, Hq)
     space = q.new_empty(_lib.paged_workspace_floats(T, plan.num_seqs, Hq, Hkv, D), dtype=torch.float32)
-    _call(q.device, _lib.attn_paged, "attn_paged", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    more = () if softcap is None and slopes is None else _scores(softcap, slopes, Hq, q.device)
+    _call(q.device, _lib.attn_paged_ex if more else _lib.attn_paged, "attn_paged", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           out.data_ptr(), lse.data_ptr(), space.data_ptr(), T, Hq, Hkv, D, q_stride, out_stride,
           num_pages, page_size, page_stride, slot_stride, head_stride, block_table.data_ptr(), per,
           table_stride, plan.buffer.data_ptr(), plan.num_seqs,
-          D ** -0.5 if scale is None else float(scale), _DTYPE_CODE[q.dtype], int(fill))
+          D ** -0.5 if scale is None else float(scale), *more, _DTYPE_CODE[q.dtype], int(fill))
     return out, lse

@@ -13,8 +13,11 @@ from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRCS = [os.path.join(PKG, "csrc", name) for name in
-        ("attn_plan.hip", "attn_fwd.hip", "attn_bwd.hip", "attn_paged.hip", "kv_append.hip")]
+# sources and their flags: the attention is compiled once for each form of its scores, the longest
+# compilations first
+SRCS = [(os.path.join(PKG, "csrc", name), [f"-DATTN_MODS={mods}"])
+        for name in ("attn_bwd.hip", "attn_paged.hip", "attn_fwd.hip") for mods in (3, 2, 1, 0)]
+SRCS += [(os.path.join(PKG, "csrc", name), []) for name in ("attn_plan.hip", "kv_append.hip")]
 LIB_PATH = os.path.join(PKG, "libattn.so")
 ARCH = "gfx950"
 
@@ -41,13 +44,14 @@ def build(extra_flags=(), out: str = LIB_PATH) -> str:
     import tempfile
     tmp = out + ".tmp"
     with tempfile.TemporaryDirectory() as d:
-        def compile_one(src):
-            obj = os.path.join(d, os.path.basename(src) + ".o")
-            subprocess.run([hipcc(), *HIPCC_FLAGS, *extra_flags, "-c", "-o", obj, src], check=True)
+        def compile_one(item):
+            number, (src, flags) = item
+            obj = os.path.join(d, f"{number}_{os.path.basename(src)}.o")
+            subprocess.run([hipcc(), *HIPCC_FLAGS, *flags, *extra_flags, "-c", "-o", obj, src], check=True)
             return obj
 
-        with ThreadPoolExecutor(4) as pool:
-            objs = list(pool.map(compile_one, SRCS))
+        with ThreadPoolExecutor(8) as pool:
+            objs = list(pool.map(compile_one, enumerate(SRCS)))
         subprocess.run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs,
                         "-L", PKG, "-l:librope_qk.so", "-Wl,-rpath,$ORIGIN"], check=True)
     os.replace(tmp, out)

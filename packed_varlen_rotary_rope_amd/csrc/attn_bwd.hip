@@ -26,10 +26,11 @@
 #include "attn_packed.h"
 #include "attn_tile.h"
 
-namespace attn {
-namespace {
+#ifndef ATTN_MODS  // what scores go through (attn_scores.h): this file is compiled once for each
+#define ATTN_MODS 0
+#endif
 
-constexpr int32_t kExactKeys = 256;  // tiles up to here form D_i from P and dP
+namespace attn {
 
 struct BwdParams {
   const void* dout;
@@ -40,6 +41,8 @@ struct BwdParams {
   const float* lse;
   float* lse2;   // scratch: lse * log2 e and
   float* delta;  // D_i, by key/value head and packed row: [Hkv][T * G]
+  float* slope;  // kBias, the same way: slope * log2 e and
+  int32_t* at;   // the token's position
   void* dq;
   void* dk;
   void* dv;
@@ -49,10 +52,19 @@ struct BwdParams {
   float* part;  // scratch: [2 shares][dK, dV][128][D], of tiles that are cut
   int64_t dout_stride, q_stride, k_stride, v_stride, out_stride, dq_stride, dk_stride, dv_stride;
   int32_t T, Hq, Hkv, G, D, num_seqs;
-  float scale, scale2;  // scale2: times log2 e
+  float scale, scale2;  // scale2: of what exp2 sees, times log2 e
   int32_t fill;
   Div31 by_hkv, by_g;
+  ScoreParams scores;
 };
+
+template <int MODS>
+int32_t launch_bwd(const BwdParams& p, const PackedSizes& z, int32_t dtype, hipStream_t s);
+
+namespace {
+
+constexpr int32_t kExactKeys = 256;  // tiles up to here form D_i from P and dP
+constexpr bool kHasCap = ATTN_MODS & kCap, kHasBias = ATTN_MODS & kBias;
 
 // Zeros to `n` rows of `heads` heads from head0.
 template <typename T>
@@ -84,7 +96,7 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   const uint32_t tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t chunks = p.D >> 3;
-  if (item.gap != 0) {
+  if (item.prefix == kGap) {
     if (p.fill) clear_rows(static_cast<T*>(p.dq), start, n, p.dq_stride, kvh * p.G, p.G, chunks);
     return;
   }
@@ -99,11 +111,14 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   const int32_t clamped = on ? row : row_end - 1;
   const int32_t token = div31(clamped, p.by_g);
   const int32_t head = kvh * p.G + (clamped - token * p.G);
-  const int32_t seen = token + 1;
-  const int32_t wave_end =
-      wave_row0 < row_end ? (int32_t)div31(min(wave_row0 + 32, row_end) - 1, p.by_g) + 1 : 0;
-  const int32_t wave_all = div31(min(wave_row0, row_end - 1), p.by_g) + 1;
-  const int32_t key_end = div31(row_end - 1, p.by_g) + 1;
+  const int32_t prefix = min(item.prefix, n);
+  auto seen_by = [&](int32_t packed) __attribute__((always_inline)) {  // keys that a row sees
+    return max((int32_t)div31(packed, p.by_g) + 1, prefix);
+  };
+  const int32_t seen = max(token + 1, prefix);
+  const int32_t wave_end = wave_row0 < row_end ? seen_by(min(wave_row0 + 32, row_end) - 1) : 0;
+  const int32_t wave_all = seen_by(min(wave_row0, row_end - 1));
+  const int32_t key_end = seen_by(row_end - 1);
 
   const int64_t at_row = (int64_t)(start + token);
   x8<T> qf[KS], df[KS];
@@ -124,6 +139,8 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   const int64_t at_stat = at_row * p.Hq + head;
   float lse2 = p.lse[at_stat] * (float)kLog2e;
   if (lse2 == -__builtin_inff()) lse2 = 0.0f;  // every score is -inf: all weights are 0
+  float slope = 0.0f;
+  if constexpr (kHasBias) slope = p.scores.slopes[head] * (float)kLog2e;
 
   f32x16 dq[DB];
   clear_unused_chunks<CPR>(lds, kStages * 2 * BN, chunks);
@@ -153,6 +170,7 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
 #pragma unroll
     for (int x = s * kPerStep; x < (s + 1) * kPerStep && x < kPieces; ++x) piece(b + kStages - 1, x);
   };
+  f32x16 bent;  // kCap: tanh of the scores at hand
   auto weights = [&](auto mode, const uint8_t* kt, int32_t key0, int c, f32x16& s, f32x16& dp)
                      __attribute__((always_inline)) {
 #pragma unroll
@@ -163,9 +181,19 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
       s = mfma(read_rows<T, CPR>(kt, 32 * c + (lane & 31), 2 * t + half), qf[t], s);
       dp = mfma(read_rows<T, CPR>(kt + kTileBytes, 32 * c + (lane & 31), 2 * t + half), df[t], dp);
     }
+    if constexpr (kHasCap) {
+      bend_scores(s, p.scores.bend);
+      bent = s;
+    }
+    const float d0 = distance(key0 + 32 * c + 4 * (int32_t)half, token);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2));
+      if constexpr (kHasBias) {
+        const float d = d0 + (float)(8 * (i / 4) + i % 4);
+        s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -(slope * __builtin_fabsf(d))) - lse2);
+      } else {
+        s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale2, -lse2));
+      }
       if constexpr (decltype(mode)::value != kWhole) {
         const int32_t key = key0 + 32 * c + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
         if (key >= seen) s[i] = dp[i] = 0.0f;
@@ -180,6 +208,7 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         s[i] = s[i] * (dp[i] - delta);
+        if constexpr (kHasCap) s[i] *= __builtin_fmaf(-bent[i], bent[i], 1.0f);
         if constexpr (decltype(mode)::value != kWhole) {  // also where D_i is not finite
           const int32_t key = key0 + 32 * c + 8 * (i / 4) + 4 * (int32_t)half + i % 4;
           if (key >= seen) s[i] = 0.0f;
@@ -241,6 +270,10 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
     const int64_t at = ((int64_t)kvh * p.T + start) * p.G + row;
     p.lse2[at] = lse2;
     p.delta[at] = delta;
+    if constexpr (kHasBias) {
+      p.slope[at] = slope;
+      p.at[at] = token;
+    }
   }
   // two loops, and a second walk where it is needed, as in the forward
   const int32_t all = wave_end > 0 ? wave_all / BN : 0;
@@ -315,15 +348,15 @@ __device__ inline int64_t end_of_tile(const BwdParams& p, const Place& w, int32_
   return tile + 1 < w.tiles ? p.key_tiles[tile + 1].first : w.units;
 }
 
-// lse and D of a row that is none: no weight.
-__device__ const float kNoRow[2] = {__builtin_inff(), 0.0f};
+// lse and D, slope and position of a row that is none: no weight.
+__device__ const float kNoRow[4] = {__builtin_inff(), 0.0f, 0.0f, 0.0f};
 
 template <typename T, int DB>
 __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(const BwdParams p) {
   constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BM = kRowBlock;
   constexpr int kTileBytes = BM * CPR * 16, kLoads = BM * CPR / 256;
   constexpr bool kPipelined = DB > 2;
-  constexpr int kStatBytes = 2 * BM * 4, kStage = 2 * kTileBytes + kStatBytes, kStages = 4;
+  constexpr int kStatBytes = (kHasBias ? 4 : 2) * BM * 4, kStage = 2 * kTileBytes + kStatBytes, kStages = 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage];
   __shared__ __attribute__((aligned(16))) uint8_t flags[16];
 
@@ -381,8 +414,10 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
     const int32_t key = wave_key0 + (lane & 31);
     const bool on = key < n;
     const int32_t at_key = on ? key : n - 1;
-    const int32_t first = at_key * p.G;  // the first row that sees this lane's key
-    const int32_t wave_all = wave_key0 < n ? min(wave_key0 + 31, n - 1) * p.G : rows;  // the wave's every key
+    const int32_t prefix = tile.prefix;
+    const int32_t first = first_row_of_key(at_key, prefix, p.G);  // that sees this lane's key
+    // and the wave's every key
+    const int32_t wave_all = wave_key0 < n ? first_row_of_key(min(wave_key0 + 31, n - 1), prefix, p.G) : rows;
 
     x8<T> kf[KS], vf[KS];
     load_row<T>(kf, static_cast<const T*>(p.k) + (int64_t)(start + at_key) * p.k_stride +
@@ -393,14 +428,17 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
 
     // this piece's row blocks: the tile's first kTileUnits are what it costs beside them
     const int32_t block0 = (int32_t)max(from - kTileUnits, (int64_t)0);
-    const int32_t blocks = min((int32_t)max(to - kTileUnits, (int64_t)0), blocks_of_tile(n, key0, p.G)) - block0;
-    const int32_t row_begin = key0 * p.G / BM * BM + block0 * BM;
+    const int32_t blocks = min((int32_t)max(to - kTileUnits, (int64_t)0), blocks_of_tile(n, key0, prefix, p.G)) - block0;
+    const int32_t row_begin = first_row_of_key(key0, prefix, p.G) / BM * BM + block0 * BM;
     auto first_row = [&](int32_t i) __attribute__((always_inline)) { return row_begin + i * BM; };
 
     const T* q = static_cast<const T*>(p.q) + (int64_t)start * p.q_stride + (int64_t)kvh * p.G * p.D;
     const T* g = static_cast<const T*>(p.dout) + (int64_t)start * p.dout_stride +
                  (int64_t)kvh * p.G * p.D;
     const float* stats = (half ? p.delta : p.lse2) + ((int64_t)kvh * p.T + start) * p.G;
+    const float* more_stats = stats;
+    if constexpr (kHasBias)
+      more_stats = (half ? reinterpret_cast<const float*>(p.at) : p.slope) + ((int64_t)kvh * p.T + start) * p.G;
     // the next block's rows of this thread: head of the group, and offsets
     uint32_t heads[kLoads];
     int64_t q_at[kLoads], g_at[kLoads];
@@ -428,8 +466,9 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
       }
     };
     // The x-th copy of block b; blocks are begun in order, each after a call of go_to. The first
-    // is of lse and D of the rows, 32 words each, by the first wave: it waits for one copy more
-    // than it would have to, the other waves for what they need.
+    // is of lse and D of the rows, 32 words each, by the first wave (and with a bias of slope and
+    // position by the second): it waits for one copy more than it would have to, the other waves for
+    // what they need.
     constexpr int kPieces = 2 * kLoads, kPerStep = (kPieces + KS - 1) / KS;
     auto go_to = [&](int32_t b) __attribute__((always_inline)) {
       if (b == 0 || first_row(b) + BM > rows) seek(first_row(b));  // also where the rows end
@@ -443,6 +482,10 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
         const int32_t row = first_row(b) + (int32_t)(lane & 31);
         copy_word_to_lds(row < rows ? stats + row : kNoRow + half, gd + kTileBytes);
       }
+      if (kHasBias && x == 0 && wave == 1) {
+        const int32_t row = first_row(b) + (int32_t)(lane & 31);
+        copy_word_to_lds(row < rows ? more_stats + row : kNoRow + 2 + half, gd + kTileBytes + 2 * BM * 4);
+      }
       if (x % 2 == 0) copy_chunk_to_lds(q + q_at[i], qd + dst, lanes[i]);
       else copy_chunk_to_lds(g + g_at[i], gd + dst, lanes[i]);
     };
@@ -455,8 +498,10 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
     // the next is waited for. (With all of P and dS beside the first half of the products the
     // pass of a packed batch took 339 us, and 318 so.) Up to 64 columns two waves share a SIMD, and a
     // block is finished before the next is begun.
-    f32x16 s, dp;             // of the block at hand, then of the next one
+    f32x16 s, dp;             // of the block at hand, then of the next one (kCap: tanh of the scores)
     f32x4 lse2[4], delta[4];  // of rows 8 j + 4 half .. + 3
+    f32x4 slope[4];           // kBias, and
+    i32x4 places[4];          // the position that this lane's key has to them
     float wx[2], dx[2];
     uint32_t w[8], ds[8];  // P and dS of row pairs, narrowed
     x8<T> qr[KS], gr[KS];  // rows of the next block, the first two steps' from the round before
@@ -465,6 +510,10 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
       const float* stat = reinterpret_cast<const float*>(qt + 2 * kTileBytes);
       lse2[j] = *reinterpret_cast<const f32x4*>(stat + 8 * j + 4 * half);
       delta[j] = *reinterpret_cast<const f32x4*>(stat + 32 + 8 * j + 4 * half);
+      if constexpr (kHasBias) {
+        slope[j] = *reinterpret_cast<const f32x4*>(stat + 64 + 8 * j + 4 * half);
+        places[j] = *reinterpret_cast<const i32x4*>(stat + 96 + 8 * j + 4 * half);
+      }
     };
     // The u-th of 32 operations from S and dP to P (even) and dS (odd), in order.
     auto weigh = [&](auto mode, int u, const f32x16& sv, const f32x16& dpv, int32_t row0)
@@ -474,10 +523,16 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
       const int32_t at = row0 + 8 * j + 4 * (int32_t)half + e;
       const bool gone = MODE != kWhole && (at < first || (MODE == kCareful && at >= rows));
       if (u % 2 == 0) {
-        wx[c] = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[i], p.scale2, -lse2[j][e]));
+        if constexpr (kHasBias) {
+          const float bias = -(slope[j][e] * __builtin_fabsf(distance(at_key, places[j][e])));
+          wx[c] = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[i], p.scale2, bias) - lse2[j][e]);
+        } else {
+          wx[c] = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[i], p.scale2, -lse2[j][e]));
+        }
         if (gone) wx[c] = 0.0f;
       } else {
         dx[c] = wx[c] * (dpv[i] - delta[j][e]);
+        if constexpr (kHasCap) dx[c] *= __builtin_fmaf(-sv[i], sv[i], 1.0f);
         if (gone) dx[c] = 0.0f;
         if (c == 1) {
           w[i / 2] = narrow2<T>(wx[0], wx[1]);
@@ -507,6 +562,7 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
         second_half(t);
       }
       step();
+      if constexpr (kHasCap) bend_scores(a, p.scores.bend);
       s_out = a;
       dp_out = c;
     };
@@ -752,14 +808,27 @@ int32_t launch_size(const BwdParams& p, const PackedSizes& z, hipStream_t s) {
 }
 
 }  // namespace
+
+template <>
+int32_t launch_bwd<ATTN_MODS>(const BwdParams& p, const PackedSizes& z, int32_t dtype, hipStream_t s) {
+  return dtype == ROPE_BF16 ? launch_size<__bf16>(p, z, s) : launch_size<_Float16>(p, z, s);
+}
+
 }  // namespace attn
+
+#if ATTN_MODS == 0
 
 using namespace attn;
 
 extern "C" int64_t attn_bwd_scratch_floats(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv,
                                            int32_t D) {
+  return attn_bwd_ex_scratch_floats(T, num_seqs, Hq, Hkv, D, 0);
+}
+
+extern "C" int64_t attn_bwd_ex_scratch_floats(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv,
+                                              int32_t D, int32_t biased) {
   if (!valid_batch(T, num_seqs, Hq, Hkv) || !valid_head_size(D) || D > 128) return -1;
-  return (int64_t)2 * key_shares(D) * 2 * kKeyTile * D + 2 * T * Hq;
+  return (int64_t)2 * key_shares(D) * 2 * kKeyTile * D + (biased ? 4 : 2) * T * Hq;
 }
 
 extern "C" int32_t attn_bwd(const void* dout, const void* q, const void* k, const void* v,
@@ -770,9 +839,22 @@ extern "C" int32_t attn_bwd(const void* dout, const void* q, const void* k, cons
                             int64_t dk_stride, int64_t dv_stride, const int32_t* plan,
                             int32_t num_seqs, double scale, int32_t dtype, int32_t fill,
                             void* stream) {
+  return attn_bwd_ex(dout, q, k, v, out, lse, scratch, dq, dk, dv, T, Hq, Hkv, D, dout_stride, q_stride,
+                     k_stride, v_stride, out_stride, dq_stride, dk_stride, dv_stride, plan, num_seqs,
+                     scale, 0.0, nullptr, dtype, fill, stream);
+}
+
+extern "C" int32_t attn_bwd_ex(const void* dout, const void* q, const void* k, const void* v,
+                               const void* out, const float* lse, float* scratch, void* dq, void* dk,
+                               void* dv, int64_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                               int64_t dout_stride, int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, int64_t out_stride, int64_t dq_stride,
+                               int64_t dk_stride, int64_t dv_stride, const int32_t* plan,
+                               int32_t num_seqs, double scale, double cap, const float* slopes,
+                               int32_t dtype, int32_t fill, void* stream) {
   if (!valid_dtype16(dtype)) return ROPE_EUNSUPPORTED;
   if (attn_plan_ints(T, num_seqs, Hq, Hkv) < 0 || !valid_head_size(D) || D > 128) return ROPE_EINVAL;
-  if (!valid_scale(scale)) return ROPE_EINVAL;
+  if (!valid_scale(scale) || !valid_cap(cap, scale)) return ROPE_EINVAL;
   BwdParams p;
   if (!token_stride(dout_stride, Hq, D, &p.dout_stride) ||
       !token_stride(q_stride, Hq, D, &p.q_stride) || !token_stride(k_stride, Hkv, D, &p.k_stride) ||
@@ -799,6 +881,8 @@ extern "C" int32_t attn_bwd(const void* dout, const void* q, const void* k, cons
   p.part = scratch;
   p.lse2 = scratch + (int64_t)2 * key_shares(D) * 2 * kKeyTile * D;
   p.delta = p.lse2 + T * Hq;
+  p.slope = p.delta + T * Hq;  // with slopes only, as is the next
+  p.at = reinterpret_cast<int32_t*>(p.slope + T * Hq);
   p.dq = dq;
   p.dk = dk;
   p.dv = dv;
@@ -811,10 +895,18 @@ extern "C" int32_t attn_bwd(const void* dout, const void* q, const void* k, cons
   p.D = D;
   p.num_seqs = num_seqs;
   p.scale = (float)scale;
-  p.scale2 = (float)(scale * kLog2e);
+  p.scale2 = score_scale(scale, cap);
+  p.scores = score_params(scale, cap, slopes);
   p.fill = fill;
   p.by_hkv = make_div31(Hkv);
   p.by_g = make_div31(p.G);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return dtype == ROPE_BF16 ? launch_size<__bf16>(p, z, s) : launch_size<_Float16>(p, z, s);
+  switch (score_mods(cap, slopes)) {
+    case 0: return launch_bwd<0>(p, z, dtype, s);
+    case kBias: return launch_bwd<kBias>(p, z, dtype, s);
+    case kCap: return launch_bwd<kCap>(p, z, dtype, s);
+    default: return launch_bwd<kBias | kCap>(p, z, dtype, s);
+  }
 }
+
+#endif

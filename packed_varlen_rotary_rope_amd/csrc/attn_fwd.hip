@@ -19,8 +19,11 @@
 #include "attn_packed.h"
 #include "attn_tile.h"
 
+#ifndef ATTN_MODS  // what scores go through (attn_scores.h): this file is compiled once for each
+#define ATTN_MODS 0
+#endif
+
 namespace attn {
-namespace {
 
 struct FwdParams {
   const void* q;
@@ -35,12 +38,18 @@ struct FwdParams {
   float scale;  // times log2 e
   int32_t fill;
   Div31 by_hkv, by_g;
+  ScoreParams scores;
 };
 
-template <typename T, int DB>
+template <int MODS>
+int32_t launch_fwd(const FwdParams& p, int64_t blocks, int32_t dtype, hipStream_t s);
+
+namespace {
+
+template <typename T, int DB, int MODS>
 __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const FwdParams p) {
   constexpr int BN = keys_per_block(DB);
-  using Tile = FwdTile<T, DB, BN>;
+  using Tile = FwdTile<T, DB, BN, MODS>;
   constexpr int CPR = Tile::CPR, kLoads = BN * CPR / 256;
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * Tile::kTileBytes];  // two blocks in flight
 
@@ -56,7 +65,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
   const uint32_t chunks = p.D >> 3;
   T* out = static_cast<T*>(p.out);
 
-  if (item.gap != 0) {  // rows of no sequence
+  if (item.prefix == kGap) {  // rows of no sequence
     if (!p.fill) return;
     const uint32_t per_token = p.G * chunks;
     for (uint32_t i = tid; i < n * per_token; i += 256) {
@@ -81,13 +90,18 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
   const int32_t clamped = on ? row : row_end - 1;
   const int32_t token = div31(clamped, p.by_g);
   const int32_t head = kvh * p.G + (clamped - token * p.G);
-  const int32_t seen = token + 1;
+  const int32_t prefix = min(item.prefix, n);
+  auto seen_by = [&](int32_t packed) __attribute__((always_inline)) {  // keys that a row sees
+    return max((int32_t)div31(packed, p.by_g) + 1, prefix);
+  };
+  const int32_t seen = max(token + 1, prefix);
   // keys that some row, and that every row, of the wave and of the tile sees
-  const int32_t wave_end = wave_row0 < row_end ? (int32_t)div31(min(wave_row0 + 32, row_end) - 1, p.by_g) + 1 : 0;
-  const int32_t wave_all = div31(min(wave_row0, row_end - 1), p.by_g) + 1;
-  const int32_t key_end = div31(row_end - 1, p.by_g) + 1;
+  const int32_t wave_end = wave_row0 < row_end ? seen_by(min(wave_row0 + 32, row_end) - 1) : 0;
+  const int32_t wave_all = seen_by(min(wave_row0, row_end - 1));
+  const int32_t key_end = seen_by(row_end - 1);
 
   Tile t;
+  t.set_scores(p.scores, head, token);
   load_row<T>(t.q, static_cast<const T*>(p.q) + (int64_t)(start + token) * p.q_stride +
                        (int64_t)head * p.D, half, chunks);
   clear_unused_chunks<CPR>(lds, 4 * BN, chunks);
@@ -159,7 +173,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_fwd_kernel(const Fw
 
 template <typename T, int DB>
 int32_t launch(const FwdParams& p, int64_t blocks, hipStream_t s) {
-  hipLaunchKernelGGL((attn_fwd_kernel<T, DB>), dim3((unsigned)blocks), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_fwd_kernel<T, DB, ATTN_MODS>), dim3((unsigned)blocks), dim3(256), 0, s, p);
   return launched();
 }
 
@@ -177,7 +191,15 @@ int32_t launch_size(const FwdParams& p, int64_t blocks, hipStream_t s) {
 }
 
 }  // namespace
+
+template <>
+int32_t launch_fwd<ATTN_MODS>(const FwdParams& p, int64_t blocks, int32_t dtype, hipStream_t s) {
+  return dtype == ROPE_BF16 ? launch_size<__bf16>(p, blocks, s) : launch_size<_Float16>(p, blocks, s);
+}
+
 }  // namespace attn
+
+#if ATTN_MODS == 0
 
 using namespace attn;
 
@@ -186,9 +208,18 @@ extern "C" int32_t attn_fwd(const void* q, const void* k, const void* v, void* o
                             int64_t k_stride, int64_t v_stride, int64_t out_stride,
                             const int32_t* plan, int32_t num_seqs, double scale, int32_t dtype,
                             int32_t fill, void* stream) {
+  return attn_fwd_ex(q, k, v, out, lse, T, Hq, Hkv, D, q_stride, k_stride, v_stride, out_stride, plan,
+                     num_seqs, scale, 0.0, nullptr, dtype, fill, stream);
+}
+
+extern "C" int32_t attn_fwd_ex(const void* q, const void* k, const void* v, void* out, float* lse,
+                               int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int64_t q_stride,
+                               int64_t k_stride, int64_t v_stride, int64_t out_stride,
+                               const int32_t* plan, int32_t num_seqs, double scale, double cap,
+                               const float* slopes, int32_t dtype, int32_t fill, void* stream) {
   if (!valid_dtype16(dtype)) return ROPE_EUNSUPPORTED;
   if (attn_plan_ints(T, num_seqs, Hq, Hkv) < 0 || !valid_head_size(D)) return ROPE_EINVAL;
-  if (!valid_scale(scale)) return ROPE_EINVAL;
+  if (!valid_scale(scale) || !valid_cap(cap, scale)) return ROPE_EINVAL;
   FwdParams p;
   if (!token_stride(q_stride, Hq, D, &p.q_stride) || !token_stride(k_stride, Hkv, D, &p.k_stride) ||
       !token_stride(v_stride, Hkv, D, &p.v_stride) ||
@@ -213,11 +244,18 @@ extern "C" int32_t attn_fwd(const void* q, const void* k, const void* v, void* o
   p.Hkv = Hkv;
   p.D = D;
   p.num_seqs = num_seqs;
-  p.scale = (float)(scale * kLog2e);
+  p.scale = score_scale(scale, cap);
+  p.scores = score_params(scale, cap, slopes);
   p.fill = fill;
   p.by_hkv = make_div31(Hkv);
   p.by_g = make_div31(p.G);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return dtype == ROPE_BF16 ? launch_size<__bf16>(p, blocks, s)
-                            : launch_size<_Float16>(p, blocks, s);
+  switch (score_mods(cap, slopes)) {
+    case 0: return launch_fwd<0>(p, blocks, dtype, s);
+    case kBias: return launch_fwd<kBias>(p, blocks, dtype, s);
+    case kCap: return launch_fwd<kCap>(p, blocks, dtype, s);
+    default: return launch_fwd<kBias | kCap>(p, blocks, dtype, s);
+  }
 }
+
+#endif

@@ -27,8 +27,11 @@
 #include "attn_plan.h"
 #include "attn_tile.h"
 
+#ifndef ATTN_MODS  // what scores go through (attn_scores.h): this file is compiled once for each
+#define ATTN_MODS 0
+#endif
+
 namespace attn {
-namespace {
 
 constexpr int kBuckets = 256;
 constexpr int kSplitKeys = 64;   // splits begin at multiples of this
@@ -45,6 +48,8 @@ struct Item {
   int32_t key0, key_end;
   int32_t seq;
   int32_t slot;    // of its partial result in units of 32 rows; < 0: the tile is not split
+  int32_t prefix;  // keys that every row at a position sees, of those held
+  int32_t unused[3];
 };
 struct Join {
   int32_t q0, row0, rows, slot, splits, units, unused0, unused1;
@@ -62,9 +67,14 @@ inline Sizes paged_sizes(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv) {
 
 // ---- plan ----------------------------------------------------------------------------------
 
+#if ATTN_MODS == 0
+
+namespace {
+
 struct PlanParams {
   const int32_t* cu;
   const int32_t* kv_lens;
+  const int32_t* prefix_lens;
   int32_t T, num_seqs, G, Hkv;
   int32_t* header;
   Item* items;
@@ -74,7 +84,7 @@ struct PlanParams {
 
 struct PlanShared {
   SeqChunk c;
-  int32_t held[kPlanThreads];
+  int32_t held[kPlanThreads], prefix[kPlanThreads];
   int32_t tiles[kPlanThreads];  // inclusive running count
   int32_t count[kBuckets];      // items per bucket, then their places
   unsigned long long total;
@@ -99,6 +109,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(const PlanPara
     for (int32_t s0 = 0; s0 <= p.num_seqs; s0 += kPlanThreads) {
       load_sequences(s.c, p.cu, p.num_seqs, p.T, s0, &carry);
       s.held[t] = s.c.n[t] > 0 ? p.kv_lens[s0 + t - 1] : 0;
+      s.prefix[t] = p.prefix_lens != nullptr && s.c.n[t] > 0 ? min(max(p.prefix_lens[s0 + t - 1], 0), max(s.held[t], 0)) : 0;
       s.tiles[t] = block_scan<AddOp>(ceil_div(s.c.n[t] * p.G, kRowTile) +
                                          ceil_div(s.c.end[t] - s.c.a[t] - s.c.n[t], kKeyTile),
                                      s.c.scan);
@@ -112,6 +123,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(const PlanPara
         item.q0 = s.c.a[lo];
         item.seq = s0 + lo - 1;
         item.slot = -1;
+        item.prefix = s.prefix[lo];
         int32_t blocks = 0, tile_rows = 0;
         if (j >= ceil_div(rows, kRowTile)) {  // rows of no sequence
           item.q0 += s.c.n[lo] + (j - ceil_div(rows, kRowTile)) * kKeyTile;
@@ -125,7 +137,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(const PlanPara
           item.before = (int32_t)max((int64_t)s.held[lo] - s.c.n[lo], (int64_t)INT32_MIN);
           item.key0 = 0;
           const int64_t last = (int64_t)item.before + (item.row0 + tile_rows - 1) / p.G;
-          item.key_end = last < 0 ? 0 : (int32_t)min(last + 1, (int64_t)kMostKeys);
+          item.key_end = last < 0 ? 0 : (int32_t)min(max(last + 1, (int64_t)item.prefix), (int64_t)kMostKeys);
           blocks = ceil_div(item.key_end, kSplitKeys);
         }
         if (pass == 0) {
@@ -181,6 +193,10 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(const PlanPara
   }
 }
 
+}  // namespace
+
+#endif
+
 // ---- attention -------------------------------------------------------------------------------
 
 struct PagedParams {
@@ -202,7 +218,15 @@ struct PagedParams {
   float scale;  // times log2 e
   int32_t fill;
   Div31 by_hkv, by_g, by_page;
+  ScoreParams scores;
 };
+
+template <int MODS>
+int32_t launch_paged(const PagedParams& p, const Sizes& sizes, int32_t dtype, hipStream_t s);
+template <typename T>
+int32_t launch_join(const PagedParams& p, const Sizes& sizes, hipStream_t s);
+
+namespace {
 
 // A wave's view of the cache: rows of key blocks of BN keys, by way of the block table.
 template <int BN, int CPR>
@@ -286,7 +310,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   // visible keys of a token, 0 for none; within this split
   auto seen_by = [&](int32_t tok) __attribute__((always_inline)) {
     const int64_t s = (int64_t)item.before + tok + 1;
-    return (int32_t)min(max(s, (int64_t)0), (int64_t)key_end);
+    return s <= 0 ? 0 : (int32_t)min(max(s, (int64_t)item.prefix), (int64_t)key_end);
   };
   const int32_t seen = seen_by(token);
   const int32_t wave_end =
@@ -304,13 +328,16 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
     const int32_t tok = div31(c, p.by_g);
     return (item.q0 + tok) * stride + (int64_t)(kvh * p.G + c - tok * p.G) * unit;
   };
+  const int32_t head = kvh * p.G + clamped - token * p.G;
+  const int32_t position = (int32_t)((uint32_t)item.before + token);  // rows before 0 see nothing
   const T* q_row = static_cast<const T*>(p.q) + row_at(p.q_stride, p.D, false);
   const int32_t keys = key_end - item.key0;
   clear_unused_chunks<CPR>(lds, 4 * BN, chunks);
   __syncthreads();  // a wave's copies may land in what another clears
 
   if (!small) {
-    FwdTile<T, DB, BN> t;
+    FwdTile<T, DB, BN, ATTN_MODS> t;
+    t.set_scores(p.scores, head, position);
     load_row<T>(t.q, q_row, half, chunks);
     const int32_t blocks = keys > 0 ? (keys + BN - 1) / BN : 0;
     const PagedKeys<BN, CPR> src{table, pages[wave], offsets[wave], key_end};
@@ -405,7 +432,8 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   // scores are formed its V is on the way, and while its V is used the next block's K.
   constexpr bool kOneBuffer = DB > 4;
   constexpr int kLoads = 32 * CPR / 64;
-  FwdTile<T, DB, 32> t;
+  FwdTile<T, DB, 32, ATTN_MODS> t;
+  t.set_scores(p.scores, head, position);
   float low = 0.0f;
   load_row<T>(t.q, q_row, half, chunks);
   {
@@ -554,6 +582,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
 
 // Joins the splits of a tile: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, each m_i with what
 // its rounding left.
+#if ATTN_MODS == 0
 template <typename T>
 __global__ __launch_bounds__(256) void paged_join_kernel(const PagedParams p) {
   const uint32_t index = div31(blockIdx.x, p.by_hkv);
@@ -614,16 +643,14 @@ __global__ __launch_bounds__(256) void paged_join_kernel(const PagedParams p) {
     if (e == 0) p.lse[(int64_t)(j.q0 + tok) * p.Hq + h] = log_sum_exp(m, l);
   }
 }
+#endif
 
 template <typename T, int DB>
 int32_t launch(const PagedParams& p, const Sizes& sizes, hipStream_t s) {
   hipLaunchKernelGGL((attn_paged_kernel<T, DB>), dim3((unsigned)(sizes.items * p.Hkv)), dim3(256), 0,
                      s, p);
   const int32_t st = launched();
-  if (st != ROPE_OK) return st;
-  hipLaunchKernelGGL((paged_join_kernel<T>), dim3((unsigned)(sizes.joins * p.Hkv), kRowTile / 32),
-                     dim3(256), 0, s, p);
-  return launched();
+  return st != ROPE_OK ? st : launch_join<T>(p, sizes, s);
 }
 
 template <typename T>
@@ -640,18 +667,38 @@ int32_t launch_size(const PagedParams& p, const Sizes& sizes, hipStream_t s) {
 }
 
 }  // namespace
+
+template <>
+int32_t launch_paged<ATTN_MODS>(const PagedParams& p, const Sizes& sizes, int32_t dtype, hipStream_t s) {
+  return dtype == ROPE_BF16 ? launch_size<__bf16>(p, sizes, s) : launch_size<_Float16>(p, sizes, s);
+}
+
+#if ATTN_MODS == 0
+template <typename T>
+int32_t launch_join(const PagedParams& p, const Sizes& sizes, hipStream_t s) {
+  hipLaunchKernelGGL((paged_join_kernel<T>), dim3((unsigned)(sizes.joins * p.Hkv), kRowTile / 32),
+                     dim3(256), 0, s, p);
+  return launched();
+}
+template int32_t launch_join<__bf16>(const PagedParams& p, const Sizes& sizes, hipStream_t s);
+template int32_t launch_join<_Float16>(const PagedParams& p, const Sizes& sizes, hipStream_t s);
+#endif
+
 }  // namespace attn
+
+#if ATTN_MODS == 0
 
 using namespace attn;
 
-static_assert(sizeof(Item) == 32 && sizeof(Join) == 32, "items are 8 words");
+constexpr int32_t kItemWords = 12, kJoinWords = 8;
+static_assert(sizeof(Item) == 4 * kItemWords && sizeof(Join) == 4 * kJoinWords, "words");
 
 extern "C" {
 
 int64_t paged_plan_ints(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv) {
   if (attn_plan_ints(T, num_seqs, Hq, Hkv) < 0) return -1;
   const Sizes z = paged_sizes(T, num_seqs, Hq, Hkv);
-  return kHeader + 8 * (z.items + z.joins);
+  return kHeader + kItemWords * z.items + kJoinWords * z.joins;
 }
 
 int64_t paged_workspace_floats(int64_t T, int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D) {
@@ -661,12 +708,19 @@ int64_t paged_workspace_floats(int64_t T, int32_t num_seqs, int32_t Hq, int32_t 
 
 int32_t paged_plan(const int32_t* cu_seqlens, int32_t num_seqs, const int32_t* kv_lens, int64_t T,
                    int32_t Hq, int32_t Hkv, int32_t* plan, int64_t plan_ints, void* stream) {
+  return paged_plan_ex(cu_seqlens, num_seqs, kv_lens, nullptr, T, Hq, Hkv, plan, plan_ints, stream);
+}
+
+int32_t paged_plan_ex(const int32_t* cu_seqlens, int32_t num_seqs, const int32_t* kv_lens,
+                      const int32_t* prefix_lens, int64_t T, int32_t Hq, int32_t Hkv, int32_t* plan,
+                      int64_t plan_ints, void* stream) {
   const int64_t need = paged_plan_ints(T, num_seqs, Hq, Hkv);
   if (need < 0 || plan_ints < need || !data_pointer(plan)) return ROPE_EINVAL;
   if (num_seqs > 0 && (cu_seqlens == nullptr || kv_lens == nullptr)) return ROPE_EINVAL;
   PlanParams p;
   p.cu = cu_seqlens;
   p.kv_lens = kv_lens;
+  p.prefix_lens = prefix_lens;
   p.T = (int32_t)T;
   p.num_seqs = num_seqs;
   p.G = Hq / Hkv;
@@ -686,9 +740,21 @@ int32_t attn_paged(const void* q, const void* k_cache, const void* v_cache, void
                    int64_t slot_stride, int64_t head_stride, const int32_t* block_table,
                    int32_t max_pages, int64_t table_stride, const int32_t* plan, int32_t num_seqs,
                    double scale, int32_t dtype, int32_t fill, void* stream) {
+  return attn_paged_ex(q, k_cache, v_cache, out, lse, workspace, T, Hq, Hkv, D, q_stride, out_stride,
+                       num_pages, page_size, page_stride, slot_stride, head_stride, block_table, max_pages,
+                       table_stride, plan, num_seqs, scale, 0.0, nullptr, dtype, fill, stream);
+}
+
+int32_t attn_paged_ex(const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
+                      float* workspace, int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int64_t q_stride,
+                      int64_t out_stride, int32_t num_pages, int32_t page_size, int64_t page_stride,
+                      int64_t slot_stride, int64_t head_stride, const int32_t* block_table,
+                      int32_t max_pages, int64_t table_stride, const int32_t* plan, int32_t num_seqs,
+                      double scale, double cap, const float* slopes, int32_t dtype, int32_t fill,
+                      void* stream) {
   if (!valid_dtype16(dtype)) return ROPE_EUNSUPPORTED;
   if (attn_plan_ints(T, num_seqs, Hq, Hkv) < 0 || !valid_head_size(D)) return ROPE_EINVAL;
-  if (!valid_scale(scale)) return ROPE_EINVAL;
+  if (!valid_scale(scale) || !valid_cap(cap, scale)) return ROPE_EINVAL;
   PagedParams p;
   if (!token_stride(q_stride, Hq, D, &p.q_stride) || !token_stride(out_stride, Hq, D, &p.out_stride))
     return ROPE_EINVAL;
@@ -729,13 +795,21 @@ int32_t attn_paged(const void* q, const void* k_cache, const void* v_cache, void
   p.num_pages = num_pages;
   p.page_size = page_size;
   p.max_pages = max_pages;
-  p.scale = (float)(scale * kLog2e);
+  p.scale = score_scale(scale, cap);
+  p.scores = score_params(scale, cap, slopes);
   p.fill = fill;
   p.by_hkv = make_div31(Hkv);
   p.by_g = make_div31(p.G);
   p.by_page = make_div31(page_size);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return dtype == ROPE_BF16 ? launch_size<__bf16>(p, z, s) : launch_size<_Float16>(p, z, s);
+  switch (score_mods(cap, slopes)) {
+    case 0: return launch_paged<0>(p, z, dtype, s);
+    case kBias: return launch_paged<kBias>(p, z, dtype, s);
+    case kCap: return launch_paged<kCap>(p, z, dtype, s);
+    default: return launch_paged<kBias | kCap>(p, z, dtype, s);
+  }
 }
 
 }  // extern "C"
+
+#endif

@@ -1,0 +1,72 @@
+// attn_scores.h -- what scores may go through before the softmax: a cap by a tanh, and a bias that
+// depends on the distance of query and key.
+//
+// Mathematics: s = scale q.k becomes c tanh(s / c), and then s - slope_h |i - j| with i and j the
+// positions of query and key. In base 2, with t = tanh(q.k bend), bend = scale / c, the score is
+// t (c log2 e) - (slope_h log2 e) |i - j|: a kernel's q.k is replaced by t, its scale by c log2 e,
+// and everything behind it stays as it is. The gradient gets a factor 1 - t^2, from the same t.
+#pragma once
+
+#include "attn_common.h"
+#include "tanh_constants.h"
+
+namespace attn {
+
+enum ScoreMods : int { kBias = 1, kCap = 2 };
+
+// What a kernel compiled with ATTN_MODS of them is given.
+struct ScoreParams {
+  const float* slopes;  // of each query head
+  float bend;           // scale / cap
+};
+
+// cap 0: none; else positive, with scale / cap and cap log2 e well within single precision.
+inline bool valid_cap(double cap, double scale) {
+  return cap == 0.0 || (cap > 0.0 && cap * kLog2e < 1e30 && scale / cap > 1e-30 && scale / cap < 1e30);
+}
+inline int score_mods(double cap, const float* slopes) {
+  return (cap != 0.0 ? kCap : 0) | (slopes != nullptr ? kBias : 0);
+}
+inline ScoreParams score_params(double scale, double cap, const float* slopes) {
+  return {slopes, cap != 0.0 ? (float)(scale / cap) : 0.0f};
+}
+inline float score_scale(double scale, double cap) {  // of what the softmax sees, in base 2
+  return (float)((cap != 0.0 ? cap : scale) * kLog2e);
+}
+
+// tanh(s by) of 16 scores, within 2^-22 of it relatively: a polynomial up to 1, which is all that most
+// blocks need, else 1 - 2 / (1 + exp(2 y)) too (8 operations of the full rate, against 4 and two
+// of a quarter of it). A score's result depends on no other's.
+__device__ inline void bend_scores(f32x16& s, float by) {
+  f32x16 y;
+  float most = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    y[i] = s[i] * by;
+    most = __builtin_fmaxf(most, __builtin_fabsf(y[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float z = y[i] * y[i];
+    float x = kTanhPoly[kTanhDegree];
+#pragma unroll
+    for (int k = kTanhDegree - 1; k >= 0; --k) x = __builtin_fmaf(x, z, kTanhPoly[k]);
+    s[i] = y[i] * x;
+  }
+  if (__any(most > 1.0f)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float a = __builtin_fabsf(y[i]);
+      const float e = __builtin_amdgcn_exp2f(a * (float)(2.0 * kLog2e));
+      const float t = __builtin_fmaf(__builtin_amdgcn_rcpf(1.0f + e), -2.0f, 1.0f);
+      s[i] = a > 1.0f ? __builtin_copysignf(t, y[i]) : s[i];
+    }
+  }
+}
+
+// key0 - pos as a number, where they are near enough for a key to be seen; no overflow elsewhere.
+__device__ inline float distance(int32_t key, int32_t pos) {
+  return (float)(int32_t)((uint32_t)key - (uint32_t)pos);
+}
+
+}  // namespace attn

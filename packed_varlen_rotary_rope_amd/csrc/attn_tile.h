@@ -14,7 +14,7 @@
 // reads.
 #pragma once
 
-#include "attn_common.h"
+#include "attn_scores.h"
 
 namespace attn {
 
@@ -85,8 +85,9 @@ __device__ inline void add_nonfinite_row(f32x16 (&o)[DB], const uint8_t* tile, u
     }
 }
 
-// The running state of 32 query rows of a wave, against blocks of BN keys.
-template <typename T, int DB, int BN>
+// The running state of 32 query rows of a wave, against blocks of BN keys. MODS: what scores go
+// through (attn_scores.h).
+template <typename T, int DB, int BN, int MODS = 0>
 struct FwdTile {
   static constexpr int CPR = chunks_per_row(DB);
   static constexpr int KB = BN / 32;
@@ -100,14 +101,29 @@ struct FwdTile {
 
   bool was_large;  // of the wave: some row's m was large, and has risen since
 
+  float bend;      // kCap
+  float slope;     // kBias: of this lane's row, times log2 e,
+  int32_t at;      // and its position
+
+  // Sets what MODS needs for this lane's row: a query head, and its position.
+  __device__ void set_scores(const ScoreParams& p, int32_t head, int32_t position) {
+    if constexpr (MODS & kCap) bend = p.bend;
+    if constexpr (MODS & kBias) {
+      slope = p.slopes[head] * (float)kLog2e;
+      asm volatile("" : "+v"(slope));  // waited for here, not in a loop (as in settle)
+      at = position;
+    }
+  }
+
   static __device__ bool is_large(float m) {
     return __builtin_fabsf(m) > kLargeScore && __builtin_fabsf(m) < __builtin_inff();
   }
   // Whether scores are so large that scale * s - m, with m rounded, may be far from 0 for the
   // largest of them, and its weight beyond the type's range: the walk is done again in kCareful
   // mode with `exact` set, every block of it. Any m counts that the row had: the sums of an earlier
-  // one may be infinite, which no later factor takes back.
-  __device__ bool large() const { return was_large || is_large(m); }
+  // one may be infinite, which no later factor takes back. With a bias the scores themselves are in
+  // base 2, m is one of them, and their difference is exact enough as it is.
+  __device__ bool large() const { return !(MODS & kBias) && (was_large || is_large(m)); }
 
   __device__ void clear() {
 #pragma unroll
@@ -152,6 +168,21 @@ struct FwdTile {
   __device__ void weights(f32x16 (&s)[KB], x8<T> (&p)[2 * KB], int32_t key0, int32_t seen,
                           uint64_t hidden, float scale, uint32_t lane) {
     const uint32_t half = lane >> 5;
+    if constexpr (MODS & kCap) {
+#pragma unroll
+      for (int b = 0; b < KB; ++b) bend_scores(s[b], bend);
+    }
+    if constexpr (MODS & kBias) {
+      const float d0 = distance(key0 + 4 * (int32_t)half, at);
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float d = d0 + (float)(32 * b + 8 * (i / 4) + i % 4);
+          s[b][i] = __builtin_fmaf(s[b][i], scale, -(slope * __builtin_fabsf(d)));
+        }
+      scale = 1.0f;
+    }
     if constexpr (MODE != kWhole) {
 #pragma unroll
       for (int b = 0; b < KB; ++b)

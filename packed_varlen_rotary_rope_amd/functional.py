@@ -219,43 +219,52 @@ def _rows_for_kernel(t: torch.Tensor) -> torch.Tensor:
     return t.clone(memory_format=torch.contiguous_format)
 
 
-def _plan_of(plan, cu_seqlens, seqused, T, Hq, Hkv):
+def _plan_of(plan, cu_seqlens, seqused, prefix_lens, T, Hq, Hkv):
     if plan is None:
         if cu_seqlens is None:
             raise ValueError("give a plan or cu_seqlens")
-        return _rope.attn_plan(cu_seqlens, T, Hq, Hkv, seqused=seqused)
-    if cu_seqlens is not None or seqused is not None:
-        raise ValueError("a plan holds the sequences: give it or cu_seqlens (and seqused), not both")
+        return _rope.attn_plan(cu_seqlens, T, Hq, Hkv, seqused=seqused, prefix_lens=prefix_lens)
+    if cu_seqlens is not None or seqused is not None or prefix_lens is not None:
+        raise ValueError("a plan holds the sequences: give it or cu_seqlens (and seqused, prefix_lens), "
+                         "not both")
     return plan
+
+
+def _constant(slopes):
+    if slopes is not None and slopes.requires_grad and torch.is_grad_enabled():
+        raise ValueError("slopes get no gradient: give them detached")
+    return slopes
 
 
 class _Attn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, plan, scale):
-        out, lse = _rope.attn_fwd(q, k, v, plan, scale)
+    def forward(ctx, q, k, v, plan, scale, softcap, slopes):
+        out, lse = _rope.attn_fwd(q, k, v, plan, scale, softcap=softcap, slopes=slopes)
         # the plan's buffer too: autograd notices where it has been written over since
-        ctx.save_for_backward(q, k, v, out, lse, plan.buffer)
-        ctx.plan, ctx.scale = plan, scale
+        ctx.save_for_backward(q, k, v, out, lse, plan.buffer, slopes)
+        ctx.plan, ctx.scale, ctx.softcap = plan, scale, softcap
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
-        q, k, v, out, lse, _ = ctx.saved_tensors
-        dq, dk, dv = _rope.attn_bwd(_rows_for_kernel(dout), q, k, v, out, lse, ctx.plan, ctx.scale)
-        return dq, dk, dv, None, None
+        q, k, v, out, lse, _, slopes = ctx.saved_tensors
+        dq, dk, dv = _rope.attn_bwd(_rows_for_kernel(dout), q, k, v, out, lse, ctx.plan, ctx.scale,
+                                    softcap=ctx.softcap, slopes=slopes)
+        return dq, dk, dv, None, None, None, None
 
 
 def attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan=None, cu_seqlens=None,
-         scale=None, seqused=None) -> torch.Tensor:
+         scale=None, seqused=None, prefix_lens=None, softcap=None, slopes=None) -> torch.Tensor:
     """Differentiable causal attention of a packed batch: q [T, Hq, D], k and v [T, Hkv, D]
     (bf16 or f16, views with contiguous heads, D a multiple of 8 up to 128, without gradients 256), by the sequences
     of `plan` (``attn_plan``, made once per batch for every layer) or of cu_seqlens (with
-    optional seqused; a plan is made here then). Rows of no sequence get 0, and so do their
-    gradients. Returns [T, Hq, D]."""
+    optional seqused and prefix_lens; a plan is made here then). Rows of no sequence get 0, and so
+    do their gradients. softcap and slopes as in ``attn_fwd``; they are constants. Returns
+    [T, Hq, D]."""
     _head_sizes(q.shape[-1], q, k, v)
-    plan = _plan_of(plan, cu_seqlens, seqused, q.shape[0], q.shape[1], k.shape[1])
-    return _Attn.apply(q, k, v, plan, None if scale is None else float(scale))
+    plan = _plan_of(plan, cu_seqlens, seqused, prefix_lens, q.shape[0], q.shape[1], k.shape[1])
+    return _Attn.apply(q, k, v, plan, None if scale is None else float(scale), softcap, _constant(slopes))
 
 
 def _head_sizes(D: int, *inputs) -> None:
@@ -272,34 +281,35 @@ def _qkv_heads(qkv: torch.Tensor, Hq: int, Hkv: int):
 
 class _AttnQKV(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, qkv, Hq, Hkv, plan, scale):
+    def forward(ctx, qkv, Hq, Hkv, plan, scale, softcap, slopes):
         q, k, v = _qkv_heads(qkv, Hq, Hkv)
-        out, lse = _rope.attn_fwd(q, k, v, plan, scale)
-        ctx.save_for_backward(qkv, out, lse, plan.buffer)
-        ctx.heads, ctx.plan, ctx.scale = (Hq, Hkv), plan, scale
+        out, lse = _rope.attn_fwd(q, k, v, plan, scale, softcap=softcap, slopes=slopes)
+        ctx.save_for_backward(qkv, out, lse, plan.buffer, slopes)
+        ctx.heads, ctx.plan, ctx.scale, ctx.softcap = (Hq, Hkv), plan, scale, softcap
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
-        qkv, out, lse, _ = ctx.saved_tensors
+        qkv, out, lse, _, slopes = ctx.saved_tensors
         q, k, v = _qkv_heads(qkv, *ctx.heads)
         grad = torch.empty_like(qkv, memory_format=torch.contiguous_format)
         dq, dk, dv = _qkv_heads(grad, *ctx.heads)
         _rope.attn_bwd(_rows_for_kernel(dout), q, k, v, out, lse, ctx.plan, ctx.scale, dq, dk, dv,
-                 zero_rest=True)
-        return grad, None, None, None, None
+                 zero_rest=True, softcap=ctx.softcap, slopes=slopes)
+        return grad, None, None, None, None, None, None
 
 
 def attn_qkv(qkv: torch.Tensor, num_q_heads: int, num_kv_heads: int, plan=None, cu_seqlens=None,
-             scale=None, seqused=None) -> torch.Tensor:
+             scale=None, seqused=None, prefix_lens=None, softcap=None, slopes=None) -> torch.Tensor:
     """attn() on the Q, K and V heads of a fused projection output, as ``rope_qkv`` takes and
     returns it; the gradient is one tensor of its shape, which rope_qkv's backward may rotate in
     place. Returns [T, Hq, D]."""
     Hq, Hkv = int(num_q_heads), int(num_kv_heads)
     _head_sizes(_qkv_split(qkv, Hq, Hkv)[0].shape[2], qkv)
-    plan = _plan_of(plan, cu_seqlens, seqused, qkv.shape[0], Hq, Hkv)
-    return _AttnQKV.apply(qkv, Hq, Hkv, plan, None if scale is None else float(scale))
+    plan = _plan_of(plan, cu_seqlens, seqused, prefix_lens, qkv.shape[0], Hq, Hkv)
+    return _AttnQKV.apply(qkv, Hq, Hkv, plan, None if scale is None else float(scale), softcap,
+                          _constant(slopes))
 
 
 class _Glu(torch.autograd.Function):
