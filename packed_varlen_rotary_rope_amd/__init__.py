@@ -435,11 +435,14 @@ def glu_bwd(kind: str, dh, e, g, de=None, dg=None, index_mode: int = INDEX_AUTO)
 # ---------------------------------------------------------------- attention
 
 _ATTENTION = ("AttnPlan", "attn_plan", "attn_fwd", "attn_bwd", "PagedPlan", "paged_plan",
-              "attn_paged", "kv_append_")
+              "attn_paged", "kv_append_", "AXES_LAYOUTS", "qk_apply_axes", "kv_append_slots_",
+              "PagePool", "page_pool", "PageStep", "page_step", "page_release_")
 
 if os.path.exists(os.path.join(os.path.dirname(LIB_PATH), "libattn.so")):
     from .attention import (  # noqa: E402
-        AttnPlan, PagedPlan, attn_bwd, attn_fwd, attn_paged, attn_plan, kv_append_, paged_plan,
+        AXES_LAYOUTS, AttnPlan, PagePool, PageStep, PagedPlan, attn_bwd, attn_fwd, attn_paged,
+        attn_plan, kv_append_, kv_append_slots_, page_pool, page_release_, page_step, paged_plan,
+        qk_apply_axes,
     )
     __all__ += _ATTENTION
 else:  # the rest of the package does without that library; its own names do not

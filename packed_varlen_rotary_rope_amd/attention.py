@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -55,8 +56,15 @@ def _load() -> ctypes.CDLL:
     lib.attn_bwd_ex_scratch_floats.restype = i64
     lib.paged_plan_ex.argtypes = [vp, i32, vp, vp, i64, i32, i32, vp, i64, vp]
     lib.attn_paged_ex.argtypes = lib.attn_paged.argtypes[:23] + [dbl, vp] + lib.attn_paged.argtypes[23:]
+    lib.rope_qk_apply_axes.argtypes = ([vp] * 4 + [i64, i32, i32, i32] + [i64] * 4 +
+                                       [vp, i64, vp, i32, i32, dbl, dbl, i32, i32, vp])
+    lib.kv_append_slots.argtypes = ([vp] * 6 + [i64, i32, i32, i32] + [i64] * 4 + [i32, i32] + [i64] * 3 +
+                                    [vp, vp, i64, vp, i32, i32, dbl, dbl, i32, vp])
+    lib.kv_page_step.argtypes = [vp, vp, i32, i64, i32, vp, i32, i64, vp, i32] + [vp] * 8
+    lib.kv_page_release.argtypes = [vp, vp, i32, i32, vp, i32, i64, vp, i32, vp, vp]
     for name in ("attn_plan", "attn_fwd", "attn_bwd", "kv_append", "paged_plan", "attn_paged",
-                 "attn_plan_ex", "attn_fwd_ex", "attn_bwd_ex", "paged_plan_ex", "attn_paged_ex"):
+                 "attn_plan_ex", "attn_fwd_ex", "attn_bwd_ex", "paged_plan_ex", "attn_paged_ex",
+                 "rope_qk_apply_axes", "kv_append_slots", "kv_page_step", "kv_page_release"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -330,18 +338,9 @@ def _table(block_table, num_seqs, device):
     return per, row if B > 1 else per
 
 
-def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: float, q=None,
-               q_out=None, pos_scale: float = 1.0):
-    """Append the new tokens' keys (rotated) and values to a paged cache, in place, and rotate
-    their queries, in one launch. k, v [T, Hkv, D] and q [T, Hq, D] (bf16, f16 or f32; views
-    whose tokens hold their heads contiguously) are the new tokens of B sequences, rows
-    cu_seqlens[s] .. cu_seqlens[s+1] - 1 (int32[B+1]) of sequence s, which holds kv_lens[s]
-    tokens with them (int32[B]): token i of n goes to position kv_lens[s] - n + i, in page
-    block_table[s, position // page_size] (int32 [B, max_pages]) of the caches [num_pages,
-    page_size, Hkv, D]. Keys and queries are rotated as qk_apply_ex_ does at that position.
-    Tokens at a negative position, of no sequence, behind the table or on a page number that
-    is no page are not appended. No two tokens of a call may share a cache row. Returns the
-    rotated q, in q_out (a new tensor if None; may be q itself), or None without q."""
+def _append_rows(k, v, k_cache, v_cache, q, q_out):
+    """What the appends check alike: (sizes and strides of the new tokens' rows, the cache's shape and
+    strides, q_out)."""
     shape, dtype, dev = k.shape, k.dtype, k.device
     if len(shape) != 3 or v.shape != shape:
         raise ValueError("expected k and v [T, Hkv, D]")
@@ -372,6 +371,23 @@ def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: 
             if n > 1 and step < extent:
                 raise ValueError("rows of the cache overlap (an expanded tensor cannot be written)")
             extent += (n - 1) * step
+    return (T, Hq, Hkv, D, q_stride, out_stride, k_stride, v_stride), cache, steps, q_out
+
+
+def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: float, q=None,
+               q_out=None, pos_scale: float = 1.0):
+    """Append the new tokens' keys (rotated) and values to a paged cache, in place, and rotate
+    their queries, in one launch. k, v [T, Hkv, D] and q [T, Hq, D] (bf16, f16 or f32; views
+    whose tokens hold their heads contiguously) are the new tokens of B sequences, rows
+    cu_seqlens[s] .. cu_seqlens[s+1] - 1 (int32[B+1]) of sequence s, which holds kv_lens[s]
+    tokens with them (int32[B]): token i of n goes to position kv_lens[s] - n + i, in page
+    block_table[s, position // page_size] (int32 [B, max_pages]) of the caches [num_pages,
+    page_size, Hkv, D]. Keys and queries are rotated as qk_apply_ex_ does at that position.
+    Tokens at a negative position, of no sequence, behind the table or on a page number that
+    is no page are not appended. No two tokens of a call may share a cache row. Returns the
+    rotated q, in q_out (a new tensor if None; may be q itself), or None without q."""
+    rows, cache, steps, q_out = _append_rows(k, v, k_cache, v_cache, q, q_out)
+    dev = k.device
     cu = _index(cu_seqlens, "cu_seqlens", dev)
     num_seqs = cu.numel() - 1
     if num_seqs < 0:
@@ -379,10 +395,9 @@ def kv_append_(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, theta: 
     lens = _index(kv_lens, "kv_lens", dev, num_seqs)
     per, table_stride = _table(block_table, num_seqs, dev)
     _call(dev, _lib.kv_append, "kv_append", _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
-          k_cache.data_ptr(), v_cache.data_ptr(), T, Hq, Hkv, D, q_stride, out_stride, k_stride,
-          v_stride, cache[0], cache[1], steps[0], steps[1], steps[2], block_table.data_ptr(), per,
-          table_stride, cu.data_ptr(), num_seqs, lens.data_ptr(), float(theta), float(pos_scale),
-          _DTYPE_CODE[dtype])
+          k_cache.data_ptr(), v_cache.data_ptr(), *rows, cache[0], cache[1], steps[0], steps[1], steps[2],
+          block_table.data_ptr(), per, table_stride, cu.data_ptr(), num_seqs, lens.data_ptr(), float(theta),
+          float(pos_scale), _DTYPE_CODE[k.dtype])
     return q_out
 
 
@@ -467,3 +482,179 @@ def attn_paged(q, k_cache, v_cache, block_table, plan: PagedPlan, scale=None, ou
           table_stride, plan.buffer.data_ptr(), plan.num_seqs,
           D ** -0.5 if scale is None else float(scale), *more, _DTYPE_CODE[q.dtype], int(fill))
     return out, lse
+
+
+# ---------------------------------------------------------------- positions with several axes
+
+AXES_LAYOUTS = {"sections": 0, "interleaved": 1, "separate": 2}
+
+
+def _axes(position_ids, sections, layout, T: int, D: int, device):
+    """The C arguments of positions with several axes."""
+    if position_ids.dtype != torch.int32 or position_ids.device != device:
+        raise TypeError(f"position_ids must be an int32 tensor on {device}")
+    if layout not in AXES_LAYOUTS:
+        raise ValueError(f"layout: expected one of {', '.join(AXES_LAYOUTS)}")
+    sections = (D // 2,) if sections is None else tuple(int(n) for n in sections)
+    axes = len(sections)
+    if not 1 <= axes <= 4 or min(sections) < 0 or sum(sections) != D // 2:
+        raise ValueError(f"sections: expected 1 to 4 numbers of frequencies, D / 2 = {D // 2} in all")
+    if layout == "interleaved" and any(n > 0 and axes * (n - 1) + a >= D // 2
+                                       for a, n in enumerate(sections) if a):
+        raise ValueError("sections: an axis does not find its turns among the frequencies")
+    if position_ids.dim() == 1 and axes == 1:
+        position_ids = position_ids[None]
+    if position_ids.dim() != 2 or tuple(position_ids.shape) != (axes, T):
+        raise ValueError(f"position_ids: expected [{axes}, {T}], an axis for each section")
+    row, step = position_ids.stride()
+    if (T > 1 and step != 1) or (axes > 1 and row < T):
+        raise ValueError("position_ids: an axis's positions must be contiguous and of its own")
+    return position_ids.data_ptr(), max(row, T), (ctypes.c_int32 * axes)(*sections), axes, AXES_LAYOUTS[layout]
+
+
+def qk_apply_axes(q, k, position_ids, sections, theta: float, direction: int = 1, layout: str = "sections",
+                  pos_scale: float = 1.0, q_out=None, k_out=None):
+    """Rotate q [T, Hq, D] and k [T, Hkv, D] (bf16, f16 or f32; views whose tokens hold their heads
+    contiguously) by positions with several axes (time, height, width), in one launch: int32
+    position_ids [axes, T], a section of the D / 2 frequencies for each axis. layout "sections":
+    consecutive ones of one ladder of frequencies; "interleaved": the axes in turn along that
+    ladder, the first also where the others have none left; "separate": each section with a ladder
+    of its own, theta^(-i/n). direction -1 is the transposed rotation, for gradients. A token with a
+    negative position on any axis is not rotated. Returns (q, k) rotated, in q_out and k_out (new
+    tensors if None; may be q and k themselves)."""
+    T, Hq, D = q.shape if q.dim() == 3 else (-1, -1, -1)
+    if T < 0 or k.dim() != 3 or k.shape[0] != T or k.shape[2] != D:
+        raise ValueError("expected q [T, Hq, D] and k [T, Hkv, D]")
+    if k.dtype != q.dtype or k.device != q.device:
+        raise TypeError("q and k must share one dtype and device")
+    Hkv = k.shape[1]
+    strides = []
+    outs = []
+    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        stride = _token_rows(t, name, _ANY)
+        if out is None:
+            out = t.new_empty(t.shape)
+        elif out is not t and _token_rows(_like(out, t, t.shape, name + "_out"), name + "_out", _ANY) != stride \
+                and out.data_ptr() == t.data_ptr():
+            raise ValueError(f"{name}_out: in place, but with another stride")
+        outs.append(out)
+        strides += [stride, _token_rows(out, name + "_out", _ANY)]
+    axes = _axes(position_ids, sections, layout, T, D, q.device)
+    _call(q.device, _lib.rope_qk_apply_axes, "rope_qk_apply_axes", q.data_ptr(), outs[0].data_ptr(),
+          k.data_ptr(), outs[1].data_ptr(), T, Hq, Hkv, D, *strides, *axes, float(theta), float(pos_scale),
+          _DTYPE_CODE[q.dtype], int(direction))
+    return outs[0], outs[1]
+
+
+def kv_append_slots_(k, v, k_cache, v_cache, slots, position_ids, theta: float, sections=None,
+                     layout: str = "sections", q=None, q_out=None, pos_scale: float = 1.0):
+    """kv_append_ by a slot map and given positions: token t's key (rotated) and value go to the cache
+    row slots[t] = page * page_size + slot in the page (int64[T], as page_step returns it; a number
+    that is no row, -1, leaves the token out). position_ids (int32 [T], or [axes, T] with sections
+    and layout as in qk_apply_axes) rotate the keys and queries; a token with a negative position is
+    written unrotated. No two tokens may name one row. Returns the rotated q, or None without q."""
+    rows, cache, steps, q_out = _append_rows(k, v, k_cache, v_cache, q, q_out)
+    T, _, _, D = rows[:4]
+    dev = k.device
+    if slots.dtype != torch.int64 or slots.device != dev or not slots.is_contiguous():
+        raise TypeError(f"slots must be a contiguous int64 tensor on {dev}")
+    if tuple(slots.shape) != (T,):
+        raise ValueError("slots must have one entry per token")
+    axes = _axes(position_ids, sections, layout, T, D, dev)
+    _call(dev, _lib.kv_append_slots, "kv_append_slots", _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), *rows, cache[0], cache[1], steps[0], steps[1], steps[2],
+          slots.data_ptr(), *axes, float(theta), float(pos_scale), _DTYPE_CODE[k.dtype])
+    return q_out
+
+
+# ---------------------------------------------------------------- pages
+
+class PagePool:
+    """The free pages of a cache: a ring of page numbers (int32[num_pages] on the GPU) and its state
+    (int32[2]: the first free page's place, and how many are free)."""
+
+    def __init__(self, ring, state):
+        dev = ring.device
+        _gpu(dev)
+        _index(ring, "ring", dev)
+        _index(state, "state", dev, 2)
+        if ring.dim() != 1 or not 1 <= ring.numel() <= 1 << 30:
+            raise ValueError("ring: expected 1 .. 2^30 page numbers")
+        self.ring, self.state = ring, state
+
+
+def page_pool(num_pages: int, device=None) -> PagePool:
+    """A pool of which all pages 0 .. num_pages - 1 are free."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return PagePool(torch.arange(num_pages, dtype=torch.int32, device=device),
+                    torch.tensor([0, num_pages], dtype=torch.int32, device=device))
+
+
+class PageStep(NamedTuple):
+    """What page_step returns; see there."""
+    cu_seqlens: torch.Tensor
+    kv_lens: torch.Tensor
+    held: torch.Tensor
+    positions: torch.Tensor
+    state: torch.Tensor
+    slots: torch.Tensor
+
+
+def page_step(pool: PagePool, block_table, held, new_lens, T: int, page_size: int, out=None) -> PageStep:
+    """Pages, slots and positions of one step over a paged cache, on the GPU: sequence s holds held[s]
+    tokens and gets new_lens[s] (int32[B]) of the step's T. The pages that they need are taken from
+    the pool in the order of the sequences and written behind those that block_table (int32 [B,
+    max_pages]) has, and what this step's calls take is returned: cu_seqlens (int32[B+1]), kv_lens
+    (int32[B]), positions (int32[T]) and slots (int64[T]) of the new tokens, -1 for rows of none.
+    held and pool stay as they are: take the step's `held` and `state` over for the next one
+    (``pool.state = step.state``; with fixed addresses, in a captured graph, by copy_). A sequence
+    is refused where it needs more pages than its row of the table has, where the pages asked for up
+    to it are more than are free, and where its tokens do not all lie in the T rows: its kv_lens is 0,
+    which leaves its tokens out of kv_append_ and attn_paged, its held what it was. `out`: a step
+    of the same sizes to be written over, other than the one whose `held` or `state` this reads."""
+    if not isinstance(pool, PagePool):
+        raise TypeError("pool: expected a PagePool")
+    dev = pool.ring.device
+    T, page_size, B = int(T), int(page_size), new_lens.numel()
+    _index(new_lens, "new_lens", dev)
+    _index(held, "held", dev, B)
+    _index(pool.state, "state", dev, 2)
+    per, table_stride = _table(block_table, B, dev)
+    if not 0 <= T <= 1 << 30 or not 1 <= page_size <= 1 << 30:
+        raise ValueError("T: expected 0 .. 2^30, page_size: 1 .. 2^30")
+    if B > 1 and per > table_stride:
+        raise ValueError("block_table: its rows overlap (an expanded tensor cannot be written)")
+    if out is None:
+        # one allocation; state at its front
+        state, cu, kv_lens, after, positions = torch.empty(
+            3 + 3 * B + T, dtype=torch.int32, device=dev).split_with_sizes((2, B + 1, B, B, T))
+        out = PageStep(cu, kv_lens, after, positions, state, torch.empty(T, dtype=torch.int64, device=dev))
+    elif not isinstance(out, PageStep):
+        raise TypeError("out: expected what page_step returns")
+    elif (out.held.numel(), out.positions.numel(), out.held.device) != (B, T, dev):
+        raise ValueError("out: a step of other sizes or of another device")
+    elif (B > 0 and out.held.data_ptr() == held.data_ptr()) or out.state.data_ptr() == pool.state.data_ptr():
+        raise ValueError("out: the step whose held or state is read cannot be written over")
+    _call(dev, _lib.kv_page_step, "kv_page_step", new_lens.data_ptr(), held.data_ptr(), B, T, page_size,
+          block_table.data_ptr(), per, table_stride, pool.ring.data_ptr(), pool.ring.numel(),
+          pool.state.data_ptr(), out.cu_seqlens.data_ptr(), out.kv_lens.data_ptr(), out.held.data_ptr(),
+          out.positions.data_ptr(), out.slots.data_ptr(), out.state.data_ptr())
+    return out
+
+
+def page_release_(pool: PagePool, block_table, held, gone, page_size: int) -> None:
+    """Give the pages of the sequences with gone[s] (bool[B]) back to the pool, in place: the first
+    ceil(held[s] / page_size) entries of their rows of block_table; their held becomes 0."""
+    if not isinstance(pool, PagePool):
+        raise TypeError("pool: expected a PagePool")
+    dev, B = pool.ring.device, held.numel()
+    _index(held, "held", dev)
+    _index(pool.state, "state", dev, 2)
+    if gone.dtype != torch.bool or gone.device != dev or not gone.is_contiguous():
+        raise TypeError(f"gone must be a contiguous bool tensor on {dev}")
+    if gone.numel() != B:
+        raise ValueError("gone must have one entry per sequence")
+    per, table_stride = _table(block_table, B, dev)
+    _call(dev, _lib.kv_page_release, "kv_page_release", held.data_ptr(), gone.data_ptr(), B, int(page_size),
+          block_table.data_ptr(), per, table_stride, pool.ring.data_ptr(), pool.ring.numel(),
+          pool.state.data_ptr())

@@ -1,6 +1,6 @@
-"""Build the HIP library libattn.so (packed and paged attention kernels and the cache
-append) for gfx950 with hipcc (in-tree). It links against librope_qk.so beside it, whose
-inverse frequencies the append uses; build that first (build.py).
+"""Build the HIP library libattn.so (packed and paged attention kernels, the cache append and its
+pages, the rotation with several axes) for gfx950 with hipcc (in-tree). It links against
+librope_qk.so beside it, whose inverse frequencies the rotations use; build that first (build.py).
 
 Usage: python packed_varlen_rotary_rope_amd/build_attn.py  (run as a script: importing the
 package itself needs the libraries)
@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 # compilations first
 SRCS = [(os.path.join(PKG, "csrc", name), [f"-DATTN_MODS={mods}"])
         for name in ("attn_bwd.hip", "attn_paged.hip", "attn_fwd.hip") for mods in (3, 2, 1, 0)]
-SRCS += [(os.path.join(PKG, "csrc", name), []) for name in ("attn_plan.hip", "kv_append.hip")]
+SRCS += [(os.path.join(PKG, "csrc", name), []) for name in
+         ("rope_axes.hip", "attn_plan.hip", "kv_append.hip", "kv_pages.hip")]
 LIB_PATH = os.path.join(PKG, "libattn.so")
 ARCH = "gfx950"
 

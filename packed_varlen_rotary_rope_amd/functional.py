@@ -10,6 +10,7 @@ torch.autograd (no arithmetic of its own).
     q, k = rope_qk(q, k, cu, theta, seqused=su,    # padded layout, launched over its
                    cu_valid=valid_prefix(cu, su), valid_tokens=n)  # n rotated tokens only
     q, k = rope_qk_table(q, k, cos_tab, sin_tab, cu_seqlens)  # cos/sin from tables
+    qkv = rope_qkv_axes(qkv, Hq, Hkv, ids, (16, 24, 24), theta)  # positions [3, T]: time, height, width
     o = attn_qkv(qkv, Hq, Hkv, plan)               # attention of a fused QKV output
     o = attn(q, k, v, plan)                        # plan = attn_plan(cu, T, Hq, Hkv), once a batch
     h = glu("swiglu", e, g)                        # h = silu(e) * g
@@ -206,6 +207,72 @@ def rope_qk_table(q: torch.Tensor, k: torch.Tensor, cos_tab: torch.Tensor, sin_t
     through unchanged, and so do their gradients."""
     return _RopeQKTable.apply(_own_storage(q), _own_storage(k), cos_tab, sin_tab, cu_seqlens,
                               seqused, position_ids, seq_offsets, bool(inplace_backward))
+
+
+def _token_major(t: torch.Tensor) -> torch.Tensor:
+    """t [T, H, D] itself where its tokens hold their heads contiguously, else a contiguous copy."""
+    T, H, D = t.shape
+    if t.stride(2) == 1 and t.stride(1) == D and t.stride(0) >= H * D:
+        return t
+    return t.contiguous()
+
+
+class _RopeQKAxes(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, position_ids, sections, theta, layout, pos_scale):
+        ctx.save_for_backward(position_ids)
+        ctx.args = sections, theta, layout, pos_scale
+        return _rope.qk_apply_axes(q, k, position_ids, sections, theta, 1, layout, pos_scale)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk):
+        (position_ids,) = ctx.saved_tensors
+        sections, theta, layout, pos_scale = ctx.args
+        dq, dk = _rope.qk_apply_axes(_token_major(dq), _token_major(dk), position_ids, sections, theta, -1,
+                                     layout, pos_scale)
+        return dq, dk, None, None, None, None, None
+
+
+def rope_qk_axes(q: torch.Tensor, k: torch.Tensor, position_ids: torch.Tensor, sections, theta: float,
+                 layout: str = "sections", pos_scale: float = 1.0):
+    """Differentiable rotation of q [T, Hq, D] and k [T, Hkv, D] by positions with several axes
+    (int32 [axes, T]; sections and layout as in ``qk_apply_axes``), into new tensors: one launch
+    forward, one backward, which leaves the incoming gradients as they are. Returns (q, k)."""
+    return _RopeQKAxes.apply(q, k, position_ids, tuple(sections), float(theta), layout, float(pos_scale))
+
+
+class _RopeQKVAxes(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, qkv, Hq, Hkv, position_ids, sections, theta, layout, pos_scale):
+        q, k = _qkv_split(qkv, Hq, Hkv)
+        _rope.qk_apply_axes(q, k, position_ids, sections, theta, 1, layout, pos_scale, q, k)
+        ctx.mark_dirty(qkv)
+        ctx.save_for_backward(position_ids)
+        ctx.heads, ctx.args = (Hq, Hkv), (sections, theta, layout, pos_scale)
+        return qkv
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        (position_ids,) = ctx.saved_tensors
+        sections, theta, layout, pos_scale = ctx.args
+        if not g.is_contiguous():
+            g = g.contiguous()
+        grad = torch.empty_like(g)
+        dq, dk, dv = _qkv_heads(g, *ctx.heads)
+        q, k, v = _qkv_heads(grad, *ctx.heads)
+        _rope.qk_apply_axes(dq, dk, position_ids, sections, theta, -1, layout, pos_scale, q, k)
+        v.copy_(dv)
+        return grad, None, None, None, None, None, None, None
+
+
+def rope_qkv_axes(qkv: torch.Tensor, num_q_heads: int, num_kv_heads: int, position_ids: torch.Tensor,
+                  sections, theta: float, layout: str = "sections", pos_scale: float = 1.0) -> torch.Tensor:
+    """rope_qk_axes() on the Q and K heads inside a fused QKV projection output, in place, as
+    ``rope_qkv`` does it; its gradient is one new tensor. Returns qkv."""
+    return _RopeQKVAxes.apply(qkv, int(num_q_heads), int(num_kv_heads), position_ids, tuple(sections),
+                              float(theta), layout, float(pos_scale))
 
 
 def _rows_for_kernel(t: torch.Tensor) -> torch.Tensor:
