@@ -487,29 +487,32 @@ def attn_paged(q, k_cache, v_cache, block_table, plan: PagedPlan, scale=None, ou
 # ---------------------------------------------------------------- positions with several axes
 
 AXES_LAYOUTS = {"sections": 0, "interleaved": 1, "separate": 2}
+_SECTIONS = [ctypes.c_int32 * n for n in range(5)]
 
 
 def _axes(position_ids, sections, layout, T: int, D: int, device):
     """The C arguments of positions with several axes."""
-    if position_ids.dtype != torch.int32 or position_ids.device != device:
-        raise TypeError(f"position_ids must be an int32 tensor on {device}")
+    half = D // 2
+    if sections is None:
+        sections = (half,)
+    axes = len(sections)
     if layout not in AXES_LAYOUTS:
         raise ValueError(f"layout: expected one of {', '.join(AXES_LAYOUTS)}")
-    sections = (D // 2,) if sections is None else tuple(int(n) for n in sections)
-    axes = len(sections)
-    if not 1 <= axes <= 4 or min(sections) < 0 or sum(sections) != D // 2:
-        raise ValueError(f"sections: expected 1 to 4 numbers of frequencies, D / 2 = {D // 2} in all")
-    if layout == "interleaved" and any(n > 0 and axes * (n - 1) + a >= D // 2
-                                       for a, n in enumerate(sections) if a):
-        raise ValueError("sections: an axis does not find its turns among the frequencies")
-    if position_ids.dim() == 1 and axes == 1:
-        position_ids = position_ids[None]
-    if position_ids.dim() != 2 or tuple(position_ids.shape) != (axes, T):
+    if not 1 <= axes <= 4 or min(sections) < 0 or sum(sections) != half:
+        raise ValueError(f"sections: expected 1 to 4 numbers of frequencies, D / 2 = {half} in all")
+    if layout == "interleaved":
+        for a in range(1, axes):
+            if sections[a] > 0 and axes * (sections[a] - 1) + a >= half:
+                raise ValueError("sections: an axis does not find its turns among the frequencies")
+    if position_ids.dtype != torch.int32 or position_ids.device != device:
+        raise TypeError(f"position_ids must be an int32 tensor on {device}")
+    shape, stride = position_ids.shape, position_ids.stride()
+    if shape != (axes, T) and (axes > 1 or shape != (T,)):
         raise ValueError(f"position_ids: expected [{axes}, {T}], an axis for each section")
-    row, step = position_ids.stride()
-    if (T > 1 and step != 1) or (axes > 1 and row < T):
+    row = stride[0] if axes > 1 else T
+    if (T > 1 and stride[-1] != 1) or row < T:
         raise ValueError("position_ids: an axis's positions must be contiguous and of its own")
-    return position_ids.data_ptr(), max(row, T), (ctypes.c_int32 * axes)(*sections), axes, AXES_LAYOUTS[layout]
+    return position_ids.data_ptr(), row, _SECTIONS[axes](*sections), axes, AXES_LAYOUTS[layout]
 
 
 def qk_apply_axes(q, k, position_ids, sections, theta: float, direction: int = 1, layout: str = "sections",
@@ -522,28 +525,36 @@ def qk_apply_axes(q, k, position_ids, sections, theta: float, direction: int = 1
     of its own, theta^(-i/n). direction -1 is the transposed rotation, for gradients. A token with a
     negative position on any axis is not rotated. Returns (q, k) rotated, in q_out and k_out (new
     tensors if None; may be q and k themselves)."""
-    T, Hq, D = q.shape if q.dim() == 3 else (-1, -1, -1)
-    if T < 0 or k.dim() != 3 or k.shape[0] != T or k.shape[2] != D:
+    shape, kshape, dtype, dev = q.shape, k.shape, q.dtype, q.device
+    if len(shape) != 3 or len(kshape) != 3 or kshape[0] != shape[0] or kshape[2] != shape[2]:
         raise ValueError("expected q [T, Hq, D] and k [T, Hkv, D]")
-    if k.dtype != q.dtype or k.device != q.device:
+    if k.dtype != dtype or k.device != dev:
         raise TypeError("q and k must share one dtype and device")
-    Hkv = k.shape[1]
-    strides = []
-    outs = []
-    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-        stride = _token_rows(t, name, _ANY)
-        if out is None:
-            out = t.new_empty(t.shape)
-        elif out is not t and _token_rows(_like(out, t, t.shape, name + "_out"), name + "_out", _ANY) != stride \
-                and out.data_ptr() == t.data_ptr():
-            raise ValueError(f"{name}_out: in place, but with another stride")
-        outs.append(out)
-        strides += [stride, _token_rows(out, name + "_out", _ANY)]
-    axes = _axes(position_ids, sections, layout, T, D, q.device)
-    _call(q.device, _lib.rope_qk_apply_axes, "rope_qk_apply_axes", q.data_ptr(), outs[0].data_ptr(),
-          k.data_ptr(), outs[1].data_ptr(), T, Hq, Hkv, D, *strides, *axes, float(theta), float(pos_scale),
-          _DTYPE_CODE[q.dtype], int(direction))
-    return outs[0], outs[1]
+    T, Hq, D = shape
+    q_stride, k_stride = _token_rows(q, "q", _ANY), _token_rows(k, "k", _ANY)
+    axes = _axes(position_ids, sections, layout, T, D, dev)
+    if q_out is None:
+        q_out, q_out_stride = torch.empty(shape, dtype=dtype, device=dev), 0
+    else:
+        q_out_stride = _out_rows(q_out, q, q_stride, "q_out")
+    if k_out is None:
+        k_out, k_out_stride = torch.empty(kshape, dtype=dtype, device=dev), 0
+    else:
+        k_out_stride = _out_rows(k_out, k, k_stride, "k_out")
+    _call(dev, _lib.rope_qk_apply_axes, "rope_qk_apply_axes", q.data_ptr(), q_out.data_ptr(), k.data_ptr(),
+          k_out.data_ptr(), T, Hq, kshape[1], D, q_stride, q_out_stride, k_stride, k_out_stride, *axes,
+          float(theta), float(pos_scale), _DTYPE_CODE[dtype], int(direction))
+    return q_out, k_out
+
+
+def _out_rows(out, t, stride: int, name: str) -> int:
+    """Token stride of the output for t."""
+    if out is t:
+        return stride
+    out_stride = _token_rows(_like(out, t, t.shape, name), name, _ANY)
+    if out.data_ptr() == t.data_ptr() and out_stride != stride:
+        raise ValueError(f"{name}: in place, but with another stride")
+    return out_stride
 
 
 def kv_append_slots_(k, v, k_cache, v_cache, slots, position_ids, theta: float, sections=None,
@@ -614,11 +625,12 @@ def page_step(pool: PagePool, block_table, held, new_lens, T: int, page_size: in
     of the same sizes to be written over, other than the one whose `held` or `state` this reads."""
     if not isinstance(pool, PagePool):
         raise TypeError("pool: expected a PagePool")
-    dev = pool.ring.device
+    ring, before = pool.ring, pool.state
+    dev = ring.device
     T, page_size, B = int(T), int(page_size), new_lens.numel()
     _index(new_lens, "new_lens", dev)
     _index(held, "held", dev, B)
-    _index(pool.state, "state", dev, 2)
+    _index(before, "state", dev, 2)
     per, table_stride = _table(block_table, B, dev)
     if not 0 <= T <= 1 << 30 or not 1 <= page_size <= 1 << 30:
         raise ValueError("T: expected 0 .. 2^30, page_size: 1 .. 2^30")
@@ -633,12 +645,12 @@ def page_step(pool: PagePool, block_table, held, new_lens, T: int, page_size: in
         raise TypeError("out: expected what page_step returns")
     elif (out.held.numel(), out.positions.numel(), out.held.device) != (B, T, dev):
         raise ValueError("out: a step of other sizes or of another device")
-    elif (B > 0 and out.held.data_ptr() == held.data_ptr()) or out.state.data_ptr() == pool.state.data_ptr():
+    elif (B > 0 and out.held.data_ptr() == held.data_ptr()) or out.state.data_ptr() == before.data_ptr():
         raise ValueError("out: the step whose held or state is read cannot be written over")
     _call(dev, _lib.kv_page_step, "kv_page_step", new_lens.data_ptr(), held.data_ptr(), B, T, page_size,
-          block_table.data_ptr(), per, table_stride, pool.ring.data_ptr(), pool.ring.numel(),
-          pool.state.data_ptr(), out.cu_seqlens.data_ptr(), out.kv_lens.data_ptr(), out.held.data_ptr(),
-          out.positions.data_ptr(), out.slots.data_ptr(), out.state.data_ptr())
+          block_table.data_ptr(), per, table_stride, ring.data_ptr(), ring.numel(), before.data_ptr(),
+          out.cu_seqlens.data_ptr(), out.kv_lens.data_ptr(), out.held.data_ptr(), out.positions.data_ptr(),
+          out.slots.data_ptr(), out.state.data_ptr())
     return out
 
 

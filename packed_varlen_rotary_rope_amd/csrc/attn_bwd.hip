@@ -78,7 +78,7 @@ __device__ inline void clear_rows(T* x, int32_t start, int32_t n, int64_t stride
   }
 }
 
-template <typename T, int DB>
+template <typename T, int DB, int MODS>
 __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p) {
   constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BN = DB <= 2 ? 64 : 32;
   constexpr int kTileBytes = BN * CPR * 16, kLoads = BN * CPR / 256;
@@ -351,7 +351,7 @@ __device__ inline int64_t end_of_tile(const BwdParams& p, const Place& w, int32_
 // lse and D, slope and position of a row that is none: no weight.
 __device__ const float kNoRow[4] = {__builtin_inff(), 0.0f, 0.0f, 0.0f};
 
-template <typename T, int DB>
+template <typename T, int DB, int MODS>
 __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(const BwdParams p) {
   constexpr int CPR = chunks_per_row(DB), KS = 2 * DB, BM = kRowBlock;
   constexpr int kTileBytes = BM * CPR * 16, kLoads = BM * CPR / 256;
@@ -575,7 +575,7 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
       if constexpr (!kPipelined) {
         wait_copies_and_sync<(kStages - 2) * kPieces>();  // block b; the buffer before it is free
 #pragma unroll
-        for (int j = 0; j < 4; ++j) read_stats(qt, j);
+        for (int j = 0; j < (kHasBias ? 1 : 4); ++j) read_stats(qt, j);
         read_row(qt, 0);
         read_row(qt, 1);
       }
@@ -623,7 +623,13 @@ __global__ __launch_bounds__(256, DB <= 2 ? 2 : 1) void attn_bwd_keys_kernel(con
         read(0);
         read(1);
 #pragma unroll
-        for (int u = 0; u < 32; ++u) weigh(mode, u, s, dp, row0);
+        for (int u = 0; u < 32; ++u) {
+          if (kHasBias && u % 8 == 0) {  // the four kinds of a row's would not all find registers
+            step();
+            if (u < 24) read_stats(qt, u / 8 + 1);
+          }
+          weigh(mode, u, s, dp, row0);
+        }
       }
       x8<T> wb, db;
 #pragma unroll
@@ -785,12 +791,12 @@ inline int32_t key_shares(int32_t D) { return D <= 64 ? 512 : 256; }
 
 template <typename T, int DB>
 int32_t launch(const BwdParams& p, const PackedSizes& z, hipStream_t s) {
-  hipLaunchKernelGGL((attn_bwd_rows_kernel<T, DB>), dim3((unsigned)(z.rows * p.Hkv)), dim3(256), 0, s,
+  hipLaunchKernelGGL((attn_bwd_rows_kernel<T, DB, ATTN_MODS>), dim3((unsigned)(z.rows * p.Hkv)), dim3(256), 0, s,
                      p);
   int32_t st = launched();
   if (st != ROPE_OK) return st;
   const unsigned shares = key_shares(p.D);
-  hipLaunchKernelGGL((attn_bwd_keys_kernel<T, DB>), dim3(shares), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_bwd_keys_kernel<T, DB, ATTN_MODS>), dim3(shares), dim3(256), 0, s, p);
   st = launched();
   if (st != ROPE_OK) return st;
   hipLaunchKernelGGL((attn_bwd_join_kernel<T>), dim3(shares, kKeyTile / 32), dim3(256), 0, s, p);

@@ -259,7 +259,7 @@ struct PagedKeys {
 // This wave's reads of LDS are done: what they read may be overwritten.
 __device__ inline void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
 
-template <typename T, int DB>
+template <typename T, int DB, int MODS>
 __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const PagedParams p) {
   constexpr int CPR = chunks_per_row(DB), BN = keys_per_block(DB);
   constexpr int kTileBytes = BN * CPR * 16, kSmallTile = 32 * CPR * 16;
@@ -336,7 +336,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   __syncthreads();  // a wave's copies may land in what another clears
 
   if (!small) {
-    FwdTile<T, DB, BN, ATTN_MODS> t;
+    FwdTile<T, DB, BN, MODS> t;
     t.set_scores(p.scores, head, position);
     load_row<T>(t.q, q_row, half, chunks);
     const int32_t blocks = keys > 0 ? (keys + BN - 1) / BN : 0;
@@ -432,7 +432,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attn_paged_kernel(const 
   // scores are formed its V is on the way, and while its V is used the next block's K.
   constexpr bool kOneBuffer = DB > 4;
   constexpr int kLoads = 32 * CPR / 64;
-  FwdTile<T, DB, 32, ATTN_MODS> t;
+  FwdTile<T, DB, 32, MODS> t;
   t.set_scores(p.scores, head, position);
   float low = 0.0f;
   load_row<T>(t.q, q_row, half, chunks);
@@ -647,7 +647,7 @@ __global__ __launch_bounds__(256) void paged_join_kernel(const PagedParams p) {
 
 template <typename T, int DB>
 int32_t launch(const PagedParams& p, const Sizes& sizes, hipStream_t s) {
-  hipLaunchKernelGGL((attn_paged_kernel<T, DB>), dim3((unsigned)(sizes.items * p.Hkv)), dim3(256), 0,
+  hipLaunchKernelGGL((attn_paged_kernel<T, DB, ATTN_MODS>), dim3((unsigned)(sizes.items * p.Hkv)), dim3(256), 0,
                      s, p);
   const int32_t st = launched();
   return st != ROPE_OK ? st : launch_join<T>(p, sizes, s);

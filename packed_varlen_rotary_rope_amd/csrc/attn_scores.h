@@ -34,9 +34,18 @@ inline float score_scale(double scale, double cap) {  // of what the softmax see
   return (float)((cap != 0.0 ? cap : scale) * kLog2e);
 }
 
-// tanh(s by) of 16 scores, within 2^-22 of it relatively: a polynomial up to 1, which is all that most
-// blocks need, else 1 - 2 / (1 + exp(2 y)) too (8 operations of the full rate, against 4 and two
-// of a quarter of it). A score's result depends on no other's.
+// tanh(y) for |y| up to kTanhNear.
+__device__ inline float tanh_near(float y) {
+  const float z = y * y;
+  float x = kTanhPoly[kTanhDegree];
+#pragma unroll
+  for (int k = kTanhDegree - 1; k >= 0; --k) x = __builtin_fmaf(x, z, kTanhPoly[k]);
+  return y * x;
+}
+
+// tanh(s by) of 16 scores, within 2^-22 of it relatively: a polynomial up to kTanhNear, which is all
+// that most blocks need, else 1 - 2 / (1 + exp(2 y)) too (8 operations of the full rate, against 4 and
+// two of a quarter of it, and exact near 0). A score's result depends on no other's.
 __device__ inline void bend_scores(f32x16& s, float by) {
   f32x16 y;
   float most = 0.0f;
@@ -46,20 +55,14 @@ __device__ inline void bend_scores(f32x16& s, float by) {
     most = __builtin_fmaxf(most, __builtin_fabsf(y[i]));
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float z = y[i] * y[i];
-    float x = kTanhPoly[kTanhDegree];
-#pragma unroll
-    for (int k = kTanhDegree - 1; k >= 0; --k) x = __builtin_fmaf(x, z, kTanhPoly[k]);
-    s[i] = y[i] * x;
-  }
-  if (__any(most > 1.0f)) {
+  for (int i = 0; i < 16; ++i) s[i] = tanh_near(y[i]);
+  if (__any(most > kTanhNear)) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float a = __builtin_fabsf(y[i]);
       const float e = __builtin_amdgcn_exp2f(a * (float)(2.0 * kLog2e));
       const float t = __builtin_fmaf(__builtin_amdgcn_rcpf(1.0f + e), -2.0f, 1.0f);
-      s[i] = a > 1.0f ? __builtin_copysignf(t, y[i]) : s[i];
+      s[i] = a > kTanhNear ? __builtin_copysignf(t, y[i]) : s[i];
     }
   }
 }

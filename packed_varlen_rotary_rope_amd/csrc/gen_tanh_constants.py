@@ -1,10 +1,10 @@
 """Generate tanh_constants.h: the fp32 polynomial with which the attention kernels cap scores,
 each coefficient rounded once from a 60-digit mpmath value.
 
-For |y| <= 1, tanh(y) = y P(y^2) with P a Chebyshev fit of degree DEGREE on [0, 1]
+For |y| <= NEAR, tanh(y) = y P(y^2) with P a Chebyshev fit of degree DEGREE on [0, NEAR^2]
 (mpmath.chebyfit). Its error with fp32 coefficients, evaluated by Horner's rule in fp32 as
-the kernels do, is checked below MOST relative before the header is written; above 1 the
-kernels take 1 - 2 / (1 + exp(2 |y|)), which loses less than a bit there.
+the kernels do, is checked below MOST relative before the header is written; above NEAR the
+kernels take 1 - 2 / (1 + exp(2 |y|)), which loses about a bit there.
 
 Usage: python -m packed_varlen_rotary_rope_amd.csrc.gen_tanh_constants [--check]
 (--check: exit 1 if the committed header differs from a fresh generation).
@@ -19,7 +19,8 @@ import numpy as np
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 OUT = os.path.join(HERE, "tanh_constants.h")
-DEGREE = 7
+DEGREE = 5
+NEAR = mp.mpf("0.8")
 MOST = 2.0 ** -22
 mp.mp.dps = 60
 
@@ -31,7 +32,7 @@ def ratio(z):
 
 
 def coefficients():
-    return [np.float32(str(c)) for c in mp.chebyfit(ratio, [0, 1], DEGREE + 1)][::-1]
+    return [np.float32(str(c)) for c in mp.chebyfit(ratio, [0, NEAR ** 2], DEGREE + 1)][::-1]
 
 
 def evaluate(c, y):
@@ -46,7 +47,8 @@ def evaluate(c, y):
 
 def worst(c):
     out = 0.0
-    for y in np.concatenate([np.linspace(2.0 ** -20, 1, 4001), 2.0 ** np.linspace(-100, 0, 501)]):
+    near = float(NEAR)
+    for y in np.concatenate([np.linspace(2.0 ** -20, near, 4001), near * 2.0 ** np.linspace(-100, 0, 501)]):
         exact = mp.tanh(mp.mpf(float(np.float32(y))))
         out = max(out, float(abs(mp.mpf(float(evaluate(c, y))) / exact - 1)))
     return out
@@ -58,8 +60,9 @@ def text():
     if not error < MOST:
         raise SystemExit(f"the fit is off by {error:.3g}")
     lines = ["// Generated by gen_tanh_constants.py -- do not edit. tanh(y) = y sum_i kTanhPoly[i] y^(2 i)",
-             f"// for |y| <= 1, relative error {error:.1e} as evaluated in fp32.", "#pragma once", "",
-             "namespace attn {", "", f"constexpr int kTanhDegree = {DEGREE};",
+             f"// for |y| <= kTanhNear, relative error {error:.1e} as evaluated in fp32.", "#pragma once", "",
+             "namespace attn {", "", f"constexpr float kTanhNear = {float(np.float32(str(NEAR))):.9e}f;",
+             f"constexpr int kTanhDegree = {DEGREE};",
              f"constexpr float kTanhPoly[{DEGREE + 1}] = {{" + ", ".join(f"{float(x):.9e}f" for x in c) + "};",
              "", "}  // namespace attn", ""]
     return "\n".join(lines)

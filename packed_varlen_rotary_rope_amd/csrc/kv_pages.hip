@@ -8,7 +8,7 @@
 //
 // What bounds it: latency. A chain of loads, a scan and a search is most of a step of some thousand
 // tokens, so everything is one launch, without an order among its workgroups: each reads the
-// lengths from the first sequence on and scans them (4000 are four chunks), up to the tokens that are its
+// lengths from the first sequence on and scans them, 4096 at a time, up to the tokens that are its
 // own; one more writes what there is for each sequence.
 #include "attn_plan.h"
 #include "../../include/kv_pages.h"
@@ -19,6 +19,8 @@ namespace {
 constexpr int32_t kMostTokens = INT32_MAX - 4096;
 constexpr int64_t kMost = (int64_t)1 << 30;
 constexpr int32_t kTokensOfGroup = 2048;
+constexpr int kPerThread = 4;  // sequences
+constexpr int kChunk = kPerThread * kPlanThreads;
 
 // Tokens and pages: two sums of up to INT32_MAX, which they do not exceed.
 struct PairSum {
@@ -66,11 +68,22 @@ __device__ inline int32_t ring_at(int32_t first, int32_t i, int32_t num_pages) {
   return x < num_pages ? x : x - num_pages;
 }
 
+// The sequence of a token: the first of a chunk whose running count exceeds it.
+__device__ inline int find_sequence(const int32_t* upto, int32_t token) {
+  int lo = 0, hi = kChunk - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (upto[mid] > token) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
 __global__ __launch_bounds__(kPlanThreads) void kv_page_step_kernel(const StepParams p) {
   __shared__ uint64_t scan[kPlanWaves];
-  __shared__ int32_t upto[kPlanThreads];    // tokens up to each sequence of a chunk, itself too
-  __shared__ int32_t begin[kPlanThreads];   // what it held; < 0: refused
-  __shared__ int32_t fresh[kPlanThreads];   // where its new pages begin in the ring, less those it has
+  __shared__ int32_t upto[kChunk];    // tokens up to each sequence of a chunk, itself too
+  __shared__ int32_t begin[kChunk];   // what it held; < 0: refused
+  __shared__ int32_t fresh[kChunk];   // where its new pages begin in the ring, less those it has
   __shared__ uint64_t total;
   __shared__ int32_t used;
   const int t = threadIdx.x;
@@ -82,33 +95,54 @@ __global__ __launch_bounds__(kPlanThreads) void kv_page_step_kernel(const StepPa
   if (t == 0) used = 0;
 
   uint64_t before = 0;
-  for (int32_t s0 = 0; s0 < p.num_seqs; s0 += kPlanThreads) {
-    const int32_t s = s0 + t;
-    const int32_t n = s < p.num_seqs ? max(p.new_lens[s], 0) : 0;
-    const int32_t held = s < p.num_seqs ? max(p.held[s], 0) : 0;
-    const int64_t sum = (int64_t)held + n;
-    const int32_t has = pages_of(held, p.by_page);
-    const bool fits = sum < kMostTokens && pages_of((int32_t)sum, p.by_page) <= p.max_pages;
-    const int32_t wants = n > 0 && fits ? pages_of((int32_t)sum, p.by_page) - has : 0;
-    const uint64_t upto_here = PairSum::apply(before, block_scan<PairSum>((uint64_t)wants << 32 | (uint32_t)n, scan));
-    const int32_t last_token = (int32_t)(uint32_t)upto_here, last_page = (int32_t)(upto_here >> 32);
-    const bool served = n == 0 || (fits && last_token <= p.T && (wants == 0 || last_page <= count));
-    upto[t] = last_token;
-    begin[t] = served ? held : -1;
-    fresh[t] = last_page - wants - has;
-    if (t == kPlanThreads - 1) total = upto_here;
-    if (of_sequences && s < p.num_seqs) {
-      if (s == 0) p.cu[0] = 0;
-      p.cu[s + 1] = min(last_token, p.T);
-      p.kv_lens[s] = served ? (int32_t)min(sum, (int64_t)INT32_MAX) : 0;
-      p.held_out[s] = served && n > 0 ? (int32_t)sum : p.held[s];
-      if (served && wants > 0) atomicMax(&used, last_page);
+  for (int32_t s0 = 0; s0 < p.num_seqs; s0 += kChunk) {
+    int32_t n[kPerThread], held[kPerThread], wants[kPerThread];
+    bool fits[kPerThread];
+    uint64_t mine = 0;
+#pragma unroll
+    for (int y = 0; y < kPerThread; ++y) {
+      const int32_t s = s0 + t * kPerThread + y;
+      n[y] = s < p.num_seqs ? max(p.new_lens[s], 0) : 0;
+      held[y] = s < p.num_seqs ? max(p.held[s], 0) : 0;
+    }
+#pragma unroll
+    for (int y = 0; y < kPerThread; ++y) {
+      const int64_t sum = (int64_t)held[y] + n[y];
+      fits[y] = sum < kMostTokens && pages_of((int32_t)sum, p.by_page) <= p.max_pages;
+      wants[y] = n[y] > 0 && fits[y] ? pages_of((int32_t)sum, p.by_page) - pages_of(held[y], p.by_page) : 0;
+      mine = PairSum::apply(mine, (uint64_t)wants[y] << 32 | (uint32_t)n[y]);
+    }
+    const uint64_t all = PairSum::apply(before, block_scan<PairSum>(mine, scan));
+    if (t == kPlanThreads - 1) total = all;
+    // and back to each of the thread's sequences: what is before the first of them
+    uint64_t here = __shfl_up(all, 1);
+    if ((t & 63) == 0) {
+      here = before;
+      for (int w = 0; w < t >> 6; ++w) here = PairSum::apply(here, scan[w]);
+    }
+#pragma unroll
+    for (int y = 0; y < kPerThread; ++y) {
+      const int32_t x = t * kPerThread + y, s = s0 + x;
+      here = PairSum::apply(here, (uint64_t)wants[y] << 32 | (uint32_t)n[y]);
+      const int32_t last_token = (int32_t)(uint32_t)here, last_page = (int32_t)(here >> 32);
+      const bool served = n[y] == 0 || (fits[y] && last_token <= p.T && (wants[y] == 0 || last_page <= count));
+      upto[x] = last_token;
+      begin[x] = served ? held[y] : -1;
+      fresh[x] = last_page - wants[y] - pages_of(held[y], p.by_page);
+      if (of_sequences && s < p.num_seqs) {
+        const int32_t sum = (int32_t)((uint32_t)held[y] + (uint32_t)n[y]);  // where it is served, below 2^31
+        if (s == 0) p.cu[0] = 0;
+        p.cu[s + 1] = min(last_token, p.T);
+        p.kv_lens[s] = served ? sum : 0;
+        p.held_out[s] = served && n[y] > 0 ? sum : p.held[s];
+        if (served && wants[y] > 0) atomicMax(&used, last_page);
+      }
     }
     __syncthreads();
     const int32_t from = max(first_token, (int32_t)(uint32_t)before);
     const int32_t to = min(end_token, (int32_t)(uint32_t)total);
     for (int32_t token = from + t; token < to; token += kPlanThreads) {
-      const int x = find_slot(upto, token);
+      const int x = find_sequence(upto, token);
       const int32_t start = x > 0 ? upto[x - 1] : (int32_t)(uint32_t)before;
       const int32_t h = begin[x];
       int32_t pos = -1;

@@ -7,15 +7,21 @@
 // consecutive tokens, as many as give each of its threads kUnroll pairs of 16-byte chunks (fewer
 // where that would leave CUs without work): the loads of all of them are begun, cos and sin of the
 // tokens' frequencies are evaluated into LDS while they are on the way, and the pairs are rotated
-// and written.
+// and written, past the caches (non-temporal). Loads go past them too where a half row is whole
+// 128-byte lines, which no other chunk then needs again. Measured, GPU time at bf16 and 32 + 8 heads of
+// 128, 10814 tokens: 52 us through the caches, 43 with such stores, 40.5 with loads too, which is 5.5
+// TB/s (a large copy moves 5.1); 16 + 16 heads of 96: 36.5, 26.6, and 30.8, for lines are fetched
+// twice. 16004 tokens of 32 + 8 heads into the cache: 87, 74, 70 us. Workgroups of 64, 256 or 512 threads
+// and unrolling by 2 or 8 were up to 25 % slower on some of twelve such shapes and nowhere faster than 10 %.
 #include "attn_common.h"
 #include "cr_sincos.h"
+#include "storage.h"
 #include "../../include/rope_axes.h"
 
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxHalf = 256;
 constexpr int kUnroll = 4;
 constexpr int kMostTokens = 16;        // of a workgroup
@@ -40,14 +46,9 @@ struct AxesParams {
   float inv_freq[kMaxHalf];
 };
 
-template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Chunk {
-  T v[VEC];
-};
-
-template <typename T, int VEC, bool SLOTS>
+template <typename T, int VEC, bool SLOTS, bool LINES>
 __global__ __launch_bounds__(kThreads) void rope_axes_kernel(const AxesParams p) {
-  using C = Chunk<T, VEC>;
+  using C = storage::Chunk<T, VEC>;
   __shared__ float cs[kTableFloats], sn[kTableFloats];
   __shared__ int64_t row_of[kMostTokens];  // of the cache, in elements; < 0: none
   __shared__ uint8_t turns[kMostTokens];
@@ -86,8 +87,13 @@ __global__ __launch_bounds__(kThreads) void rope_axes_kernel(const AxesParams p)
         const T* src = static_cast<const T*>(is_q ? p.q : is_v ? p.v : p.k) +
                        (int64_t)(t0 + y) * (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) +
                        ((int64_t)h * p.D + c * VEC);
-        lo[u] = *reinterpret_cast<const C*>(src);
-        hi[u] = *reinterpret_cast<const C*>(src + half);
+        if constexpr (LINES) {
+          lo[u] = storage::load_chunk<T, VEC>(src);
+          hi[u] = storage::load_chunk<T, VEC>(src + half);
+        } else {
+          lo[u] = *reinterpret_cast<const C*>(src);
+          hi[u] = *reinterpret_cast<const C*>(src + half);
+        }
       }
     }
     if (i0 == 0) {  // the same for the whole workgroup
@@ -136,8 +142,8 @@ __global__ __launch_bounds__(kThreads) void rope_axes_kernel(const AxesParams p)
           }
         }
         if (write) {
-          *reinterpret_cast<C*>(to) = lo[u];
-          *reinterpret_cast<C*>(to + half) = hi[u];
+          storage::store_chunk<T, VEC>(to, lo[u]);
+          storage::store_chunk<T, VEC>(to + half, hi[u]);
         }
       }
     }
@@ -148,12 +154,17 @@ template <typename T, bool SLOTS>
 int32_t launch(const AxesParams& p, int32_t bytes, hipStream_t s) {
   const dim3 grid((unsigned)((p.T + (int64_t)p.group - 1) / p.group)), block(kThreads);
   switch (bytes / (int32_t)sizeof(T)) {
-    case 1: hipLaunchKernelGGL((rope_axes_kernel<T, 1, SLOTS>), grid, block, 0, s, p); break;
-    case 2: hipLaunchKernelGGL((rope_axes_kernel<T, 2, SLOTS>), grid, block, 0, s, p); break;
-    case 4: hipLaunchKernelGGL((rope_axes_kernel<T, 4, SLOTS>), grid, block, 0, s, p); break;
+    case 1: hipLaunchKernelGGL((rope_axes_kernel<T, 1, SLOTS, false>), grid, block, 0, s, p); break;
+    case 2: hipLaunchKernelGGL((rope_axes_kernel<T, 2, SLOTS, false>), grid, block, 0, s, p); break;
+    case 16 / sizeof(T):
+      if (p.D / 2 * sizeof(T) % 128 == 0)
+        hipLaunchKernelGGL((rope_axes_kernel<T, 16 / sizeof(T), SLOTS, true>), grid, block, 0, s, p);
+      else
+        hipLaunchKernelGGL((rope_axes_kernel<T, 16 / sizeof(T), SLOTS, false>), grid, block, 0, s, p);
+      break;
     default:
-      if constexpr (sizeof(T) == 2)
-        hipLaunchKernelGGL((rope_axes_kernel<T, 8, SLOTS>), grid, block, 0, s, p);
+      if constexpr (sizeof(T) == 2)  // 8 bytes
+        hipLaunchKernelGGL((rope_axes_kernel<T, 4, SLOTS, false>), grid, block, 0, s, p);
       else
         return ROPE_EINVAL;
   }
