@@ -19,8 +19,6 @@ namespace {
 constexpr int32_t kMostTokens = INT32_MAX - 4096;
 constexpr int64_t kMost = (int64_t)1 << 30;
 constexpr int32_t kTokensOfGroup = 2048;
-constexpr int kPerThread = 4;  // sequences
-constexpr int kChunk = kPerThread * kPlanThreads;
 
 // Tokens and pages: two sums of up to INT32_MAX, which they do not exceed.
 struct PairSum {
@@ -69,8 +67,9 @@ __device__ inline int32_t ring_at(int32_t first, int32_t i, int32_t num_pages) {
 }
 
 // The sequence of a token: the first of a chunk whose running count exceeds it.
+template <int N>
 __device__ inline int find_sequence(const int32_t* upto, int32_t token) {
-  int lo = 0, hi = kChunk - 1;
+  int lo = 0, hi = N - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (upto[mid] > token) hi = mid;
@@ -79,7 +78,9 @@ __device__ inline int find_sequence(const int32_t* upto, int32_t token) {
   return lo;
 }
 
+template <int kPerThread>  // sequences
 __global__ __launch_bounds__(kPlanThreads) void kv_page_step_kernel(const StepParams p) {
+  constexpr int kChunk = kPerThread * kPlanThreads;
   __shared__ uint64_t scan[kPlanWaves];
   __shared__ int32_t upto[kChunk];    // tokens up to each sequence of a chunk, itself too
   __shared__ int32_t begin[kChunk];   // what it held; < 0: refused
@@ -95,6 +96,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_page_step_kernel(const StepPa
   if (t == 0) used = 0;
 
   uint64_t before = 0;
+  int32_t most = 0;  // pages up to the last sequence that gets one
   for (int32_t s0 = 0; s0 < p.num_seqs; s0 += kChunk) {
     int32_t n[kPerThread], held[kPerThread], wants[kPerThread];
     bool fits[kPerThread];
@@ -135,14 +137,14 @@ __global__ __launch_bounds__(kPlanThreads) void kv_page_step_kernel(const StepPa
         p.cu[s + 1] = min(last_token, p.T);
         p.kv_lens[s] = served ? sum : 0;
         p.held_out[s] = served && n[y] > 0 ? sum : p.held[s];
-        if (served && wants[y] > 0) atomicMax(&used, last_page);
+        if (served && wants[y] > 0) most = last_page;
       }
     }
     __syncthreads();
     const int32_t from = max(first_token, (int32_t)(uint32_t)before);
     const int32_t to = min(end_token, (int32_t)(uint32_t)total);
     for (int32_t token = from + t; token < to; token += kPlanThreads) {
-      const int x = find_sequence(upto, token);
+      const int x = find_sequence<kChunk>(upto, token);
       const int32_t start = x > 0 ? upto[x - 1] : (int32_t)(uint32_t)before;
       const int32_t h = begin[x];
       int32_t pos = -1;
@@ -168,6 +170,11 @@ __global__ __launch_bounds__(kPlanThreads) void kv_page_step_kernel(const StepPa
     __syncthreads();
   }
   if (of_sequences) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) most = max(most, __shfl_xor(most, d));
+    __syncthreads();
+    if ((t & 63) == 0) atomicMax(&used, most);
+    __syncthreads();
     if (t == 0) {
       if (p.num_seqs == 0) p.cu[0] = 0;
       p.state_out[0] = ring_at(first, used, p.num_pages);
@@ -269,8 +276,13 @@ int32_t kv_page_step(const int32_t* new_lens, const int32_t* held, int32_t num_s
   p.num_pages = num_pages;
   p.by_page = make_div31(page_size);
   const unsigned groups = (unsigned)((T + kTokensOfGroup - 1) / kTokensOfGroup) + 1;
-  hipLaunchKernelGGL(kv_page_step_kernel, dim3(groups), dim3(kPlanThreads), 0,
-                     static_cast<hipStream_t>(stream), p);
+  // several sequences a thread, and one scan for all, where one a thread would take several
+  if (num_seqs > kPlanThreads)
+    hipLaunchKernelGGL((kv_page_step_kernel<4>), dim3(groups), dim3(kPlanThreads), 0,
+                       static_cast<hipStream_t>(stream), p);
+  else
+    hipLaunchKernelGGL((kv_page_step_kernel<1>), dim3(groups), dim3(kPlanThreads), 0,
+                       static_cast<hipStream_t>(stream), p);
   return launched();
 }
 
