@@ -44,7 +44,7 @@ __device__ inline float tanh_near(float y) {
 }
 
 // tanh(s by) of 16 scores, within 2^-22 of it relatively: a polynomial up to kTanhNear, which is all
-// that most blocks need, else 1 - 2 / (1 + exp(2 y)) too (8 operations of the full rate, against 4 and
+// that most blocks need, else 1 - 2 / (1 + exp(2 y)) too (7 operations of the full rate, against 4 and
 // two of a quarter of it, and exact near 0). A score's result depends on no other's.
 __device__ inline void bend_scores(f32x16& s, float by) {
   f32x16 y;

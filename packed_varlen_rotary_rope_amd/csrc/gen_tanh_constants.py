@@ -19,8 +19,8 @@ import numpy as np
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 OUT = os.path.join(HERE, "tanh_constants.h")
-DEGREE = 5
-NEAR = mp.mpf("0.8")
+DEGREE = 4
+NEAR = mp.mpf("0.6")
 MOST = 2.0 ** -22
 mp.mp.dps = 60
 

@@ -4,8 +4,8 @@
 
 namespace attn {
 
-constexpr float kTanhNear = 8.000000119e-01f;
-constexpr int kTanhDegree = 5;
-constexpr float kTanhPoly[6] = {9.999999404e-01f, -3.333266675e-01f, 1.332093179e-01f, -5.310926959e-02f, 1.908435300e-02f, -4.349738825e-03f};
+constexpr float kTanhNear = 6.000000238e-01f;
+constexpr int kTanhDegree = 4;
+constexpr float kTanhPoly[5] = {9.999999404e-01f, -3.333230317e-01f, 1.331006438e-01f, -5.209665373e-02f, 1.546875108e-02f};
 
 }  // namespace attn
