@@ -43,7 +43,8 @@ typedef enum rope_axes_layout {
  *  q, q_out   device [T][Hq][D], the heads of a token contiguous; q_out may be q (then with one
  *             token stride), else it must not overlap an input. Both NULL with Hq 0
  *  k, k_out   the same, [T][Hkv][D]
- *  T          0 .. 2^31 - 1; Hq, Hkv 0 .. 4096, not both 0
+ *  T          0 .. 33554431 (more, up to 2^31 - 1, where several tokens make a workgroup of 512 chunk
+ *             pairs); Hq, Hkv 0 .. 4096, not both 0
  *  D          even, 2 .. 512; dtype any rope_dtype; any strides and alignment (0: heads * D; the
  *             widest access that they allow is used)
  *  position_ids   device int32: axis a of token t at a * ids_stride + t
@@ -59,7 +60,7 @@ int32_t rope_qk_apply_axes(const void* q, void* q_out, const void* k, void* k_ou
 
 /* Writes new keys and values into the cache rows that a slot map names, the keys rotated, and the
  * rotated queries to q_out (as kv_append, which finds the rows by a block table). One launch.
- *  q, q_out, k, v, k_cache, v_cache, strides and sizes as in kv_append of attn.h (T up to 2^31 - 1)
+ *  q, q_out, k, v, k_cache, v_cache, strides and sizes as in kv_append of attn.h (T as above)
  *  slots      device int64[T]: token t goes to slot slots[t] % page_size of page slots[t] /
  *             page_size; a number outside 0 .. num_pages * page_size - 1 (-1) is no slot, and its
  *             token is not written. No two tokens may name one slot: it would hold parts of either

@@ -1,6 +1,6 @@
 """Fused, in-place, packed variable-length QK rotary position embedding (RoPE), the
 SwiGLU / GeGLU MLP activations, and the attention beside them (packed, and over a
-paged cache), for AMD Instinct MI355X (gfx950).
+paged cache, with its pages and positions with several axes), for AMD Instinct MI355X (gfx950).
 
 Thin Python binding over the C ABI of ``include/rope_qk.h`` and ``include/glu.h``
 (librope_qk.so, built from ``csrc/rope_qk.hip`` and ``csrc/glu.hip``). This module

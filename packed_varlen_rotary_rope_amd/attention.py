@@ -1,10 +1,11 @@
 """Attention around the rotary embedding: causal attention over packed sequences (forward
 and backward), the append of new keys and values to a paged cache (rotated on the way), and
-attention over that cache.
+attention over that cache, with capped and biased scores and prefixes, the rotation by positions with several axes, and the
+pages of the cache.
 
-Thin binding over the C ABI of ``include/attn.h`` and ``include/attn_ex.h`` (libattn.so, built by build_attn.py from
-``csrc/attn_*.hip`` and ``csrc/kv_append.hip``), as the package's other entry points are: it checks
-tensor metadata and marshals pointers, sizes and the current HIP stream. There is no
+Thin binding over the C ABI of ``include/attn.h``, ``attn_ex.h``, ``rope_axes.h`` and ``kv_pages.h``
+(libattn.so, built by build_attn.py from ``csrc/attn_*.hip``, ``kv_append.hip``, ``rope_axes.hip`` and
+``kv_pages.hip``), as the package's other entry points are: it checks tensor metadata and marshals pointers, sizes and the current HIP stream. There is no
 fallback: if the library is missing, importing this module raises. The public names are
 exported by the package itself; differentiable wrappers live in ``functional``.
 

