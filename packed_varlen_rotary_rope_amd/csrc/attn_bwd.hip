@@ -69,6 +69,11 @@ namespace {
 // 2048 tokens, scores of size 4 under a cap of 50, are off by 0.0024 of their norm with it, of which the
 // rounding of dS and of the result is all, and by 0.0032 without (bf16, 32 + 8 heads of 128).
 constexpr int32_t kExactKeys = ATTN_MODS ? INT32_MAX : 256;
+// dQ of changed scores takes dS in two parts, rounded and what the rounding left, up to 64 columns, where the
+// vector unit is what is waited for and a product more costs 1 to 3 % of the pass (28 samples of 799 tokens,
+// 32 + 8 heads of 64, cap and bias: 425 and 427 us): dQ is then off by the rounding of the result alone. At 128
+// columns it would be 10 % (415 and 457 us for eight samples of 256 to 2048 tokens).
+constexpr bool two_parts(int db) { return ATTN_MODS != 0 && db <= 2; }
 constexpr bool kHasCap = ATTN_MODS & kCap, kHasBias = ATTN_MODS & kBias;
 // Where a batch is too small to give every workgroup of the dK/dV pass so many units, cuts that would leave
 // a tile a block or none before or behind them are moved to its end: a piece without blocks costs its latency and a
@@ -229,12 +234,15 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const x8<T> ds = narrow8<T>(s, t);
+        x8<T> low;  // what its rounding left
+        if constexpr (two_parts(DB)) low = rest8<T>(s, ds, t);
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
           x8<T> kc = read_columns<T, CPR>(kt, 32 * c + 16 * t, d, lane);
           // a key that is seen and not finite has made dS NaN or 0 already
           if constexpr (decltype(mode)::value == kCareful) kc = cleaned<T>(kc);
           dq[d] = mfma(kc, ds, dq[d]);
+          if constexpr (two_parts(DB)) dq[d] = mfma(kc, low, dq[d]);
         }
       }
     }

@@ -91,6 +91,16 @@ __device__ inline x8<T> narrow8(const f32x16& c, int s) {
   return __builtin_bit_cast(x8<T>, w);
 }
 
+// What the rounding of narrow8 left of them, narrowed.
+template <typename T>
+__device__ inline x8<T> rest8(const f32x16& c, x8<T> rounded, int s) {
+  u32x4 w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = narrow2<T>(c[8 * s + 2 * j] - (float)rounded[2 * j], c[8 * s + 2 * j + 1] - (float)rounded[2 * j + 1]);
+  return __builtin_bit_cast(x8<T>, w);
+}
+
 // The two lanes l and l + 32 hold halves of one column: lo and hi are theirs, in both.
 __device__ inline void both_halves(float x, float* lo, float* hi) {
   const uint32_t a = __builtin_bit_cast(uint32_t, x);
