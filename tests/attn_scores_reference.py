@@ -12,9 +12,11 @@ E_i = sum_j P_ij e_ij. The weights are rounded to the storage type (u), their su
 n 2^-24, exp2 and the division by a few 2^-23, and the output is rounded once:
     |out - exact| <= sum_j P_ij (u + e_ij + E_i + (n + 32) 2^-23) |v_j| + u |exact|
 up to second order, for which 1% is added. Backward, P is formed again from the scores and the rounded
-lse (|lse| 2^-22 + 2^-21 more), dP errs by D 2^-24 sum |do v|, D_i by sum |do| times the output's
-bound, r = 1 - t^2 by 2 |t| times what t is off, (1 - t^2) e / cap + |t| 2^-21, and 2^-24; dS = P (dP -
-D_i) r is rounded once, sums over c terms err by c 2^-24 of their magnitudes and outputs are rounded once.
+lse (|lse| 2^-22 + 2^-21 more), dP errs by D 2^-24 sum |do v|, D_i, where it is formed from the rounded output
+(prefixes alone), by sum |do| times the output's bound, and else, a sum of P dP, by what P and dP are
+off and n 2^-23 of its magnitudes; r = 1 - t^2 by 2 |t| times what t is off, (1 - t^2) e / cap + |t| 2^-21, and
+2^-24; dS = P (dP - D_i) r is rounded once (for dq of changed scores up to D = 64, in two parts, u^2), sums
+over c terms err by c 2^-24 of their magnitudes and outputs are rounded once.
 """
 import torch
 
@@ -139,18 +141,24 @@ def backward(do, q, k, v, seqs, scale, dtype, cap=None, slopes=None, prefixes=No
             rp = f["rel"] + f["lse"].abs()[:, None] * 2.0 ** -22 + 2.0 ** -21
             dp, delta = dh @ vh.T, (dh * f["out"]).sum(-1, keepdim=True)
             e_dp = D * 2.0 ** -24 * (dh.abs() @ vh.abs().T)
-            e_delta = (dh.abs() * (out_bound(f, u, dtype) + D * 2.0 ** -24 * f["out"].abs())).sum(-1, keepdim=True)
+            changed = cap is not None or slopes is not None
+            if changed:
+                e_delta = (p * ((rp + (n + 32) * 2.0 ** -23) * dp.abs() + e_dp)).sum(-1, keepdim=True)
+            else:
+                e_delta = (dh.abs() * (out_bound(f, u, dtype) + D * 2.0 ** -24 * f["out"].abs())).sum(-1, keepdim=True)
             r, e_r = 1.0, 0.0
             if cap is not None:
                 r = 1 - f["t"] ** 2
                 e_r = 2 * f["t"].abs() * (r * f["e"] / cap + f["t"].abs() * 2.0 ** -21) + 2.0 ** -24
             ds = p * (dp - delta) * r
-            e_ds = (u + rp) * ds.abs() + p * ((e_dp + e_delta) * (r + e_r) + (dp - delta).abs() * e_r) * (1 + rp)
-            e_ds = e_ds + tiny(dtype)
+            e_ds = rp * ds.abs() + p * ((e_dp + e_delta) * (r + e_r) + (dp - delta).abs() * e_r) * (1 + rp)
+            e_dsq = (u * u if changed and D <= 64 else u) * ds.abs() + e_ds + tiny(dtype)
+            e_ds = u * ds.abs() + e_ds + tiny(dtype)
             e_p = (u + rp) * p + tiny(dtype)
             c = (n * G + 64) * 2.0 ** -24
             grads[0][sl, h] = scale * (ds @ kh)
-            tols[0][sl, h] = 1.01 * scale * (e_ds @ kh.abs() + c * (ds.abs() @ kh.abs()))
+            terms = 2 if changed and D <= 64 else 1
+            tols[0][sl, h] = 1.01 * scale * (e_dsq @ kh.abs() + terms * c * (ds.abs() @ kh.abs()))
             grads[1][sl, g] += scale * (ds.T @ qh)
             tols[1][sl, g] += 1.01 * scale * (e_ds.T @ qh.abs() + c * (ds.abs().T @ qh.abs()))
             grads[2][sl, g] += p.T @ dh
