@@ -567,3 +567,85 @@ def test_a_service_with_images(rope):
         plan = rope.attn_plan(int32([0, lengths[s]]), lengths[s], Hq, Hkv, prefix_lens=int32([images[s]]))
         packed, _ = rope.attn_fwd(q, k, qkv[s][:, Hq + Hkv:], plan, softcap=cap)
         r.check(packed, want, tol, "packed")
+
+
+def test_captured_layer(rope):
+    """Plan, rotation, attention and their gradients through autograd in a graph: replays with other inputs,
+    positions, sequences and prefixes give the eager bits."""
+    import packed_varlen_rotary_rope_amd.functional as F
+    T, Hq, Hkv, D, sections = 260, 4, 2, 64, (12, 10, 10)
+    cu, prefixes, slopes = int32([0, 100, 260]), int32([30, 0]), slopes_of(Hq)
+    pos = torch.zeros((3, T), dtype=torch.int32, device=DEV)
+    x = normal((T, Hq + 2 * Hkv, D), 1, BF16).requires_grad_()
+    do = normal((T, Hq, D), 2, BF16)
+    plan = rope.attn_plan(cu, T, Hq, Hkv, prefix_lens=prefixes)
+
+    def layer():
+        qkv = F.rope_qkv_axes(x * 1.0, Hq, Hkv, pos, sections, 1e4)
+        out = F.attn_qkv(qkv, Hq, Hkv, plan, softcap=10.0, slopes=slopes)
+        return out, *torch.autograd.grad(out, (x,), do)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rope.attn_plan(cu, T, Hq, Hkv, out=plan, prefix_lens=prefixes)
+        res = layer()
+    for i, (bounds, pre) in enumerate((([0, 100, 260], [50, 160]), ([0, 1, 2], [1, 0]), ([20, 200, 260], [0, 9]))):
+        with torch.no_grad():
+            x.copy_(normal(x.shape, 40 + i, BF16))
+        cu.copy_(int32(bounds))
+        prefixes.copy_(int32(pre))
+        pos.copy_(torch.randint(0, 999, (3, T), device=DEV))
+        graph.replay()
+        got = [t.detach().clone() for t in res]
+        with torch.no_grad():
+            y = x.detach().clone()
+            q, k, v = y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:]
+            rope.qk_apply_axes(q, k, pos, sections, 1e4, q_out=q, k_out=k)
+            fresh = rope.attn_plan(int32(bounds), T, Hq, Hkv, prefix_lens=int32(pre))
+            more = dict(softcap=10.0, slopes=slopes)
+            out, lse = rope.attn_fwd(q, k, v, fresh, **more)
+            dq, dk, dv = rope.attn_bwd(do, q, k, v, out, lse, fresh, **more)
+            dq, dk = rope.qk_apply_axes(dq, dk, pos, sections, 1e4, -1)
+            grad = torch.cat([dq, dk, dv], 1)
+        torch.cuda.synchronize()
+        assert same(got[0], out) and same(got[1], grad)
+
+
+@pytest.mark.parametrize("cap", [1e-3, 1e4, 1e9, 1e25])
+def test_caps_of_any_size(rope, cap):
+    """Far below the scores, and far above them, where it changes nothing."""
+    cu, T, H, D = [0, 100, 170], 170, 2, 64
+    q, k, v, do = (normal((T, H, D), i, F16) for i in range(4))
+    plan = rope.attn_plan(int32(cu), T, H, H)
+    out, lse = rope.attn_fwd(q, k, v, plan, softcap=cap)
+    args = (ref.sequences(cu, T), D ** -0.5)
+    want, wlse, tol, ltol = ref.forward(q, k, v, *args, cap)
+    ref.check(out, want, tol, "out")
+    ref.check(lse, wlse, ltol, "lse")
+    grads = rope.attn_bwd(do, q, k, v, out, lse, plan, softcap=cap)
+    for name, got, x, t in zip(("dq", "dk", "dv"), grads, *ref.backward(do, q, k, v, *args, F16, cap)):
+        ref.check(got, x, t, name)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,count,most", [(5, 5, 72, 24, 9), (8, 2, 128, 40, 130), (6, 1, 64, 9, 40), (2, 2, 32, 300, 200)])
+def test_small_batches_whose_key_tiles_are_cut(rope, Hq, Hkv, D, count, most):
+    """Work below a full chip's, of many lengths: pieces of key tiles of every size, in f16."""
+    lens = torch.randint(1, most, (count,), generator=torch.Generator().manual_seed(count)).tolist()
+    lens[0] = 517
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    T, slopes = cu[-1], slopes_of(Hq)
+    q, k, v, do = (normal((T, h, D), i, F16) for i, h in enumerate((Hq, Hkv, Hkv, Hq)))
+    prefixes = [n * (s % 3) // 4 for s, n in enumerate(lens)]
+    plan = rope.attn_plan(int32(cu), T, Hq, Hkv, prefix_lens=int32(prefixes))
+    out, lse = rope.attn_fwd(q, k, v, plan, slopes=slopes)
+    grads = rope.attn_bwd(do, q, k, v, out, lse, plan, slopes=slopes)
+    want = ref.backward(do, q, k, v, ref.sequences(cu, T), D ** -0.5, F16, None, slopes, prefixes)
+    for name, got, x, t in zip(("dq", "dk", "dv"), grads, *want):
+        ref.check(got, x, t, name)
