@@ -4,7 +4,7 @@
 // Mathematics: as in kv_append.hip, with the angle of frequency j from the position on its axis.
 //
 // What bounds it: memory; every element is read once and written once. A workgroup takes `group`
-// consecutive tokens, as many as give each of its threads kUnroll pairs of 16-byte chunks (fewer
+// consecutive tokens, as many as give each of its threads two or four pairs of chunks (fewer
 // where that would leave CUs without work): the loads of all of them are begun, cos and sin of the
 // tokens' frequencies are evaluated into LDS while they are on the way, and the pairs are rotated
 // and written, past the caches (non-temporal). Loads go past them too where a half row is whole
@@ -12,7 +12,7 @@
 // 128, 10814 tokens: 52 us through the caches, 43 with such stores, 40.5 with loads too, which is 5.5
 // TB/s (a large copy moves 5.1); 16 + 16 heads of 96: 36.5, 26.6, and 30.8, for lines are fetched
 // twice. 16004 tokens of 32 + 8 heads into the cache: 87, 74, 70 us. Workgroups of 64, 256 or 512 threads
-// and unrolling by 2 or 8 were up to 25 % slower on some of twelve such shapes and nowhere faster than 10 %.
+// were up to 25 % slower on some of twelve such shapes and nowhere faster than 10 %.
 #include "attn_common.h"
 #include "cr_sincos.h"
 #include "storage.h"
@@ -23,7 +23,13 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kMaxHalf = 256;
-constexpr int kUnroll = 4;
+// Chunk pairs of a thread whose loads are in flight together. Two where the rotation alone moves 16-byte
+// chunks that share lines (16 + 16 heads of 80, 8641 tokens: 18.1 us, and 20.1 with four; 32 + 8 heads of 32: 13.0
+// and 15.5; of 96: 24.6 and 26.6; of 64: the same), four elsewhere (heads of 72, 8-byte chunks: 13.0, and 16.8 with
+// two; into the cache, heads of 64: 39.9 and 44.9).
+constexpr int unroll(int chunk_bytes, bool slots, bool lines) {
+  return chunk_bytes == 16 && !slots && !lines ? 2 : 4;
+}
 constexpr int kMostTokens = 16;        // of a workgroup
 constexpr int kTableFloats = 2048;     // of cos, and of sin: 16 KB of LDS
 constexpr int64_t kFewest = 1024;      // workgroups, where there are tokens for them
@@ -50,6 +56,7 @@ struct AxesParams {
 template <typename T, int VEC, bool SLOTS, bool LINES>
 __global__ __launch_bounds__(kThreads) void rope_axes_kernel(const AxesParams p) {
   using C = storage::Chunk<T, VEC>;
+  constexpr int kUnroll = unroll(VEC * sizeof(T), SLOTS, LINES);
   __shared__ float cs[kTableFloats], sn[kTableFloats];
   __shared__ int64_t row_of[kMostTokens];  // of the cache, in elements; < 0: none
   __shared__ uint8_t turns[kMostTokens];
@@ -151,6 +158,8 @@ __global__ __launch_bounds__(kThreads) void rope_axes_kernel(const AxesParams p)
   }
 }
 
+inline bool whole_lines(int32_t D, int32_t size) { return D / 2 * size % 128 == 0; }
+
 template <typename T, bool SLOTS>
 int32_t launch(const AxesParams& p, int32_t bytes, hipStream_t s) {
   const dim3 grid((unsigned)((p.T + (int64_t)p.group - 1) / p.group)), block(kThreads);
@@ -158,7 +167,7 @@ int32_t launch(const AxesParams& p, int32_t bytes, hipStream_t s) {
     case 1: hipLaunchKernelGGL((rope_axes_kernel<T, 1, SLOTS, false>), grid, block, 0, s, p); break;
     case 2: hipLaunchKernelGGL((rope_axes_kernel<T, 2, SLOTS, false>), grid, block, 0, s, p); break;
     case 16 / sizeof(T):
-      if (p.D / 2 * sizeof(T) % 128 == 0)
+      if (whole_lines(p.D, sizeof(T)))
         hipLaunchKernelGGL((rope_axes_kernel<T, 16 / sizeof(T), SLOTS, true>), grid, block, 0, s, p);
       else
         hipLaunchKernelGGL((rope_axes_kernel<T, 16 / sizeof(T), SLOTS, false>), grid, block, 0, s, p);
@@ -229,7 +238,7 @@ int32_t set_geometry(AxesParams& p, int32_t size, bool slots, const int64_t (&of
     while (bytes > size && x % bytes != 0) bytes >>= 1;
   const int32_t half = p.D / 2, pairs = half * size / bytes;
   const int32_t per_token = (p.Hq + (slots ? 2 : 1) * p.Hkv) * pairs;
-  int64_t group = kUnroll * kThreads / per_token;
+  int64_t group = unroll(bytes, slots, whole_lines(p.D, size)) * kThreads / per_token;
   group = group > kMostTokens ? kMostTokens : group;
   group = group > kTableFloats / half ? kTableFloats / half : group;
   group = group > p.T / kFewest ? p.T / kFewest : group;
