@@ -586,13 +586,22 @@ class PagePool:
     (int32[2]: the first free page's place, and how many are free)."""
 
     def __init__(self, ring, state):
-        dev = ring.device
-        _gpu(dev)
-        _index(ring, "ring", dev)
-        _index(state, "state", dev, 2)
-        if ring.dim() != 1 or not 1 <= ring.numel() <= 1 << 30:
-            raise ValueError("ring: expected 1 .. 2^30 page numbers")
         self.ring, self.state = ring, state
+        _pool(self)
+
+
+def _pool(pool):
+    """A pool's ring, state and device, checked: either may have been replaced since it was made."""
+    if not isinstance(pool, PagePool):
+        raise TypeError("pool: expected a PagePool")
+    ring, state = pool.ring, pool.state
+    dev = ring.device
+    _gpu(dev)
+    _index(ring, "ring", dev)
+    _index(state, "state", dev, 2)
+    if ring.dim() != 1 or not 1 <= ring.numel() <= 1 << 30:
+        raise ValueError("ring: expected 1 .. 2^30 page numbers")
+    return ring, state, dev
 
 
 def page_pool(num_pages: int, device=None) -> PagePool:
@@ -612,6 +621,35 @@ class PageStep(NamedTuple):
     slots: torch.Tensor
 
 
+def _step_buffers(out, B: int, T: int, device, ring, state, held, new_lens, block_table) -> None:
+    """Checks a step that is to be written over: its buffers, and that none of them is read or written
+    as another one too (the launch has no order in which that could be right)."""
+    if not isinstance(out, PageStep):
+        raise TypeError("out: expected what page_step returns")
+    cu, kv_lens, after, positions, after_state, slots = out
+    for t, name, n in ((cu, "cu_seqlens", B + 1), (kv_lens, "kv_lens", B), (after, "held", B),
+                       (positions, "positions", T), (after_state, "state", 2), (slots, "slots", T)):
+        if t.dtype != (torch.int64 if t is slots else torch.int32) or t.device != device or not t.is_contiguous():
+            raise TypeError(f"out.{name}: expected a contiguous int{64 if t is slots else 32} tensor on {device}")
+        if t.numel() != n:
+            raise ValueError("out: a step of other sizes or of another device")
+    spans = []  # of bytes, and whether they are written
+    for t in (*out, held, new_lens, ring, state):
+        begin = t.data_ptr()
+        spans.append((begin, begin + t.numel() * t.element_size(), len(spans) < 6))
+    if block_table.numel() > 0:
+        begin = block_table.data_ptr()
+        rows, per = block_table.shape
+        spans.append((begin, begin + 4 * ((rows - 1) * (block_table.stride(0) if rows > 1 else 0) + per), True))
+    written = touched = 0  # where the spans so far end, those that are written and all of them
+    for begin, end, writes in sorted(spans):
+        if begin < (touched if writes else written) and end > begin:
+            raise ValueError("out: what is read, or written as something else, cannot be written over")
+        touched = max(touched, end)
+        if writes:
+            written = max(written, end)
+
+
 def page_step(pool: PagePool, block_table, held, new_lens, T: int, page_size: int, out=None) -> PageStep:
     """Pages, slots and positions of one step over a paged cache, on the GPU: sequence s holds held[s]
     tokens and gets new_lens[s] (int32[B]) of the step's T. The pages that they need are taken from
@@ -623,15 +661,11 @@ def page_step(pool: PagePool, block_table, held, new_lens, T: int, page_size: in
     is refused where it needs more pages than its row of the table has, where the pages asked for up
     to it are more than are free, and where its tokens do not all lie in the T rows: its kv_lens is 0,
     which leaves its tokens out of kv_append_ and attn_paged, its held what it was. `out`: a step
-    of the same sizes to be written over, other than the one whose `held` or `state` this reads."""
-    if not isinstance(pool, PagePool):
-        raise TypeError("pool: expected a PagePool")
-    ring, before = pool.ring, pool.state
-    dev = ring.device
+    of the same sizes to be written over, none of whose tensors this reads (as `held` or `state`, say)."""
+    ring, before, dev = _pool(pool)
     T, page_size, B = int(T), int(page_size), new_lens.numel()
     _index(new_lens, "new_lens", dev)
     _index(held, "held", dev, B)
-    _index(before, "state", dev, 2)
     per, table_stride = _table(block_table, B, dev)
     if not 0 <= T <= 1 << 30 or not 1 <= page_size <= 1 << 30:
         raise ValueError("T: expected 0 .. 2^30, page_size: 1 .. 2^30")
@@ -642,12 +676,8 @@ def page_step(pool: PagePool, block_table, held, new_lens, T: int, page_size: in
         state, cu, kv_lens, after, positions = torch.empty(
             3 + 3 * B + T, dtype=torch.int32, device=dev).split_with_sizes((2, B + 1, B, B, T))
         out = PageStep(cu, kv_lens, after, positions, state, torch.empty(T, dtype=torch.int64, device=dev))
-    elif not isinstance(out, PageStep):
-        raise TypeError("out: expected what page_step returns")
-    elif (out.held.numel(), out.positions.numel(), out.held.device) != (B, T, dev):
-        raise ValueError("out: a step of other sizes or of another device")
-    elif (B > 0 and out.held.data_ptr() == held.data_ptr()) or out.state.data_ptr() == before.data_ptr():
-        raise ValueError("out: the step whose held or state is read cannot be written over")
+    else:
+        _step_buffers(out, B, T, dev, ring, before, held, new_lens, block_table)
     _call(dev, _lib.kv_page_step, "kv_page_step", new_lens.data_ptr(), held.data_ptr(), B, T, page_size,
           block_table.data_ptr(), per, table_stride, ring.data_ptr(), ring.numel(), before.data_ptr(),
           out.cu_seqlens.data_ptr(), out.kv_lens.data_ptr(), out.held.data_ptr(), out.positions.data_ptr(),
@@ -658,16 +688,13 @@ def page_step(pool: PagePool, block_table, held, new_lens, T: int, page_size: in
 def page_release_(pool: PagePool, block_table, held, gone, page_size: int) -> None:
     """Give the pages of the sequences with gone[s] (bool[B]) back to the pool, in place: the first
     ceil(held[s] / page_size) entries of their rows of block_table; their held becomes 0."""
-    if not isinstance(pool, PagePool):
-        raise TypeError("pool: expected a PagePool")
-    dev, B = pool.ring.device, held.numel()
+    ring, state, dev = _pool(pool)
+    B = held.numel()
     _index(held, "held", dev)
-    _index(pool.state, "state", dev, 2)
     if gone.dtype != torch.bool or gone.device != dev or not gone.is_contiguous():
         raise TypeError(f"gone must be a contiguous bool tensor on {dev}")
     if gone.numel() != B:
         raise ValueError("gone must have one entry per sequence")
     per, table_stride = _table(block_table, B, dev)
     _call(dev, _lib.kv_page_release, "kv_page_release", held.data_ptr(), gone.data_ptr(), B, int(page_size),
-          block_table.data_ptr(), per, table_stride, pool.ring.data_ptr(), pool.ring.numel(),
-          pool.state.data_ptr())
+          block_table.data_ptr(), per, table_stride, ring.data_ptr(), ring.numel(), state.data_ptr())
