@@ -16,7 +16,7 @@
  * to 24 bits beyond; the backward has
  *     dS_ij = P_ij (dP_ij - D_i) (1 - tanh(..)^2)
  * and no gradient of slopes; D_i is formed as sum_j P_ij dP_ij, and for dq up to D = 64 dS enters the product
- * in two parts of the storage type (one past 65504 in f16 gives no number there). Scores that are
+ * in two parts of the storage type (one past 65504 in f16 overflows as in attn.h). Scores that are
  * infinite are capped like others. Precision, layouts,
  * limits, ownership, threading and errors are those of attn.h. With cap 0 and without slopes the
  * calls are those of attn.h, and so are their results.

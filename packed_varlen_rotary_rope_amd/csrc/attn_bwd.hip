@@ -217,7 +217,8 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
       }
     }
   };
-  auto block = [&](auto mode, const uint8_t* kt, int32_t key0) __attribute__((always_inline)) {
+  // anew: in the second walk
+  auto block = [&](auto mode, auto anew, const uint8_t* kt, int32_t key0) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < BN / 32; ++c) {
       f32x16 s, dp;
@@ -234,8 +235,11 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const x8<T> ds = narrow8<T>(s, t);
-        x8<T> low;  // what its rounding left
-        if constexpr (two_parts(DB)) low = rest8<T>(s, ds, t);
+        x8<T> low;  // what its rounding left; nothing of a dS that it has made infinite
+        if constexpr (two_parts(DB)) {
+          low = rest8<T>(s, ds, t);
+          if constexpr (decltype(anew)::value) low = cleaned<T>(low);
+        }
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
           x8<T> kc = read_columns<T, CPR>(kt, 32 * c + 16 * t, d, lane);
@@ -311,17 +315,18 @@ __global__ __launch_bounds__(256, 2) void attn_bwd_rows_kernel(const BwdParams p
   // two loops, and a second walk where it is needed, as in the forward
   const int32_t all = wave_end > 0 ? wave_all / BN : 0;
   auto walk = [&](auto mode) __attribute__((always_inline)) {
+    constexpr Constant<decltype(mode)::value == kCareful> anew{};
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) dq[d][i] = 0.0f;
     for (; b < all; ++b) {
       const uint8_t* kt = arrive();
-      block(Constant<kWhole>(), kt, b * BN);
+      block(Constant<kWhole>(), anew, kt, b * BN);
     }
     for (; b < blocks; ++b) {
       const uint8_t* kt = arrive();
-      if (b * BN < wave_end) block(mode, kt, b * BN);
+      if (b * BN < wave_end) block(mode, anew, kt, b * BN);
       else skip();
     }
     wait_copies<0>();
