@@ -43,8 +43,8 @@ typedef enum rope_axes_layout {
  *  q, q_out   device [T][Hq][D], the heads of a token contiguous; q_out may be q (then with one
  *             token stride), else it must not overlap an input. Both NULL with Hq 0
  *  k, k_out   the same, [T][Hkv][D]
- *  T          0 .. 33554431 (more, up to 2^31 - 1, where several tokens make a workgroup of 512 chunk
- *             pairs); Hq, Hkv 0 .. 4096, not both 0
+ *  T          0 .. 33554431 times 16, or times 4096 / D (rounded down) for D above 256: that many
+ *             workgroups of so many tokens are a launch; Hq, Hkv 0 .. 4096, not both 0
  *  D          even, 2 .. 512; dtype any rope_dtype; any strides and alignment (0: heads * D; the
  *             widest access that they allow is used)
  *  position_ids   device int32: axis a of token t at a * ids_stride + t

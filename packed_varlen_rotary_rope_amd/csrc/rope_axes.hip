@@ -239,10 +239,12 @@ int32_t set_geometry(AxesParams& p, int32_t size, bool slots, const int64_t (&of
   const int32_t half = p.D / 2, pairs = half * size / bytes;
   const int32_t per_token = (p.Hq + (slots ? 2 : 1) * p.Hkv) * pairs;
   int64_t group = unroll(bytes, slots, whole_lines(p.D, size)) * kThreads / per_token;
+  group = group > p.T / kFewest ? p.T / kFewest : group;
+  const int64_t least = (p.T + kMostGroups - 1) / kMostGroups;  // 1, or what a dispatch leaves of very many
+  group = group < least ? least : group;
   group = group > kMostTokens ? kMostTokens : group;
   group = group > kTableFloats / half ? kTableFloats / half : group;
-  group = group > p.T / kFewest ? p.T / kFewest : group;
-  p.group = (int32_t)(group < 1 ? 1 : group);
+  p.group = (int32_t)group;
   p.by_pairs = make_div31(pairs);
   p.by_token = make_div31(per_token);
   p.by_half = make_div31(half);
