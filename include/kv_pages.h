@@ -42,7 +42,7 @@ extern "C" {
  *  slots            device int64[T], written: page * page_size + position % page_size, as
  *                   kv_append_slots of rope_axes.h takes it; -1 also where the page is negative
  *  state_out        device int32[2], written
- * No output may overlap an input or another output. One launch. */
+ * An output, the table among them, that overlaps an input or another output is refused. One launch. */
 int32_t kv_page_step(const int32_t* new_lens, const int32_t* held, int32_t num_seqs, int64_t T,
                      int32_t page_size, int32_t* block_table, int32_t max_pages, int64_t table_stride,
                      const int32_t* ring, int32_t num_pages, const int32_t* state, int32_t* cu_seqlens,

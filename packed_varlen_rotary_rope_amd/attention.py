@@ -587,21 +587,34 @@ class PagePool:
 
     def __init__(self, ring, state):
         self.ring, self.state = ring, state
-        _pool(self)
+
+    # checked where they are set, so that calls need not: either may be replaced by another one
+    @property
+    def ring(self):
+        return self._ring
+
+    @ring.setter
+    def ring(self, ring):
+        _gpu(ring.device)
+        _index(ring, "ring", ring.device if not hasattr(self, "_state") else self._state.device)
+        if ring.dim() != 1 or not 1 <= ring.numel() <= 1 << 30:
+            raise ValueError("ring: expected 1 .. 2^30 page numbers")
+        self._ring = ring
+
+    @property
+    def state(self):
+        return self._state
+
+    @state.setter
+    def state(self, state):
+        self._state = _index(state, "state", self._ring.device, 2)
 
 
 def _pool(pool):
-    """A pool's ring, state and device, checked: either may have been replaced since it was made."""
+    """A pool's ring, state and device."""
     if not isinstance(pool, PagePool):
         raise TypeError("pool: expected a PagePool")
-    ring, state = pool.ring, pool.state
-    dev = ring.device
-    _gpu(dev)
-    _index(ring, "ring", dev)
-    _index(state, "state", dev, 2)
-    if ring.dim() != 1 or not 1 <= ring.numel() <= 1 << 30:
-        raise ValueError("ring: expected 1 .. 2^30 page numbers")
-    return ring, state, dev
+    return pool._ring, pool._state, pool._ring.device
 
 
 def page_pool(num_pages: int, device=None) -> PagePool:
@@ -621,33 +634,18 @@ class PageStep(NamedTuple):
     slots: torch.Tensor
 
 
-def _step_buffers(out, B: int, T: int, device, ring, state, held, new_lens, block_table) -> None:
-    """Checks a step that is to be written over: its buffers, and that none of them is read or written
-    as another one too (the launch has no order in which that could be right)."""
+def _step_buffers(out, B: int, T: int, device) -> None:
+    """Checks the tensors of a step that is to be written over."""
     if not isinstance(out, PageStep):
         raise TypeError("out: expected what page_step returns")
-    cu, kv_lens, after, positions, after_state, slots = out
-    for t, name, n in ((cu, "cu_seqlens", B + 1), (kv_lens, "kv_lens", B), (after, "held", B),
-                       (positions, "positions", T), (after_state, "state", 2), (slots, "slots", T)):
-        if t.dtype != (torch.int64 if t is slots else torch.int32) or t.device != device or not t.is_contiguous():
-            raise TypeError(f"out.{name}: expected a contiguous int{64 if t is slots else 32} tensor on {device}")
+    for t, name, dtype, n in zip(out, PageStep._fields, _STEP_TYPES, (B + 1, B, B, T, 2, T)):
+        if t.dtype != dtype or t.device != device or not t.is_contiguous():
+            raise TypeError(f"out.{name}: expected a contiguous {str(dtype)[6:]} tensor on {device}")
         if t.numel() != n:
             raise ValueError("out: a step of other sizes or of another device")
-    spans = []  # of bytes, and whether they are written
-    for t in (*out, held, new_lens, ring, state):
-        begin = t.data_ptr()
-        spans.append((begin, begin + t.numel() * t.element_size(), len(spans) < 6))
-    if block_table.numel() > 0:
-        begin = block_table.data_ptr()
-        rows, per = block_table.shape
-        spans.append((begin, begin + 4 * ((rows - 1) * (block_table.stride(0) if rows > 1 else 0) + per), True))
-    written = touched = 0  # where the spans so far end, those that are written and all of them
-    for begin, end, writes in sorted(spans):
-        if begin < (touched if writes else written) and end > begin:
-            raise ValueError("out: what is read, or written as something else, cannot be written over")
-        touched = max(touched, end)
-        if writes:
-            written = max(written, end)
+
+
+_STEP_TYPES = (torch.int32,) * 5 + (torch.int64,)
 
 
 def page_step(pool: PagePool, block_table, held, new_lens, T: int, page_size: int, out=None) -> PageStep:
@@ -661,7 +659,8 @@ def page_step(pool: PagePool, block_table, held, new_lens, T: int, page_size: in
     is refused where it needs more pages than its row of the table has, where the pages asked for up
     to it are more than are free, and where its tokens do not all lie in the T rows: its kv_lens is 0,
     which leaves its tokens out of kv_append_ and attn_paged, its held what it was. `out`: a step
-    of the same sizes to be written over, none of whose tensors this reads (as `held` or `state`, say)."""
+    of the same sizes to be written over; what overlaps anything else that the call reads or writes is
+    refused, by a ValueError for `held` and `state` and else a RopeError."""
     ring, before, dev = _pool(pool)
     T, page_size, B = int(T), int(page_size), new_lens.numel()
     _index(new_lens, "new_lens", dev)
@@ -677,7 +676,9 @@ def page_step(pool: PagePool, block_table, held, new_lens, T: int, page_size: in
             3 + 3 * B + T, dtype=torch.int32, device=dev).split_with_sizes((2, B + 1, B, B, T))
         out = PageStep(cu, kv_lens, after, positions, state, torch.empty(T, dtype=torch.int64, device=dev))
     else:
-        _step_buffers(out, B, T, dev, ring, before, held, new_lens, block_table)
+        _step_buffers(out, B, T, dev)
+        if (B > 0 and out.held.data_ptr() == held.data_ptr()) or out.state.data_ptr() == before.data_ptr():
+            raise ValueError("out: the step whose held or state is read cannot be written over")
     _call(dev, _lib.kv_page_step, "kv_page_step", new_lens.data_ptr(), held.data_ptr(), B, T, page_size,
           block_table.data_ptr(), per, table_stride, ring.data_ptr(), ring.numel(), before.data_ptr(),
           out.cu_seqlens.data_ptr(), out.kv_lens.data_ptr(), out.held.data_ptr(), out.positions.data_ptr(),

@@ -237,6 +237,27 @@ bool valid_pool(int32_t num_seqs, int32_t page_size, int32_t max_pages, int64_t 
          table_stride >= 0 && table_stride <= (int64_t)1 << 40 && num_pages >= 1 && num_pages <= kMost;
 }
 
+// Whether an output of a step overlaps an input or another output; the workgroups have no order in which that
+// could be right.
+struct Span {
+  const void* begin;
+  int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = (uintptr_t)a.begin, y = (uintptr_t)b.begin;
+  return a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+}
+template <size_t N, size_t M>
+bool outputs_apart(const Span (&out)[N], const Span (&in)[M]) {
+  for (size_t i = 0; i < N; ++i) {
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return false;
+    for (size_t j = 0; j < M; ++j)
+      if (overlap(out[i], in[j])) return false;
+  }
+  return true;
+}
+
 }  // namespace
 }  // namespace attn
 
@@ -256,7 +277,11 @@ int32_t kv_page_step(const int32_t* new_lens, const int32_t* held, int32_t num_s
   if (num_seqs > 0 && max_pages > 0 && block_table == nullptr) return ROPE_EINVAL;
   if (T > 0 && (positions == nullptr || slots == nullptr)) return ROPE_EINVAL;
   if (ring == nullptr || state == nullptr || cu_seqlens == nullptr || state_out == nullptr) return ROPE_EINVAL;
-  if (state == state_out || (num_seqs > 0 && held == held_out)) return ROPE_EINVAL;
+  const int64_t n = num_seqs, rows = n > 0 && max_pages > 0 ? (n - 1) * table_stride + max_pages : 0;
+  if (!outputs_apart<7, 4>({{cu_seqlens, 4 * (n + 1)}, {kv_lens, 4 * n}, {held_out, 4 * n}, {positions, 4 * T},
+                            {slots, 8 * T}, {state_out, 8}, {block_table, 4 * rows}},
+                           {{new_lens, 4 * n}, {held, 4 * n}, {ring, 4 * (int64_t)num_pages}, {state, 8}}))
+    return ROPE_EINVAL;
   StepParams p;
   p.new_lens = new_lens;
   p.held = held;

@@ -1,6 +1,6 @@
-"""What page_step accepts to be written over, without a GPU: the launch is replaced by a record of it, so
-that a step whose buffers the kernel would run past, or that it reads while it writes them, is seen to be
-refused before any launch."""
+"""What page_step accepts to be written over, without a GPU: calls go as far as the launch, which fails for
+want of a device and is recorded, so that a step whose buffers the kernel would run past, or that it reads while
+it writes them, is seen to be refused before any launch."""
 import pytest
 import torch
 
@@ -8,6 +8,7 @@ import packed_varlen_rotary_rope_amd as rope
 from packed_varlen_rotary_rope_amd import attention as A
 
 B, T, PAGES = 3, 10, 8
+EINVAL = -1
 
 
 def i32(*shape):
@@ -20,9 +21,18 @@ def kind(t):
 
 @pytest.fixture
 def launches(monkeypatch):
+    if torch.cuda.is_available():
+        pytest.skip("the launches of CPU tensors here are to fail")
     seen = []
+
+    def call(device, fn, what, *args):
+        status = fn(*args, None)
+        if status == EINVAL:
+            raise rope.RopeError(status, what)
+        seen.append(what)
+
     monkeypatch.setattr(A, "_gpu", lambda device: None)
-    monkeypatch.setattr(A, "_call", lambda device, fn, what, *args: seen.append(what))
+    monkeypatch.setattr(A, "_call", call)
     return seen
 
 
@@ -82,18 +92,30 @@ def test_buffers_that_are_read_or_written_twice_are_refused(launches):
             ({"block_table": own.slots.view(torch.int32)[:4 * B].view(B, 4)}, own),
             ({}, buffers(kv_lens=line[:B], held=line[:B])), ({}, buffers(kv_lens=line[:B], positions=line[B - 1:B - 1 + T])),
             ({}, buffers(state=a["held"][:2])), ({}, buffers(held=a["block_table"].view(-1)[9:9 + B]))]:
-        with pytest.raises(ValueError):
+        with pytest.raises((ValueError, rope.RopeError)):
             rope.page_step(**{**a, **kw}, out=out)
-    assert not launches
+    table = i32(2 * B * 4)
+    with pytest.raises(rope.RopeError):  # a table that reaches into the lengths, without `out`
+        rope.page_step(**{**a, "block_table": table.view(2 * B, 4)[::2], "held": table[17:17 + B]})
+    rope.page_step(**{**a, "block_table": table.view(2 * B, 4)[::2], "held": table[20:20 + B]})
+    assert launches == ["kv_page_step"]
 
 
 @pytest.mark.parametrize("ring", [torch.arange(PAGES), i32(2 * PAGES)[::2], i32(0), torch.zeros(4, dtype=torch.int32, device="meta")],
                          ids=kind)
 def test_a_pool_that_was_changed_is_checked_again(launches, ring):
-    a = args()
-    a["pool"].ring = ring
+    pool = args()["pool"]
     with pytest.raises((TypeError, ValueError)):
-        rope.page_step(**a)
+        pool.ring = ring
     with pytest.raises((TypeError, ValueError)):
-        rope.page_release_(a["pool"], a["block_table"], a["held"], torch.zeros(B, dtype=torch.bool), 16)
-    assert not launches
+        rope.PagePool(ring, pool.state)
+    assert pool.ring.tolist() == list(range(PAGES))
+
+
+@pytest.mark.parametrize("state", [i32(1), i32(3), i32(4)[::2], torch.zeros(2), torch.zeros(2, dtype=torch.int32, device="meta")],
+                         ids=kind)
+def test_a_state_that_is_taken_over_is_checked(launches, state):
+    pool = args()["pool"]
+    with pytest.raises((TypeError, ValueError)):
+        pool.state = state
+    assert pool.state.tolist() == [0, PAGES]
