@@ -67,12 +67,13 @@ namespace {
 // dout_i . out_i, whose error matters where a row's weight lies on few keys: there dP_ij - D_i is small
 // beside either. Capped and biased scores are such rows at any length: gradients of eight samples of 256 to
 // 2048 tokens, scores of size 4 under a cap of 50, are off by 0.0024 of their norm with it, of which the
-// rounding of dS and of the result is all, and by 0.0032 without (bf16, 32 + 8 heads of 128).
+// rounding of dS and of the result is all, and by 0.0032 without (bf16, 32 + 8 heads of 128). It is paid for by a
+// walk of two products, a tanh and an exponential a score, about a third of the pass.
 constexpr int32_t kExactKeys = ATTN_MODS ? INT32_MAX : 256;
 // dQ of changed scores takes dS in two parts, rounded and what the rounding left, up to 64 columns, where the
 // vector unit is what is waited for and a product more costs 1 to 3 % of the pass (28 samples of 799 tokens,
-// 32 + 8 heads of 64, cap and bias: 425 and 427 us): dQ is then off by the rounding of the result alone. At 128
-// columns it would be 10 % (415 and 457 us for eight samples of 256 to 2048 tokens).
+// 32 + 8 heads of 64, cap and bias, 419 to 429 us with it): dQ is then off by the rounding of the result alone. At
+// 128 columns it would be 10 % (eight samples of 256 to 2048 tokens, cap, 378 to 397 us without it).
 constexpr bool two_parts(int db) { return ATTN_MODS != 0 && db <= 2; }
 constexpr bool kHasCap = ATTN_MODS & kCap, kHasBias = ATTN_MODS & kBias;
 // Where a batch is too small to give every workgroup of the dK/dV pass so many units, cuts that would leave

@@ -8,11 +8,16 @@
 //
 // What it costs: the vector unit, which the softmax already keeps as busy as the products do the matrix
 // unit. A cap takes 8 operations of the full rate a score, beside the softmax's 8 or 9 (the exponential
-// counts 4), a bias 4. Eight samples of 256 to 2048 tokens, 32 + 8 heads of 128, bf16: forward 146 us
-// without, 167 with a bias, 186 with a cap; dK and dV 303, 343, 400 (one wave on a SIMD there, so
-// nothing hides it). A bias keeps the exact distance of each pair: as one number a row and a
-// multiple of the slope for each register it would take one operation or two (163 us), but near keys
-// would then be differences of large products.
+// counts 4), a bias 4, and a cap whose scores come near it twice that (bend_scores). Eight samples of 256 to
+// 2048 tokens, 32 + 8 heads of 128, bf16, kernel times in us (medians on three cards):
+//                            forward      dQ           dK and dV
+//   nothing                  147 .. 151   214 .. 225   312 .. 327
+//   a bias                   163 .. 167   347 .. 351   331 .. 335
+//   cap 50, scores of 4      177 .. 186   378 .. 397   381 .. 401
+//   cap 50, scores of 10     220 .. 230   448 .. 467   435 .. 447   (of 16: the same)
+// dQ walks the keys twice in either form (attn_bwd.hip). A bias keeps the exact distance of each pair: as one
+// number a row and a multiple of the slope for each register it would take one operation or two (3 % of the
+// forward), but near keys would then be differences of large products.
 #pragma once
 
 #include "attn_common.h"
@@ -51,9 +56,11 @@ __device__ inline float tanh_near(float y) {
   return y * x;
 }
 
-// tanh(s by) of 16 scores, within 2^-22 of it relatively: a polynomial up to kTanhNear, which is all
-// that most blocks need, else 1 - 2 / (1 + exp(2 y)) too (7 operations of the full rate, against 4 and
-// two of a quarter of it, and exact near 0). A score's result depends on no other's. The bound is what all
+// tanh(s by) of 16 scores, within 2^-22 of it relatively: a polynomial up to kTanhNear (7 operations of
+// the full rate, and exact near 0), and where one of the wave's 1024 scores is beyond it, 1 - 2 / (1 + exp(2 y))
+// for all of them too (4 more, two of a quarter of the rate, and the choice). A score's result depends on no other's,
+// but the time does: blocks with no score past 0.6 of the cap are all of those of normal scores of size 4 under
+// a cap of 50, at size 8 some are not, and at size 10 nearly none are left. The bound is what all
 // fp32 arguments give here (1.85e-7 at most, at 0.502, and 1.5e-7 beyond 0.75); from exp2 and the reciprocal
 // within a step each, which is what their specification says, it would be 2.9e-7 (tanh_constants.h).
 __device__ inline void bend_scores(f32x16& s, float by) {

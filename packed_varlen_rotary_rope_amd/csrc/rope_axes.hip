@@ -12,7 +12,8 @@
 // 128, 10814 tokens: 52 us through the caches, 43 with such stores, 40.5 with loads too, which is 5.5
 // TB/s (a large copy moves 5.1); 16 + 16 heads of 96: 36.5, 26.6, and 30.8, for lines are fetched
 // twice. 16004 tokens of 32 + 8 heads into the cache: 87, 74, 70 us. Workgroups of 64, 256 or 512 threads
-// were up to 25 % slower on some of twelve such shapes and nowhere faster than 10 %.
+// were up to 25 % slower on some of twelve such shapes and nowhere faster than 10 %. Where there are more
+// tokens than a dispatch has workgroups, each takes as many as that needs, whatever its work.
 #include "attn_common.h"
 #include "cr_sincos.h"
 #include "storage.h"
